@@ -296,18 +296,18 @@ def _plain_plan(s):
     held, need = (s["held"] + P - 1) // P, (s["kv"] + P - 1) // P
     grow, back = (need - held).clamp(min=0), (held - need).clamp(min=0)
     A, R = grow.sum(), back.sum()
+    enough = A <= F + R                       # else no page moves and no token has a slot
     col = torch.arange(s["ld"], device=DEV)
     # released pages go on the stack in the order of (sequence, column)
     rank = (torch.cumsum(back, 0) - back)[:, None] + col - need[:, None]
-    given = (col >= need[:, None]) & (col < held[:, None])
+    given = (col >= need[:, None]) & (col < held[:, None]) & enough
     stack = torch.cat([free, free.new_zeros(1)])
     stack.scatter_(0, torch.where(given, F + rank, s["n_pages"]).reshape(-1), table.reshape(-1))
     # then every row that grows takes its pages from the top
     rank = (torch.cumsum(grow, 0) - grow)[:, None] + col - held[:, None]
-    taken = (col >= held[:, None]) & (col < need[:, None])
-    at = F + R - 1 - rank
-    table = torch.where(taken, torch.where(at >= 0, stack[at.clamp(0, s["n_pages"])], -1), table)
-    n_free = (F + R - A).clamp(min=0)
+    taken = (col >= held[:, None]) & (col < need[:, None]) & enough
+    table = torch.where(taken, stack[(F + R - 1 - rank).clamp(0, s["n_pages"])], table)
+    n_free = torch.where(enough, F + R - A, F)
     k = torch.arange(s["n_pages"], device=DEV)
     free = torch.where((k >= F) & (k < n_free), stack[:-1], free)
     row_off, q_off = _prefix(s["kv"]), _prefix(s["q"])
@@ -315,7 +315,7 @@ def _plain_plan(s):
     seq = torch.searchsorted(q_off[1:], i, right=True).clamp(max=s["n_seq"] - 1)
     pos = (s["kv"] - s["q"])[seq] + i - q_off[seq]
     page = table[seq, (pos // P).clamp(0, s["ld"] - 1)].long()
-    slots = torch.where((i < q_off[-1]) & (page >= 0), page * P + pos % P, -1)
+    slots = torch.where((i < q_off[-1]) & (page >= 0) & enough, page * P + pos % P, -1)
     return {"table": table, "free": free, "n_free": n_free.int(), "row_off": row_off, "q_off": q_off,
             "slots": slots}
 
