@@ -16,6 +16,9 @@ Tensor layouts (row-major, contiguous), with ``W = kv_lora + rope_dim``:
 * ``scores`` [n_q, ld] float32, ``idx`` [n_q, top_k + kpool - 1] int32,
   ``n_sel`` [n_q] int32, ``out`` [n_q, heads, kv_lora] float32,
   ``lse`` [n_q, heads] float32
+* the paged 8-bit cache: ``codes`` [n_pages, page_rows, W] of one-byte elements,
+  ``scales`` [n_pages, 2] uint8 ([n_pages, 1] without rope), ``block_table``
+  [n_seq, table_ld] int32, ``slots`` [tokens] int64
 """
 from __future__ import annotations
 
@@ -36,6 +39,8 @@ __all__ = [
     "OP_POOL_COMPRESS", "dsa_pool_compress", "dsa_index_prepare", "dsa_workspace_set_wait_budget",
     "FLAG_TWO_LAUNCH", "FLAG_DESC_ORDER", "FLAG_DENSE", "OP_PROJECT", "dsa_absorb_q",
     "dsa_up_project", "OP_DECODE_STEP_HOST",
+    "Pages", "make_pages", "CACHE_E4M3", "CACHE_S8", "OP_PAGE_PLAN", "OP_CACHE_APPEND",
+    "OP_PAGED_MLA", "dsa_page_plan", "dsa_cache_append", "dsa_paged_mla_attn",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdsa.so")
@@ -45,7 +50,10 @@ OP_INDEX_SCORES, OP_TOPK_SELECT, OP_SPARSE_MLA, OP_DECODE_STEP, OP_INDEX_SELECT 
 OP_POOL_COMPRESS = 5
 OP_PROJECT = 6
 OP_DECODE_STEP_HOST = 7
+OP_PAGE_PLAN, OP_CACHE_APPEND, OP_PAGED_MLA = 16, 17, 18
+CACHE_E4M3, CACHE_S8 = 0, 1
 FLAG_TWO_LAUNCH, FLAG_DESC_ORDER, FLAG_DENSE = 0x1, 0x2, 0x4
+_TORCH_DTYPE = {DSA_F32: torch.float32, DSA_BF16: torch.bfloat16}
 STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED",
           3: "DSA_ERR_WORKSPACE", 4: "DSA_ERR_CUDA", 5: "DSA_ERR_DEVICE", 6: "DSA_ERR_TIMEOUT"}
 
@@ -76,6 +84,11 @@ class PlanInfo(ctypes.Structure):
                 ("attn_rows_per_split", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("page_rows", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("table_ld", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
 
@@ -93,6 +106,7 @@ def load() -> ctypes.CDLL:
         P, S, i32, i64, sz = (ctypes.c_void_p, ctypes.POINTER(Shape), ctypes.c_int32,
                               ctypes.c_int64, ctypes.c_size_t)
         B = ctypes.POINTER(Batch)
+        G = ctypes.POINTER(Pages)
         sigs = {
             "dsa_version": ([], ctypes.c_int),
             "dsa_status_string": ([i32], ctypes.c_char_p),
@@ -113,6 +127,9 @@ def load() -> ctypes.CDLL:
             "dsa_workspace_set_wait_budget": ([P, sz, ctypes.c_uint64, P], ctypes.c_int),
             "dsa_absorb_q": ([S, i32, i32, P, P, P, P, sz, P], ctypes.c_int),
             "dsa_up_project": ([S, i32, i32, P, P, P, P, sz, P], ctypes.c_int),
+            "dsa_page_plan": ([G, i32, i64, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+            "dsa_cache_append": ([S, B, G, P, P, P, P, P, sz, P], ctypes.c_int),
+            "dsa_paged_mla_attn": ([S, B, G, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(lib, name)
@@ -278,6 +295,81 @@ def dsa_index_prepare(shape, x, pos, rope_dims, rope_base, out, stream=None) -> 
     """out = H . rope(x, pos), rounded to the shape's dtype (see dsa.h)."""
     _call("dsa_index_prepare", ctypes.byref(shape), int(x.shape[0]), _ptr(x), _ptr(pos),
           int(rope_dims), float(rope_base), _ptr(out), _stream(stream))
+
+
+def make_pages(page_rows: int, n_pages: int, table_ld: int, fmt=CACHE_E4M3) -> Pages:
+    """Geometry of a paged 8-bit cache; ``fmt`` CACHE_E4M3 / CACHE_S8 or "e4m3" / "s8"."""
+    fmt = {"e4m3": CACHE_E4M3, "s8": CACHE_S8}.get(fmt, fmt)
+    return Pages(int(page_rows), int(fmt), int(n_pages), int(table_ld))
+
+
+def _typed(t: Optional[torch.Tensor], dtype, what: str):
+    """Pointer of a tensor whose element type the call fixes."""
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{what} is {dtype}, not {t.dtype}")
+    return _ptr(t)
+
+
+def _codes(pages: Pages, t: torch.Tensor, width: int):
+    if t.element_size() != 1 or t.numel() != pages.n_pages * pages.page_rows * width:
+        raise ValueError("codes holds n_pages x page_rows x width one-byte elements")
+    return _ptr(t)
+
+
+def _scales(shape: Shape, pages: Pages, t: torch.Tensor):
+    if t.element_size() != 1 or t.numel() != pages.n_pages * (2 if shape.rope_dim else 1):
+        raise ValueError("scales holds one byte per page and part of a row")
+    return _ptr(t)
+
+
+def _at_least(t: Optional[torch.Tensor], n: int, what: str) -> None:
+    if t is None or t.numel() < n:
+        raise ValueError(f"{what} holds at least {n} elements")
+
+
+def dsa_page_plan(pages, held_len, kv_len, q_len, free_pages, n_free, block_table, row_off, q_off,
+                  slots, ws, n_free_out=None, stream=None) -> None:
+    """Block tables, slot map (``slots``, one entry per new token) and batch
+    offsets from request lengths (see dsa.h); ``n_free_out=None`` updates
+    ``n_free`` in place."""
+    n_seq, i64, i32 = held_len.numel(), torch.int64, torch.int32
+    n_free_out = n_free if n_free_out is None else n_free_out
+    _at_least(kv_len, n_seq, "kv_len")
+    _at_least(q_len, n_seq, "q_len")
+    _at_least(row_off, n_seq + 1, "row_off")
+    _at_least(q_off, n_seq + 1, "q_off")
+    _at_least(free_pages, pages.n_pages, "free_pages")
+    _at_least(block_table, n_seq * pages.table_ld, "block_table")
+    _call("dsa_page_plan", ctypes.byref(pages), n_seq, slots.numel(),
+          _typed(held_len, i64, "held_len"), _typed(kv_len, i64, "kv_len"),
+          _typed(q_len, i64, "q_len"), _typed(free_pages, i32, "free_pages"),
+          _typed(n_free, i32, "n_free"), _typed(n_free_out, i32, "n_free_out"),
+          _typed(block_table, i32, "block_table"), _typed(row_off, i64, "row_off"),
+          _typed(q_off, i64, "q_off"), _typed(slots, i64, "slots"), _ptr(ws), ws.numel(),
+          _stream(stream))
+
+
+def dsa_cache_append(shape, batch, pages, rows, slots, codes, scales, ws, stream=None) -> None:
+    """The batch's new rows [n_q, W] rounded into their slots (see dsa.h)."""
+    width = shape.kv_lora + shape.rope_dim
+    _at_least(rows, batch.n_q * width, "rows")
+    _at_least(slots, batch.n_q, "slots")
+    _call("dsa_cache_append", ctypes.byref(shape), ctypes.byref(batch), ctypes.byref(pages),
+          _typed(rows, _TORCH_DTYPE[shape.dtype], "rows"), _typed(slots, torch.int64, "slots"),
+          _codes(pages, codes, width), _scales(shape, pages, scales), _ptr(ws), ws.numel(),
+          _stream(stream))
+
+
+def dsa_paged_mla_attn(shape, batch, pages, q_abs, codes, scales, block_table, idx, n_sel, out,
+                       lse, ws, stream=None) -> None:
+    """Step 3 over the paged 8-bit cache (see dsa.h)."""
+    _at_least(block_table, batch.n_seq * pages.table_ld, "block_table")
+    _call("dsa_paged_mla_attn", ctypes.byref(shape), ctypes.byref(batch), ctypes.byref(pages),
+          _typed(q_abs, _TORCH_DTYPE[shape.dtype], "q_abs"),
+          _codes(pages, codes, shape.kv_lora + shape.rope_dim), _scales(shape, pages, scales),
+          _typed(block_table, torch.int32, "block_table"), _typed(idx, torch.int32, "idx"),
+          _typed(n_sel, torch.int32, "n_sel"), _typed(out, torch.float32, "out"),
+          _typed(lse, torch.float32, "lse"), _ptr(ws), ws.numel(), _stream(stream))
 
 
 def dsa_check_device_error(ws: Optional[torch.Tensor], stream=None) -> int:

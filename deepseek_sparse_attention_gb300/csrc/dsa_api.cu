@@ -167,6 +167,9 @@ size_t op_bytes(const Shape& sh, const BatchDev& b, int32_t op) {
         case DSA_OP_INDEX_SELECT: return step_layout(sh, b).attn;
         case DSA_OP_POOL_COMPRESS: return kWsHeaderBytes;
         case DSA_OP_PROJECT: return kWsHeaderBytes;
+        case DSA_OP_PAGE_PLAN: return align_up(scratch_off() + page_plan_scratch_bytes(b.n_seq));
+        case DSA_OP_CACHE_APPEND: return kWsHeaderBytes;
+        case DSA_OP_PAGED_MLA: return align_up(scratch_off() + paged_mla_scratch_bytes(sh, b));
         default: return 0;
     }
 }
@@ -214,8 +217,34 @@ cudaError_t enqueue_index_select(const Shape& sh, const BatchDev& b, const StepL
     return launch_select_order_desc(sh, b, scores, ld, idx, n_sel, err, st);
 }
 
+// The operations of the paged 8-bit cache, numbered apart from the others.
+bool paged_op(int32_t op) { return op >= DSA_OP_PAGE_PLAN && op <= DSA_OP_PAGED_MLA; }
+bool known_op(int32_t op) {
+    return (op >= DSA_OP_INDEX_SCORES && op <= DSA_OP_DECODE_STEP_HOST) || paged_op(op);
+}
+// Operations whose queries are new tokens, of which a batch may have millions.
+bool any_n_q(int32_t op) {
+    return op == DSA_OP_POOL_COMPRESS || op == DSA_OP_PAGE_PLAN || op == DSA_OP_CACHE_APPEND;
+}
+
+dsa_status check_pages(const dsa_pages* p, PagesDev* out) {
+    if (p == nullptr || p->n_pages < 1 || p->table_ld < 1) return DSA_ERR_INVALID_ARG;
+    if (p->format != DSA_CACHE_E4M3 && p->format != DSA_CACHE_S8) return DSA_ERR_INVALID_ARG;
+    if (p->page_rows < 1) return DSA_ERR_INVALID_ARG;
+    int32_t shift = 4;
+    while (shift < 7 && (1 << shift) != p->page_rows) ++shift;
+    if ((1 << shift) != p->page_rows || p->n_pages >= ((int64_t)1 << 31) ||
+        p->table_ld >= ((int64_t)1 << 27))
+        return DSA_ERR_UNSUPPORTED;
+    *out = PagesDev{p->page_rows, shift, p->format, p->n_pages, p->table_ld};
+    return DSA_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // Kernels one call of `op` enqueues for this shape and batch bound.
 int32_t plan_launches(const Shape& sh, const BatchDev& bh, int32_t op, int32_t splits) {
+    if (op == DSA_OP_PAGE_PLAN) return page_plan_launches();
     if (bh.n_q <= 0) return 0;
     // attention, then the split merge -- except for two tensor-core splits,
     // which merge inside the attention launch (a CTA pair)
@@ -232,6 +261,8 @@ int32_t plan_launches(const Shape& sh, const BatchDev& bh, int32_t op, int32_t s
         case DSA_OP_INDEX_SELECT: return sel;
         case DSA_OP_POOL_COMPRESS: return sh.kpool > 1 ? 1 : 0;
         case DSA_OP_PROJECT: return 1;
+        case DSA_OP_CACHE_APPEND: return 1;
+        case DSA_OP_PAGED_MLA: return paged_mla_launches(sh, bh);
         case DSA_OP_DECODE_STEP_HOST:                      // the input copy, then the step
             return 1 + ((bh.flags & DSA_FLAG_DENSE) ? attn : sel + attn);
         default: return (bh.flags & DSA_FLAG_DENSE) ? attn : sel + attn;
@@ -304,10 +335,9 @@ dsa_status dsa_workspace_size(const dsa_shape* shape, const dsa_batch* batch, in
     if (batch == nullptr || batch->n_q < 0 || batch->max_kv_len < 0 ||
         (batch->flags & ~kKnownFlags) != 0)
         return DSA_ERR_INVALID_ARG;
-    if (batch->max_kv_len >= ((int64_t)1 << 31) ||
-        (batch->n_q > 65535 && op != DSA_OP_POOL_COMPRESS))
+    if (batch->max_kv_len >= ((int64_t)1 << 31) || (batch->n_q > 65535 && !any_n_q(op)))
         return DSA_ERR_UNSUPPORTED;
-    if (op < DSA_OP_INDEX_SCORES || op > DSA_OP_DECODE_STEP_HOST) return DSA_ERR_INVALID_ARG;
+    if (!known_op(op) || (paged_op(op) && batch->n_seq < 0)) return DSA_ERR_INVALID_ARG;
     *out_bytes = op_bytes(sh, host_batch(batch, sh), op);
     return DSA_OK;
 }
@@ -320,10 +350,11 @@ dsa_status dsa_plan(const dsa_shape* shape, const dsa_batch* batch, int32_t op,
     if (s != DSA_OK) return s;
     if (batch->n_q < 0 || batch->max_kv_len < 0 || (batch->flags & ~kKnownFlags) != 0)
         return DSA_ERR_INVALID_ARG;
-    if (op < DSA_OP_INDEX_SCORES || op > DSA_OP_DECODE_STEP_HOST) return DSA_ERR_INVALID_ARG;
+    if (!known_op(op)) return DSA_ERR_INVALID_ARG;
     const BatchDev bh = host_batch(batch, sh);
     int32_t rps = 0, splits = 0;
-    plan_attention_splits(sh, bh, &rps, &splits);
+    if (op == DSA_OP_PAGED_MLA) plan_paged_splits(sh, bh, &rps, &splits);
+    else plan_attention_splits(sh, bh, &rps, &splits);
     *info = dsa_plan_info{plan_launches(sh, bh, op, splits), splits, rps, 0};
     return DSA_OK;
 }
@@ -468,6 +499,89 @@ dsa_status dsa_up_project(const dsa_shape* shape, int32_t n_q, int32_t v_dim, co
     return cuda_status(launch_up_project(sh, n_q, v_dim, o, w_uv, out, static_cast<int32_t*>(ws),
                                          static_cast<cudaStream_t>(stream)),
                        "up_project");
+}
+
+dsa_status dsa_page_plan(const dsa_pages* pages, int32_t n_seq, int64_t max_new,
+                         const int64_t* held_len, const int64_t* kv_len, const int64_t* q_len,
+                         int32_t* free_pages, const int32_t* n_free_in, int32_t* n_free_out,
+                         int32_t* block_table, int64_t* row_off, int64_t* q_off, int64_t* slots,
+                         void* ws, size_t ws_bytes, void* stream) {
+    PagesDev pg;
+    dsa_status s = check_pages(pages, &pg);
+    if (s != DSA_OK) return s;
+    if (n_seq < 0 || max_new < 0) return DSA_ERR_INVALID_ARG;
+    if (n_seq > (1 << 20) || max_new >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    if (row_off == nullptr || q_off == nullptr || free_pages == nullptr || n_free_in == nullptr ||
+        n_free_out == nullptr || (max_new > 0 && slots == nullptr) ||
+        (n_seq > 0 && (held_len == nullptr || kv_len == nullptr || q_len == nullptr ||
+                       block_table == nullptr)))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(held_len, 8) || !aligned(kv_len, 8) || !aligned(q_len, 8) ||
+        !aligned(row_off, 8) || !aligned(q_off, 8) || !aligned(slots, 8) ||
+        !aligned(free_pages, 4) || !aligned(n_free_in, 4) || !aligned(n_free_out, 4) ||
+        !aligned(block_table, 4))
+        return DSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, align_up(scratch_off() + page_plan_scratch_bytes(n_seq)))) != DSA_OK)
+        return s;
+    const PagePlanArgs a{pg,         n_seq,       max_new,   held_len, kv_len, q_len, free_pages,
+                         n_free_in,  n_free_out,  block_table, row_off, q_off, slots};
+    return cuda_status(launch_page_plan(a, bytes(ws) + scratch_off(), static_cast<int32_t*>(ws),
+                                        static_cast<cudaStream_t>(stream)),
+                       "page_plan");
+}
+
+dsa_status dsa_cache_append(const dsa_shape* shape, const dsa_batch* batch, const dsa_pages* pages,
+                            const void* rows, const int64_t* slots, void* codes, void* scales,
+                            void* ws, size_t ws_bytes, void* stream) {
+    Shape sh;
+    BatchDev b;
+    PagesDev pg;
+    dsa_status s = check_shape(shape, &sh);
+    if (s != DSA_OK) return s;
+    if ((s = check_batch(batch, sh, &b, 0x7fffffff)) != DSA_OK) return s;
+    if ((s = check_pages(pages, &pg)) != DSA_OK) return s;
+    if (b.n_seq > 65535) return DSA_ERR_UNSUPPORTED;
+    if (b.n_q > 0 && (rows == nullptr || slots == nullptr || codes == nullptr || scales == nullptr))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned(slots, 8) || !aligned16(codes)) return DSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, op_bytes(sh, b, DSA_OP_CACHE_APPEND))) != DSA_OK) return s;
+    if (b.n_q == 0) return DSA_OK;
+    return cuda_status(launch_cache_append(sh, b, pg, rows, slots, static_cast<uint8_t*>(codes),
+                                           static_cast<uint8_t*>(scales), static_cast<int32_t*>(ws),
+                                           static_cast<cudaStream_t>(stream)),
+                       "cache_append");
+}
+
+dsa_status dsa_paged_mla_attn(const dsa_shape* shape, const dsa_batch* batch,
+                              const dsa_pages* pages, const void* q_abs, const void* codes,
+                              const void* scales, const int32_t* block_table, const int32_t* idx,
+                              const int32_t* n_sel, float* out, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+    Shape sh;
+    BatchDev b;
+    PagedCache pc;
+    dsa_status s = check_shape(shape, &sh);
+    if (s != DSA_OK) return s;
+    if ((s = check_batch(batch, sh, &b)) != DSA_OK) return s;
+    if ((s = check_pages(pages, &pc.pg)) != DSA_OK) return s;
+    const bool dense = (b.flags & DSA_FLAG_DENSE) != 0;
+    if (b.n_q > 0 && (q_abs == nullptr || codes == nullptr || scales == nullptr ||
+                      block_table == nullptr || out == nullptr ||
+                      (!dense && (idx == nullptr || n_sel == nullptr))))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q_abs) || !aligned16(codes) || !aligned16(out) || !aligned16(idx) ||
+        !aligned(lse, 4) || !aligned(n_sel, 4) || !aligned(block_table, 4))
+        return DSA_ERR_INVALID_ARG;
+    const size_t need = op_bytes(sh, b, DSA_OP_PAGED_MLA);
+    if ((s = check_ws(ws, ws_bytes, need)) != DSA_OK) return s;
+    pc.codes = static_cast<const uint8_t*>(codes);
+    pc.scales = static_cast<const uint8_t*>(scales);
+    pc.block_table = block_table;
+    return cuda_status(launch_paged_mla(sh, b, pc, q_abs, dense ? nullptr : idx,
+                                        dense ? nullptr : n_sel, out, lse,
+                                        bytes(ws) + scratch_off(), need - scratch_off(),
+                                        static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)),
+                       "paged_mla_attn");
 }
 
 dsa_status dsa_decode_step(const dsa_shape* shape, const dsa_batch* batch, const void* q_idx,

@@ -32,6 +32,8 @@ enum DeviceError : int32_t {
     kDevBadIndex = 1,      // a selected index outside [0, L)
     kDevBadBatch = 2,      // offsets inconsistent with the host bounds
     kDevTimeout = 3,       // a bounded wait gave up
+    kDevNoPages = 4,       // a page plan that needs more pages than are free
+    kDevBadValue = 5,      // a value the 8-bit cache cannot hold (infinity, NaN)
 };
 
 __device__ __forceinline__ void record_error(int32_t* err, int32_t code, int32_t detail,

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "dsa_common.cuh"
+#include "paged_cache.cuh"
 
 namespace dsa {
 
@@ -199,5 +200,43 @@ cudaError_t launch_sparse_mla(const Shape& sh, const BatchDev& b, const void* q_
                               const void* cache, const int32_t* idx, const int32_t* n_sel,
                               float* out, float* lse, void* scratch, size_t scratch_bytes,
                               int32_t* err, bool q_early, cudaStream_t st);
+
+// The paged 8-bit cache.  Page plan (page_plan.cu): offsets, block table, free
+// pages and slot map from request lengths; `scratch` holds
+// page_plan_scratch_bytes() bytes.
+struct PagePlanArgs {
+    PagesDev pg;
+    int64_t n_seq, max_new;
+    const int64_t *held_len, *kv_len, *q_len;
+    int32_t* free_pages;
+    const int32_t* n_free_in;
+    int32_t* n_free_out;
+    int32_t* block_table;
+    int64_t *row_off, *q_off, *slots;
+};
+size_t page_plan_scratch_bytes(int64_t n_seq);
+int32_t page_plan_launches();
+cudaError_t launch_page_plan(const PagePlanArgs& a, void* scratch, int32_t* err, cudaStream_t st);
+
+// Append (cache_append.cu): the batch's new rows rounded into their slots.
+cudaError_t launch_cache_append(const Shape& sh, const BatchDev& b, const PagesDev& pg,
+                                const void* rows, const int64_t* slots, uint8_t* codes,
+                                uint8_t* scales, int32_t* err, cudaStream_t st);
+
+// Attention over the paged cache (paged_mla.cu).
+struct PagedCache {
+    PagesDev pg;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const int32_t* block_table;
+};
+void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_split,
+                       int32_t* n_split);
+size_t paged_mla_scratch_bytes(const Shape& sh, const BatchDev& b);
+int32_t paged_mla_launches(const Shape& sh, const BatchDev& b);
+cudaError_t launch_paged_mla(const Shape& sh, const BatchDev& b, const PagedCache& pc,
+                             const void* q_abs, const int32_t* idx, const int32_t* n_sel,
+                             float* out, float* lse, void* scratch, size_t scratch_bytes,
+                             int32_t* err, cudaStream_t st);
 
 }  // namespace dsa

@@ -12,7 +12,10 @@
  * and two producers of the indexer's inputs: dsa_index_prepare (rope, then the
  * Walsh-Hadamard rotation of projected indexer queries and keys, rounded to the
  * cache's dtype) and dsa_pool_compress (the k-pool keys, one per 4 tokens, from
- * the tokens' [key | gate] cells).
+ * the tokens' [key | gate] cells).  Step 3 also runs over a paged cache held in
+ * 8 bits: dsa_page_plan (block tables, slot maps and batch offsets from request
+ * lengths), dsa_cache_append (new rows rounded into their slots) and
+ * dsa_paged_mla_attn (the attention).
  *
  * Sources (page title -- section):
  *   "GLM-5.x (glm-dsa, glm5next)" (TensorSharp model notes) -- "The block"
@@ -159,6 +162,9 @@ int64_t dsa_index_row_width(const dsa_shape *shape);
 #define DSA_OP_POOL_COMPRESS 5
 #define DSA_OP_PROJECT 6
 #define DSA_OP_DECODE_STEP_HOST 7
+#define DSA_OP_PAGE_PLAN 16            /* of the batch only n_seq is read        */
+#define DSA_OP_CACHE_APPEND 17
+#define DSA_OP_PAGED_MLA 18
 dsa_status dsa_workspace_size(const dsa_shape *shape, const dsa_batch *batch, int32_t op,
                               size_t *bytes);
 
@@ -334,6 +340,107 @@ dsa_status dsa_up_project(const dsa_shape *shape, int32_t n_q, int32_t v_dim, co
 dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, const void *q_abs,
                                const void *cache, const int32_t *idx, const int32_t *n_sel,
                                float *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* The paged 8-bit cache
+ * ---------------------
+ * The latent cache as a pool of pages instead of packed sequences, its values
+ * held in 8 bits: half of a bf16 row's bytes, and sequences that grow without
+ * moving.  The pages have no counterpart: the layout is this library's (one of
+ * them names an 8-bit MLA cache, without its format).
+ *   codes  [n_pages, page_rows, W] 8-bit, W = kv_lora + rope_dim
+ *   scales [n_pages, parts] uint8: one E8M0 byte b per page and part of a row
+ *          (parts: the kv_lora latent columns, then the rope columns when
+ *          rope_dim > 0), standing for 2^(b - 127); 255 is NaN
+ *   block_table [n_seq, table_ld] int32: row r of sequence s is row
+ *          r % page_rows of page block_table[s][r / page_rows]; entries past a
+ *          sequence's rows are not read
+ * A code c of a page's part stands for c * 2^(b - 127), c an e4m3 number or a
+ * signed integer.  A block table may name a page several times (shared
+ * prefixes); a page that a call appends to belongs to one sequence. */
+typedef enum {
+    DSA_CACHE_E4M3 = 0,        /* 8-bit float, 4 exponent and 3 mantissa bits, +-448 */
+    DSA_CACHE_S8 = 1           /* 8-bit integer, -127..127                       */
+} dsa_cache_format;
+
+typedef struct {
+    int32_t page_rows;         /* rows of a page: 16, 32, 64 or 128                */
+    int32_t format;            /* a dsa_cache_format                               */
+    int64_t n_pages;           /* pages of the pool (< 2^31)                       */
+    int64_t table_ld;          /* entries of a block-table row (< 2^27)            */
+} dsa_pages;
+
+/* Block tables, slot maps and batch offsets from request lengths.
+ *   held_len [n_seq] int64: rows for which sequence s holds pages, the first
+ *            ceil(held_len / page_rows) entries of its block-table row (0: none)
+ *   kv_len   [n_seq] int64: rows the sequence has in this step, its new tokens
+ *            included (0: it is finished, or the row is idle)
+ *   q_len    [n_seq] int64: its new tokens, the last q_len <= kv_len rows
+ *   free_pages [n_pages] int32, in/out: a stack of the free pages, the entries
+ *            0 .. n_free - 1, its top at the end
+ *   n_free_in, n_free_out [1] int32: its height before and after (may be the
+ *            same word)
+ *   block_table [n_seq, table_ld] int32, in/out
+ *   row_off, q_off [n_seq + 1] int64 out: the batch's offsets, the exclusive
+ *            prefix sums of kv_len and q_len
+ *   slots    [max_new] int64 out: page * page_rows + row of each new token, in
+ *            the batch's order; -1 past the last one
+ * Rows with more pages than ceil(kv_len / page_rows) give the rest back: pushed
+ * in the order of (row, entry); then rows with fewer take pages from the top,
+ * in the same order.  Entries given back, and free_pages entries from the new
+ * height on, are left as they were.  If the free pages do not suffice the error
+ * word is set (code 4), no page moves, n_free_out = n_free_in and every slot is
+ * -1; row_off and q_off are written all the same.  A row with lengths out of
+ * range (negative, q_len > kv_len, more than table_ld pages) sets the error word
+ * and counts as empty.  New tokens past max_new set it too and get no slot.
+ * Nothing depends on the order in which the GPU runs: the same arguments give
+ * the same tables.  n_seq <= 2^20, max_new < 2^31; pointers 8-byte aligned
+ * (int32 ones 4-byte).  Workspace: DSA_OP_PAGE_PLAN. */
+dsa_status dsa_page_plan(const dsa_pages *pages, int32_t n_seq, int64_t max_new,
+                         const int64_t *held_len, const int64_t *kv_len, const int64_t *q_len,
+                         int32_t *free_pages, const int32_t *n_free_in, int32_t *n_free_out,
+                         int32_t *block_table, int64_t *row_off, int64_t *q_off, int64_t *slots,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/* The batch's new rows rounded into the paged cache.
+ *   rows  [n_q, W] dtype: the new rows, in the batch's order (row_off and q_off
+ *         as dsa_page_plan writes them; key_off must be given but is not read)
+ *   slots [n_q] int64: each row's slot.  The slots of one sequence's rows within
+ *         a page follow one another; -1 at a page's first new row leaves that
+ *         page's rows out
+ *   codes, scales in/out
+ * For every page and part that gets new rows: amax = the largest finite |x| of
+ * them; e = the least integer with amax <= M 2^e (M = 448 for e4m3, 127 for s8)
+ * within [-110, 119], and where the page holds earlier rows of the sequence (its
+ * first new slot is not the page's row 0) at least the page's exponent; the
+ * scale becomes e + 127, each new code x / 2^e rounded to nearest even, and
+ * where e rose the earlier rows' codes are rounded again to it.  Rows of the
+ * page behind the new ones are left as they were.  Infinities become +-M 2^e,
+ * a NaN the e4m3 NaN or s8 0, and either sets the error word (code 5), as does a
+ * page whose exponent is above 119 already, which is left as it was.  A slot
+ * outside the pool, or slots that do not follow one another, set the error word
+ * and leave the page as it was.  rows and codes 16-byte, slots 8-byte aligned.
+ * n_seq <= 65535; n_q is not limited to 65535 here.  Workspace:
+ * DSA_OP_CACHE_APPEND (the error word). */
+dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, const dsa_pages *pages,
+                            const void *rows, const int64_t *slots, void *codes, void *scales,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/* Step 3 over the paged cache: dsa_sparse_mla_attn with the rows read through
+ * the block table and their codes widened exactly.
+ *   q_abs, idx, n_sel, out, lse, flags as for dsa_sparse_mla_attn; q_abs in the
+ *   shape's dtype; the batch's total_rows bounds row_off[n_seq], key_off must
+ *   bound each sequence's keys as for the other entry points
+ *   codes, scales, block_table as above
+ * An index outside [0, L), or one whose block-table entry is no page of the
+ * pool, sets the error word and its row is skipped.  A NaN code or scale of an
+ * attended row gives NaN outputs.  float32 accumulation and softmax.  Pointers
+ * 16-byte aligned (lse, n_sel and block_table 4-byte, scales any).  Workspace:
+ * DSA_OP_PAGED_MLA. */
+dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,
+                              const dsa_pages *pages, const void *q_abs, const void *codes,
+                              const void *scales, const int32_t *block_table, const int32_t *idx,
+                              const int32_t *n_sel, float *out, float *lse, void *ws,
+                              size_t ws_bytes, void *stream);
 
 /* The whole hot path for every query of the batch: steps 1-3 in one call.
  * Scores and selections live in the workspace unless idx_out / n_sel_out are
