@@ -223,7 +223,8 @@ cudaError_t launch_cache_append(const Shape& sh, const BatchDev& b, const PagesD
                                 const void* rows, const int64_t* slots, uint8_t* codes,
                                 uint8_t* scales, int32_t* err, cudaStream_t st);
 
-// Attention over the paged cache (paged_mla.cu).
+// Attention over the paged cache: bf16 queries on the tensor cores
+// (paged_mla_tc.cu), float32 queries on CUDA cores (paged_mla.cu).
 struct PagedCache {
     PagesDev pg;
     const uint8_t* codes;
@@ -234,6 +235,10 @@ void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_spl
                        int32_t* n_split);
 size_t paged_mla_scratch_bytes(const Shape& sh, const BatchDev& b);
 int32_t paged_mla_launches(const Shape& sh, const BatchDev& b);
+cudaError_t launch_paged_mla_tc(const Shape& sh, const BatchDev& b, const PagedCache& pc,
+                                const void* q_abs, const int32_t* idx, const int32_t* n_sel,
+                                float* out, float* lse, float* part_o, float* part_ml, int32_t rps,
+                                int32_t n_split, int32_t* err, cudaStream_t st);
 cudaError_t launch_paged_mla(const Shape& sh, const BatchDev& b, const PagedCache& pc,
                              const void* q_abs, const int32_t* idx, const int32_t* n_sel,
                              float* out, float* lse, void* scratch, size_t scratch_bytes,

@@ -26,11 +26,11 @@ constexpr int kTile = 16;                        // rows per tile
 constexpr int kLatent = kLatentCols;
 constexpr int kSsStride = kTile + 1;
 
-template <typename T, int W>
+template <int W>
 struct Smem {
-    static constexpr int kQStride = W + 16 / (int)sizeof(T);
+    static constexpr int kQStride = W + 4;
     static constexpr int kRStride = W + 4;
-    static constexpr size_t kQ = (size_t)kHeads * kQStride * sizeof(T);
+    static constexpr size_t kQ = (size_t)kHeads * kQStride * sizeof(float);
     static constexpr size_t kR = (size_t)kTile * kRStride * sizeof(float);
     static constexpr size_t kS = (size_t)kHeads * kSsStride * sizeof(float);
     static constexpr size_t kStats = 3 * kHeads * sizeof(float);
@@ -42,28 +42,20 @@ __device__ __forceinline__ void widen4(const float* p, float (&f)[4]) {
     const float4 v = *reinterpret_cast<const float4*>(p);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
 }
-__device__ __forceinline__ void widen4(const __nv_bfloat16* p, float (&f)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
-template <typename T, int FMT, int W>
+template <int FMT, int W>
 __global__ void __launch_bounds__(kThreads)
-paged_mla_simt(BatchDev b, PagedCache pc, float scale, const T* __restrict__ q_abs,
+paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__ q_abs,
                const int32_t* __restrict__ idx, const int32_t* __restrict__ n_sel,
                int64_t idx_width, int32_t rows_per_split, int32_t n_split,
                float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
                float* __restrict__ part_ml, int32_t* err) {
-    using S = Smem<T, W>;
+    using S = Smem<W>;
     constexpr int kParts = W > kLatent ? 2 : 1;
     constexpr int kRowVecs = W / 16;                   // 16-byte vectors of codes
     extern __shared__ __align__(16) unsigned char smem[];
     int64_t* row_at = reinterpret_cast<int64_t*>(smem);              // pool row, -1: none
     float2* row_scale = reinterpret_cast<float2*>(row_at + kTile);
-    T* Qs = reinterpret_cast<T*>(smem + S::kRows);
+    float* Qs = reinterpret_cast<float*>(smem + S::kRows);
     float* Rs = reinterpret_cast<float*>(smem + S::kRows + S::kQ);
     float* Ss = reinterpret_cast<float*>(smem + S::kRows + S::kQ + S::kR);
     float* m_s = reinterpret_cast<float*>(smem + S::kRows + S::kQ + S::kR + S::kS);
@@ -86,8 +78,8 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const T* __restrict__ q_a
     const int64_t j_begin = (int64_t)split * rows_per_split;
     const int64_t j_end = j_begin + rows_per_split < ns ? j_begin + rows_per_split : ns;
 
-    constexpr int kQVec = 16 / (int)sizeof(T);
-    const T* qsrc = q_abs + q * (int64_t)kHeads * W;
+    constexpr int kQVec = 4;
+    const float* qsrc = q_abs + q * (int64_t)kHeads * W;
     for (int v = tid; v < kHeads * (W / kQVec); v += kThreads) {
         const int h = v / (W / kQVec), c = (v % (W / kQVec)) * kQVec;
         *reinterpret_cast<uint4*>(Qs + h * S::kQStride + c) =
@@ -240,17 +232,17 @@ void plan_splits_simt(int32_t n_q, int64_t max_rows, int32_t* rows_per_split, in
     *n_split = (int32_t)((max_rows + rps - 1) / rps);
 }
 
-template <typename T, int FMT, int W>
+template <int FMT, int W>
 cudaError_t launch_t(const Shape& sh, const BatchDev& b, const PagedCache& pc, const void* q_abs,
                      const int32_t* idx, const int32_t* n_sel, float* out, float* lse,
                      float* part_o, float* part_ml, int32_t rps, int32_t n_split, int32_t* err,
                      cudaStream_t st) {
-    using S = Smem<T, W>;
-    auto kern = paged_mla_simt<T, FMT, W>;
+    using S = Smem<W>;
+    auto kern = paged_mla_simt<FMT, W>;
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)S::kTotal);
     if (e != cudaSuccess) return e;
     e = launch_plain(kern, dim3((unsigned)n_split, (unsigned)b.n_q), dim3(kThreads), S::kTotal, st,
-                     b, pc, sh.scale, static_cast<const T*>(q_abs), idx, n_sel,
+                     b, pc, sh.scale, static_cast<const float*>(q_abs), idx, n_sel,
                      sh.index_row_width(), rps, n_split, out, lse, part_o, part_ml, err);
     if (e != cudaSuccess || n_split == 1) return e;
     return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st);
@@ -262,7 +254,9 @@ void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_spl
                        int32_t* n_split) {
     int64_t main_rows, max_rows;
     paged_rows(sh, b, &main_rows, &max_rows);
-    plan_splits_simt(b.n_q > 0 ? b.n_q : 1, max_rows, rows_per_split, n_split);
+    const int32_t n_q = b.n_q > 0 ? b.n_q : 1;
+    if (sh.dtype == DSA_BF16) plan_attention_splits_tc(n_q, main_rows, max_rows, rows_per_split, n_split);
+    else plan_splits_simt(n_q, max_rows, rows_per_split, n_split);
 }
 
 size_t paged_mla_scratch_bytes(const Shape& sh, const BatchDev& b) {
@@ -275,7 +269,8 @@ size_t paged_mla_scratch_bytes(const Shape& sh, const BatchDev& b) {
 int32_t paged_mla_launches(const Shape& sh, const BatchDev& b) {
     int32_t rps, n_split;
     plan_paged_splits(sh, b, &rps, &n_split);
-    return n_split > 1 ? 2 : 1;
+    // two tensor-core splits merge inside their launch
+    return n_split > (sh.dtype == DSA_BF16 ? 2 : 1) ? 2 : 1;
 }
 
 cudaError_t launch_paged_mla(const Shape& sh, const BatchDev& b, const PagedCache& pc,
@@ -294,13 +289,12 @@ cudaError_t launch_paged_mla(const Shape& sh, const BatchDev& b, const PagedCach
         part_o = static_cast<float*>(scratch);
         part_ml = part_o + parts * kLatent;
     }
-    using bf16 = __nv_bfloat16;
-    const bool f32 = sh.dtype == DSA_F32, wide = sh.width() == 576;
-    auto f = pc.pg.format == DSA_CACHE_E4M3
-        ? (f32 ? (wide ? launch_t<float, DSA_CACHE_E4M3, 576> : launch_t<float, DSA_CACHE_E4M3, 512>)
-               : (wide ? launch_t<bf16, DSA_CACHE_E4M3, 576> : launch_t<bf16, DSA_CACHE_E4M3, 512>))
-        : (f32 ? (wide ? launch_t<float, DSA_CACHE_S8, 576> : launch_t<float, DSA_CACHE_S8, 512>)
-               : (wide ? launch_t<bf16, DSA_CACHE_S8, 576> : launch_t<bf16, DSA_CACHE_S8, 512>));
+    if (sh.dtype == DSA_BF16)
+        return launch_paged_mla_tc(sh, b, pc, q_abs, idx, n_sel, out, lse, part_o, part_ml, rps,
+                                   n_split, err, st);
+    const bool wide = sh.width() == 576;
+    auto f = pc.pg.format == DSA_CACHE_E4M3 ? (wide ? launch_t<DSA_CACHE_E4M3, 576> : launch_t<DSA_CACHE_E4M3, 512>)
+                                            : (wide ? launch_t<DSA_CACHE_S8, 576> : launch_t<DSA_CACHE_S8, 512>);
     return f(sh, b, pc, q_abs, idx, n_sel, out, lse, part_o, part_ml, rps, n_split, err, st);
 }
 
