@@ -543,7 +543,7 @@ dsa_status dsa_cache_append(const dsa_shape* shape, const dsa_batch* batch, cons
     if (b.n_seq > 65535) return DSA_ERR_UNSUPPORTED;
     if (b.n_q > 0 && (rows == nullptr || slots == nullptr || codes == nullptr || scales == nullptr))
         return DSA_ERR_INVALID_ARG;
-    if (!aligned16(rows) || !aligned(slots, 8) || !aligned16(codes)) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned(slots, 8) || !aligned(codes, 32)) return DSA_ERR_INVALID_ARG;
     if ((s = check_ws(ws, ws_bytes, op_bytes(sh, b, DSA_OP_CACHE_APPEND))) != DSA_OK) return s;
     if (b.n_q == 0) return DSA_OK;
     return cuda_status(launch_cache_append(sh, b, pg, rows, slots, static_cast<uint8_t*>(codes),
@@ -569,7 +569,7 @@ dsa_status dsa_paged_mla_attn(const dsa_shape* shape, const dsa_batch* batch,
                       block_table == nullptr || out == nullptr ||
                       (!dense && (idx == nullptr || n_sel == nullptr))))
         return DSA_ERR_INVALID_ARG;
-    if (!aligned16(q_abs) || !aligned16(codes) || !aligned16(out) || !aligned16(idx) ||
+    if (!aligned16(q_abs) || !aligned(codes, 32) || !aligned16(out) || !aligned16(idx) ||
         !aligned(lse, 4) || !aligned(n_sel, 4) || !aligned(block_table, 4))
         return DSA_ERR_INVALID_ARG;
     const size_t need = op_bytes(sh, b, DSA_OP_PAGED_MLA);

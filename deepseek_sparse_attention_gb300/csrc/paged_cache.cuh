@@ -70,4 +70,25 @@ __device__ __forceinline__ void widen_codes(uint32_t w, float (&f)[4]) {
     }
 }
 
+// The four codes of a word as f16 (exact in both formats), two per word.
+template <int FMT>
+__device__ __forceinline__ uint2 codes_f16(uint32_t w) {
+    uint2 r;
+    if constexpr (FMT == DSA_CACHE_E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(r.x), "=r"(r.y) : "r"(w));
+    } else {
+        // a byte b under the exponent of 2^10 reads 1024 + b, b = code + 128
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));      // 1152
+        const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+        r.x = *reinterpret_cast<const uint32_t*>(&a);
+        r.y = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return r;
+}
+
 }  // namespace dsa

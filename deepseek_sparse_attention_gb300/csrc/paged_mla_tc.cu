@@ -3,29 +3,36 @@
 //
 // z[h,j] = scale * q[h,:] . row_j, p = softmax_j(z), out[h,c] = sum_j p[h,j]
 // row_j[c] for the 512 latent columns, a row being its 8-bit codes times its
-// page's power-of-two scales: both factors are exact in bf16, so the rows are
-// widened to bf16 without rounding and only q . row and P . row are formed in
-// float32 from exact products.
+// page's power-of-two scales 2^e (latent) and 2^r (rope).  The tensor cores see
+// the codes themselves: both formats are exact in f16, so a row is widened with
+// one conversion per two codes and its scales are applied to sums in float32,
+//     z = scale (2^e S_lat + 2^r S_rope),
+//     out = sum_j w_j codes_j / sum_j p_j,  w_j = p_j 2^e_j,
+// with w kept relative to a running maximum of z + e (a row's weight in the
+// output), and p relative to the same maximum with one fixed exponent taken off.
+// The query becomes f16 times one power of two per query (its elements span
+// 32 binades exactly; what is below that is below float32's reach too).  w is
+// carried as two f16 parts, hi + lo, to 2^-22 of it or 2^-25 of the largest.
 //
-// One CTA takes a range of one query's rows in tiles of 64, two bf16 row
-// buffers deep:
-//   warps 4-11  load the tile's rows through the block table (four threads a
-//               row, each 16 codes of every 64-column block, a tile ahead in
-//               registers), widen them and store them in the 128-byte swizzle.
-//               A buffer is handed over in pieces of 128 columns: a piece is
-//               refilled as soon as the value product has read it, and the next
-//               scores start as soon as their first piece is in;
-//   warp 12     issues S^T = R . Q^T (M = 64 rows, N = 64 heads, K = the row)
-//               and O^T += R^T . P^T (M = 128 latent columns, K = 64 rows), the
+// One CTA takes a range of one query's rows in tiles of 64, two f16 row buffers
+// deep:
+//   warps 8-15  load the tile's rows through the block table, a tile ahead in
+//               registers, widen them and store them in the 128-byte swizzle.  A
+//               buffer is handed over in pieces of 128 columns, a pair of warps
+//               to each: a piece is refilled as soon as the value product has
+//               read it, and the next scores start as soon as their first is in;
+//   warp 16     issues S^T = R . Q^T (M = 64 rows, N = 64 heads, K = the row)
+//               and O^T += R^T . W^T (M = 128 latent columns, K = 64 rows), the
 //               scores of tile t + 1 before the values of tile t;
-//   warps 0-3   softmax: a 16x64b load gives every lane a row and the 32 heads
-//               of one parity; running maxima raised only past a slack of 2^8
-//               (and O^T rescaled in TMEM then), P as bf16 hi + lo, 2^-18 of it.
-// An M = 128 MMA of N = 64 takes 51 cycles and one of N = 128 takes 67 (measured
-// back to back on one SM): the cost is reading the row operand.  So where TMEM
-// has room (two of the four latent blocks: 2 x 64 columns of scores, 2 x 128 and
-// 2 x 64 of output) hi and lo are one product of N = 128 whose halves are added
-// in the epilogue, and two products of N = 64 elsewhere.
+//   warps 0-7   softmax: a 16x64b load gives every lane a row and 16 heads (the
+//               query's rows are laid out so that they are neighbours); maxima
+//               are raised only past a slack, and those heads' columns of O^T
+//               rescaled in TMEM then.
+// Operand reads from shared memory bound the MMAs (128 bytes a cycle; measured
+// back to back on one SM: M = 64, N = 64 34 cycles, M = 128 with N = 64 50 and with
+// N = 128 66).  So where TMEM has room hi and lo are one product of N = 128 whose
+// halves are added in the epilogue -- two of the four latent blocks (three without
+// rope) -- and two products of N = 64 elsewhere: 2,540 cycles a tile in all.
 // Splits of one query are combined by the log-sum-exp merge: a launch over the
 // partials, or, for two splits, the two CTAs of a cluster through distributed
 // shared memory.
@@ -47,46 +54,48 @@ constexpr int kHeads = 64;
 constexpr int kTileRows = 64;
 constexpr int kLatent = kLatentCols;
 constexpr int kLatentBlocks = 4;                     // of 128 columns (MMA M)
-constexpr int kWideBlocks = 2;                       // of them with P hi and lo in one product
-constexpr uint32_t kBlock = 64 * 128;                // 64 rows or heads x 64 bf16 columns: 8 KB
+constexpr uint32_t kBlock = 64 * 128;                // 64 rows or heads x 64 f16 columns: 8 KB
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 0;                        // S^T of buffer b: 64 b
-constexpr uint32_t kOCol = 128;
+constexpr uint32_t kSCol = 0, kSRopeCol = 64;        // S^T of the latent and the rope columns
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;                        // lazy rescale threshold (log2 units)
+// A running maximum is raised (and O^T rescaled) only when it is exceeded by more
+// than this, in log2: w stays below 2^14, within f16.
+constexpr float kSlack = 14.f;
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any row
-constexpr int kSoftmaxThreads = 128;
+constexpr int kSoftmaxThreads = 256;
 constexpr int kLoaders = 256;
 constexpr int kThreads = kSoftmaxThreads + kLoaders + 32;
 constexpr int kMmaWarp = (kSoftmaxThreads + kLoaders) / 32;
-
-// First TMEM column of latent block i: hi at +0 (and lo at +64 in a wide one).
-__host__ __device__ constexpr uint32_t o_col(int i) {
-    return kOCol + 64u * (uint32_t)(i < kWideBlocks ? 2 * i : kWideBlocks + i);
-}
-static_assert(o_col(kLatentBlocks - 1) + 64 == kTmemCols, "TMEM budget");
 
 template <int W>
 struct Cfg {
     static constexpr int kCB = W / 64;               // 64-column blocks of a row
     static constexpr int kPieces = (kCB + 1) / 2;    // handed over 128 columns at a time
+    // latent blocks with hi and lo in one product, and O^T's columns: hi at +0
+    // (and lo at +64 in a wide block)
+    static constexpr int kWide = W == 576 ? 2 : 3;
+    static constexpr uint32_t kOCol = W == 576 ? 128 : 64;
+    __host__ __device__ static constexpr uint32_t o_col(int i) {
+        return kOCol + 64u * (uint32_t)(i < kWide ? 2 * i : kWide + i);
+    }
+    static_assert(kOCol + 64 * (kWide + kLatentBlocks) == kTmemCols, "TMEM budget");
     static constexpr uint32_t kOffQ = 0;
     static constexpr uint32_t kOffR = kCB * kBlock;
     static constexpr uint32_t kBufBytes = kCB * kBlock;
-    // P_hi^T [64 rows x 64 heads] of buffer b: the buffer's rope block, which the
-    // scores no longer need, or its own.  P_lo^T: one block, written once the
-    // previous tile's value products are done.  It lies behind both P_hi.
+    // W_hi^T [64 rows x 64 heads] of buffer b: the buffer's rope block, which the
+    // scores no longer need, or its own.  W_lo^T: one block, written once the
+    // previous tile's value products are done.  It lies behind both W_hi.
     static constexpr uint32_t kOffPx = kOffR + 2 * kBufBytes;
     static constexpr uint32_t kOffPlo = W == 576 ? kOffPx : kOffPx + 2 * kBlock;
     static constexpr uint32_t kOffBar = kOffPlo + kBlock;       // up to 32 barriers
-    static constexpr uint32_t kOffValid = kOffBar + 256;        // [2][64] bytes
-    static constexpr uint32_t kOffRed = kOffValid + 128;        // [4][64] int
-    static constexpr uint32_t kOffL = kOffRed + 4 * 64 * 4;     // [64] float
+    static constexpr uint32_t kOffRow = kOffBar + 256;          // [2][64] packed scales
+    static constexpr uint32_t kOffL = kOffRow + 2 * 64 * 4;     // [64] float
     static constexpr uint32_t kOffM = kOffL + 64 * 4;           // [64] float
-    static constexpr uint32_t kOffMisc = kOffM + 64 * 4;
-    static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+    static constexpr uint32_t kOffMs = kOffM + 64 * 4;          // [64] float
+    static constexpr uint32_t kOffMisc = kOffMs + 64 * 4;
+    static constexpr uint32_t kSmemBytes = kOffMisc + 64 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     __host__ __device__ static constexpr uint32_t off_p(int b) {
         return W == 576 ? kOffR + b * kBufBytes + 8 * kBlock : kOffPx + b * kBlock;
@@ -99,62 +108,55 @@ __device__ __forceinline__ int fkey(float f) {           // order-preserving flo
 }
 __device__ __forceinline__ float fval(int k) { return __int_as_float(k >= 0 ? k : k ^ 0x7fffffff); }
 
-// Sixteen codes times their scale as bf16 (exact), two 16-byte pieces.
-template <int FMT>
-__device__ __forceinline__ void widen16(const uint4& w, float f, uint4 (&r)[2]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float x[4];
-        widen_codes<FMT>(u[i], x);
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0] * f, x[1] * f);
-        const __nv_bfloat162 c = __floats2bfloat162_rn(x[2] * f, x[3] * f);
-        o[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-        o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&c);
-    }
-    r[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    r[1] = make_uint4(o[4], o[5], o[6], o[7]);
+__device__ __forceinline__ float ex2(float x) {          // 2^x, 0 below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// True in every softmax thread if `v` is true in any (named barrier 1).
-__device__ __forceinline__ bool softmax_any(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)v), "n"(kSoftmaxThreads) : "memory");
-    return r != 0;
+// 32 bytes of read-only memory (32-byte aligned).
+__device__ __forceinline__ void ldg_32bytes(const uint8_t* p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "l"(p));
 }
+
+// Packed scales of a tile's row: the bytes of its two parts and this flag.
+constexpr uint32_t kHasRow = 0x10000u;
+
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
 
-// Maxima of x[0..31] over the 16 lanes of a parity by a halving exchange: at
-// each step a lane keeps half of its values, swaps the other half with its
-// partner across one lane bit and takes the maximum (30 shuffles in all); it
-// ends with those of x[e0] and x[e0 + 1], e0 = 2 (lane & 1) + 4 ((lane >> 2) & 7).
-__device__ __forceinline__ float2 halving_max(const float (&x)[32], int lane) {
-    float a[16], b[8], c[4], d[2];
+// Maxima of x[0..15] over the 16 lanes that hold the same heads by a halving
+// exchange: at each step a lane keeps half of its values, swaps the other half
+// with its partner across one lane bit and takes the maximum; it ends with that
+// of x[8 b4 + 4 b3 + 2 b2 + b0], b the bits of its lane.
+__device__ __forceinline__ float halving_max(const float (&x)[16], int lane) {
+    float a[8], b[4], c[2];
     const bool h4 = (lane >> 4) & 1, h3 = (lane >> 3) & 1, h2 = (lane >> 2) & 1, h0 = lane & 1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        a[i] = fmaxf(h4 ? x[i + 16] : x[i], __shfl_xor_sync(0xffffffffu, h4 ? x[i] : x[i + 16], 16));
-#pragma unroll
     for (int i = 0; i < 8; ++i)
-        b[i] = fmaxf(h3 ? a[i + 8] : a[i], __shfl_xor_sync(0xffffffffu, h3 ? a[i] : a[i + 8], 8));
+        a[i] = fmaxf(h4 ? x[i + 8] : x[i], __shfl_xor_sync(0xffffffffu, h4 ? x[i] : x[i + 8], 16));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        c[i] = fmaxf(h2 ? b[i + 4] : b[i], __shfl_xor_sync(0xffffffffu, h2 ? b[i] : b[i + 4], 4));
+        b[i] = fmaxf(h3 ? a[i + 4] : a[i], __shfl_xor_sync(0xffffffffu, h3 ? a[i] : a[i + 4], 8));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        d[i] = fmaxf(h0 ? c[i + 2] : c[i], __shfl_xor_sync(0xffffffffu, h0 ? c[i] : c[i + 2], 1));
-    return make_float2(d[0], d[1]);
+        c[i] = fmaxf(h2 ? b[i + 2] : b[i], __shfl_xor_sync(0xffffffffu, h2 ? b[i] : b[i + 2], 4));
+    return fmaxf(h0 ? c[1] : c[0], __shfl_xor_sync(0xffffffffu, h0 ? c[0] : c[1], 1));
 }
 
+// 96 registers a thread at launch: of 17 warps one SM quarter (16,384 registers)
+// holds five.  The softmax gives some to the loaders, who keep two tiles' codes.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 88, kLoaderRegs = 104;
+static_assert(kSoftmaxThreads * kSoftmaxRegs + kLoaders * kLoaderRegs + 32 * kLaunchRegs <=
+                  kThreads * kLaunchRegs,
+              "registers");
 template <int FMT, int W>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b, float scale,
+paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b, float scale,
              const int32_t* __restrict__ idx, const int32_t* __restrict__ n_sel, int64_t idx_width,
              int32_t rows_per_split, int32_t n_split, int32_t pair, float* __restrict__ out,
              float* __restrict__ lse, float* __restrict__ part_o, float* __restrict__ part_ml,
@@ -164,14 +166,20 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-    uint64_t *q_full = bars, *drain = bars + 1, *s_full = bars + 2, *p_full = bars + 4,
+    uint64_t *q_full = bars, *drain = bars + 1, *s_full = bars + 2, *s_free = bars + 3,
+             *p_full = bars + 4,                     // [buffer]
+             *votes = bars + 24,                     // the softmax warps' votes on a tile
              *r_full = bars + 6,                     // [buffer][piece]
              *freed = bars + 16;                     // [buffer][latent block]: its values are in
-    uint8_t* valid = smem + C::kOffValid;
-    int* red = reinterpret_cast<int*>(smem + C::kOffRed);
+    uint32_t* rinfo = reinterpret_cast<uint32_t*>(smem + C::kOffRow);
     float* l_fin = reinterpret_cast<float*>(smem + C::kOffL);
     float* m_fin = reinterpret_cast<float*>(smem + C::kOffM);
+    float* inv_fin = reinterpret_cast<float*>(smem + C::kOffMs);     // output factors
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    uint32_t* q_max = tmem_slot + 1;
+    uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
+    int* e_first = reinterpret_cast<int*>(tmem_slot + 4);            // [4]
+    volatile uint32_t* vote = tmem_slot + 8;                         // [3] tiles
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t q = blockIdx.y;
@@ -181,10 +189,11 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
     const int half = blockIdx.z;
     const bool halved = gridDim.z == 2;
     auto owns = [&](int blk) { return !halved || (blk >> 1) == half; };
-    // Two splits of a query as a cluster: each stages its unnormalised O as
-    // [head][latent] in its shared memory, then combines half of the heads from
-    // both through distributed shared memory and writes the final output.
-    // Every thread of both CTAs calls this once (an empty split with l = 0).
+    // Two splits of a query as a cluster: each stages its output as
+    // [head][latent] in its shared memory, with the log2 of its weight in m_fin
+    // and whether it has any in l_fin; then each combines half of the heads from
+    // both through distributed shared memory.  Every thread of both CTAs calls
+    // this once (an empty split with l_fin = 0).
     float* stage = reinterpret_cast<float*>(smem);
     auto pair_merge = [&]() {
         cg::cluster_group cl = cg::this_cluster();
@@ -202,7 +211,7 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
             const float M = fmaxf(m_fin[h], m1p[h]);  // kNoMax where there was no row
             const float f0 = l0 != 0.f ? exp2f(m_fin[h] - M) : 0.f;
             const float f1 = l1 != 0.f ? exp2f(m1p[h] - M) : 0.f;
-            const float L = l0 * f0 + l1 * f1;
+            const float L = f0 + f1;
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
             if (L != 0.f) {
                 const float inv = 1.f / L;
@@ -218,21 +227,27 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
         cl.sync();                                    // the peer's reads of this stage are done
     };
 
-    if (threadIdx.x < kHeads) { m_fin[threadIdx.x] = kNoMax; l_fin[threadIdx.x] = 0.f; }
+    if (threadIdx.x < kHeads) {
+        m_fin[threadIdx.x] = kNoMax;
+        l_fin[threadIdx.x] = 0.f;
+    }
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
+        *q_max = 0;
+        mbar_init(q_full, kSoftmaxThreads + kLoaders);
         mbar_init(drain, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, kSoftmaxThreads);
+        mbar_init(votes, kSoftmaxThreads / 32);
+        vote[0] = vote[1] = vote[2] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kSoftmaxThreads);
-            for (int g = 0; g < C::kPieces; ++g) mbar_init(&r_full[i * C::kPieces + g], kLoaders);
+            for (int g = 0; g < C::kPieces; ++g)      // arrivals of warps
+                mbar_init(&r_full[i * C::kPieces + g], g < kLatentBlocks ? 2 : kLoaders / 32);
             for (int g = 0; g < kLatentBlocks; ++g) mbar_init(&freed[i * kLatentBlocks + g], 1);
         }
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
-        if (lane == 0) prefetch_tensormap(&tm_q);
-        __syncwarp();
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
@@ -252,18 +267,20 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
     pdl_trigger();
 
     // Row j of the query's list.  The loaders read the entries of their first
-    // three tiles before the list's length is known (none past its width).
+    // three tiles before the list's length is known (the list has idx_width).
     const bool dense = idx == nullptr;
     const int64_t j0 = (int64_t)split * rows_per_split;
-    const int row = (threadIdx.x - kSoftmaxThreads) >> 2, k4 = threadIdx.x & 3;
     const bool loader = warp >= kSoftmaxThreads / 32 && warp < kMmaWarp;
+    // loader warp lw brings piece lw % 4 of the rows 32 (lw / 4) .. + 31 of a tile,
+    // and the rope columns of eight of them; lane l knows where row rows0 + l is
+    const int lw = warp - kSoftmaxThreads / 32, piece = lw & 3, rows0 = 32 * (lw >> 2);
     auto entry = [&](int t, int64_t end) -> int32_t {
-        const int64_t j = j0 + (int64_t)t * kTileRows + row;
-        return j >= end ? -1 : (dense ? (int32_t)j : idx[q * idx_width + j]);
+        const int64_t j = min(j0 + (int64_t)t * kTileRows + rows0 + lane, end - 1);
+        return dense ? (int32_t)j : idx[q * idx_width + j];
     };
-    int32_t e0 = -1, e1 = -1, e2 = -1;                // entries of tiles t, t + 1, t + 2
+    int32_t e0 = 0, e1 = 0, e2 = 0;
     if (loader) {
-        const int64_t end = dense ? INT64_MAX : idx_width;
+        const int64_t end = dense ? 0x7fffffff : idx_width;
         e0 = entry(0, end);
         e1 = entry(1, end);
         e2 = entry(2, end);
@@ -294,99 +311,183 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
     }
     const int n_tiles = (int)((j1 - j0 + kTileRows - 1) / kTileRows);
 
+    // The query as f16: loaded by every warp but the MMA warp, times 2^k with
+    // its largest element in [2^14, 2^15), in the 128-byte swizzle.  Head
+    // 32 i + 16 p + k lies in row 32 i + p + 2 k: a 16x64b load of 32 columns of
+    // the scores gives a lane those of one parity, which are then 16 neighbours.
+    constexpr int kQThreads = kSoftmaxThreads + kLoaders;
+    constexpr int kQVecs = kHeads * W / 8;            // 16-byte vectors
+    constexpr int kQPer = (kQVecs + kQThreads - 1) / kQThreads;
+    auto load_query = [&](uint4 (&v)[kQPer]) {
+        const uint4* src = reinterpret_cast<const uint4*>(q_abs + q * (int64_t)kHeads * W);
+#pragma unroll
+        for (int i = 0; i < kQPer; ++i) {
+            const int c = threadIdx.x + i * kQThreads;
+            v[i] = c < kQVecs ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    // Exponent field of the largest element, then f16 times 2^k.
+    auto query_shift = [&](uint32_t mx) -> int {      // k
+        const int k = 141 - (int)(mx >> 7);
+        return k > 100 ? 100 : k;
+    };
+    auto store_query = [&](const uint4 (&v)[kQPer]) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < kQPer; ++i) {
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(u[k] & 0x7fffu, (u[k] >> 16) & 0x7fffu));
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) atomicMax(q_max, mx);
+        asm volatile("bar.sync 2, %0;" ::"n"(kQThreads) : "memory");
+        const float f = exp2i(query_shift(*q_max));
+#pragma unroll
+        for (int i = 0; i < kQPer; ++i) {
+            const int c = threadIdx.x + i * kQThreads;
+            if (c >= kQVecs) continue;
+            const int h = c / (W / 8), c8 = c % (W / 8);
+            const int n = (h & 32) + ((h >> 4) & 1) + 2 * (h & 15);
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 x = __floats2half2_rn(__uint_as_float(u[k] << 16) * f,
+                                                    __uint_as_float(u[k] & 0xffff0000u) * f);
+                o[k] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + (c8 >> 3) * kBlock + n * 128 +
+                                      (((c8 & 7) ^ (n & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+    };
+
     if (loader) {                                                     // ---- loads
+        regs_inc<kLoaderRegs>();
         // A row's way to its codes is three dependent reads (list entry, block
         // table, codes and scales): the entries are read three tiles ahead, the
         // table two, the codes one.
+        // Every read is made, of some row where there is none to read, and what it
+        // is worth is decided where it is used: a read within a branch is waited
+        // for where the branch ends.
         const int32_t* table = pc.block_table + (int64_t)qi.seq * pc.pg.table_ld;
-        auto page_at = [&](int t, int32_t r) -> int32_t {
-            const int64_t j = j0 + (int64_t)t * kTileRows + row;
-            if (j >= j1) return -1;
-            int32_t p = -1;
-            if (r >= 0 && r < qi.L && (r >> pc.pg.shift) < pc.pg.table_ld) p = table[r >> pc.pg.shift];
-            return p;
+        auto in_list = [&](int t) { return j0 + (int64_t)t * kTileRows + rows0 + lane < j1; };
+        auto in_table = [&](int32_t r) {
+            return r >= 0 && r < qi.L && (r >> pc.pg.shift) < pc.pg.table_ld;
         };
-        struct Place { const uint8_t* codes; float f0, f1; };
-        // the row's codes and scales; reports a row of the list that has no page
-        auto place = [&](int t, int32_t r, int32_t page) -> Place {
-            Place p{nullptr, 0.f, 0.f};
-            if (page >= 0 && page < pc.pg.n_pages) {
-                const int64_t at = ((int64_t)page << pc.pg.shift) + (r & (pc.pg.page_rows - 1));
-                p.codes = pc.codes + at * W + 16 * k4;
-                p.f0 = e8m0(pc.scales[(int64_t)page * kParts]);
-                if (kParts == 2) p.f1 = e8m0(pc.scales[(int64_t)page * kParts + 1]);
-            } else if (j0 + (int64_t)t * kTileRows + row < j1) {
-                record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
+        auto page_of_row = [&](int32_t r) -> int32_t { return table[in_table(r) ? r >> pc.pg.shift : 0]; };
+        const int r8 = lane >> 2, k4 = lane & 3;     // row of a group of eight, quarter of its piece
+        struct Tile {
+            uint32_t raw[4][8];                      // 32 codes of rows rows0 + 8 i + r8
+            uint4 rope;                              // 16 rope codes of row rows0 + 8 piece + r8
+            uint32_t b0, b1;                         // scales of row rows0 + lane
+            uint32_t has;                            // rows that exist, a bit each
+        };
+        auto load = [&](Tile& x, int t, int32_t r, int32_t page) {
+            const bool has = in_list(t) && in_table(r) && page >= 0 && page < pc.pg.n_pages;
+            const int64_t pg = has ? page : 0;
+            const int64_t at = has ? (pg << pc.pg.shift) + (r & (pc.pg.page_rows - 1)) : 0;
+            x.has = __ballot_sync(0xffffffffu, has);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * i + r8) * W;
+                ldg_32bytes(src + 128 * piece + 32 * k4, x.raw[i]);
             }
-            return p;
-        };
-        auto fetch = [&](const Place& p, int cb) -> uint4 {
-            return p.codes != nullptr ? __ldg(reinterpret_cast<const uint4*>(p.codes + 64 * cb))
-                                      : make_uint4(0, 0, 0, 0);
-        };
-        if (j0 + row >= j1) e0 = -1;
-        if (j0 + kTileRows + row >= j1) e1 = -1;
-        if (j0 + 2 * kTileRows + row >= j1) e2 = -1;
-        int32_t p0 = page_at(0, e0), p1 = page_at(1, e1);
-        Place cur = place(0, e0, p0);
-        uint4 raw[C::kCB];
-#pragma unroll
-        for (int cb = 0; cb < C::kCB; ++cb) raw[cb] = fetch(cur, cb);
-        int32_t p2 = page_at(2, e2), e3 = n_tiles > 3 ? entry(3, j1) : -1;
-        bool ok = true;
-        for (int t = 0; t < n_tiles && ok; ++t) {
-            const int buf = t & 1;
-            const Place nxt = t + 1 < n_tiles ? place(t + 1, e1, p1) : Place{nullptr, 0.f, 0.f};
-            uint8_t* rbuf = smem + C::kOffR + buf * C::kBufBytes + row * 128;
-#pragma unroll
-            for (int g = 0; g < C::kPieces; ++g) {
-                // the piece's columns have been read by tile t - 2's value
-                // product (the rope block, which held its P_hi, by all of it)
-                if (t >= 2 && ok)
-                    ok = mbar_wait(&freed[buf * kLatentBlocks + (g < kLatentBlocks ? g : kLatentBlocks - 1)],
-                                   (uint32_t)(((t >> 1) - 1) & 1), kWaitNs);
-                if (!ok) break;
-                if (g == 0 && k4 == 0) valid[buf * kTileRows + row] = cur.codes != nullptr;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int cb = 2 * g + c;
-                    if (cb >= C::kCB) continue;
-                    uint4 x[2];
-                    widen16<FMT>(raw[cb], cb < kLatent / 64 ? cur.f0 : cur.f1, x);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4*>(rbuf + cb * kBlock + (((2 * k4 + k) ^ (row & 7)) << 4)) =
-                            x[k];
-                    raw[cb] = fetch(nxt, cb);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&r_full[buf * C::kPieces + g]);
+            if (kParts == 2) {
+                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * piece + r8) * W;
+                x.rope = __ldg(reinterpret_cast<const uint4*>(src + kLatent + 16 * k4));
             }
-            cur = nxt;
-            e1 = e2; p1 = p2;
-            e2 = e3;
-            p2 = t + 3 < n_tiles ? page_at(t + 3, e2) : -1;
-            e3 = t + 4 < n_tiles ? entry(t + 4, j1) : -1;
+            x.b0 = __ldg(pc.scales + pg * kParts);
+            x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
+        };
+        Tile x;
+        int32_t p1;
+        {
+            uint4 v[kQPer];
+            load_query(v);
+            const int32_t p0 = page_of_row(e0);
+            p1 = page_of_row(e1);
+            load(x, 0, e0, p0);
+            store_query(v);
         }
+        bool ok = true;
+        auto step = [&](Tile& x, int t) {
+            const int buf = t & 1;
+            uint8_t* rbuf = smem + C::kOffR + buf * C::kBufBytes;
+            const uint32_t phase = (uint32_t)(((t >> 1) - 1) & 1);
+            // the piece's columns have been read by tile t - 2's value product
+            if (t >= 2) ok = mbar_wait(&freed[buf * kLatentBlocks + piece], phase, kWaitNs);
+            if (!ok) return;
+            const bool in = (x.has >> lane) & 1u;
+            if (piece == 0) rinfo[buf * kTileRows + rows0 + lane] = in ? kHasRow | (x.b1 << 8) | x.b0 : 0u;
+            if (piece == 0 && !in && in_list(t)) record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
+            // half of a 64-column block's line: four 16-byte pieces, in an order
+            // that keeps eight lanes on eight of the line's places
+            uint8_t* dst = rbuf + (2 * piece + (k4 >> 1)) * kBlock + (rows0 + r8) * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool row_in = (x.has >> (8 * i + r8)) & 1u;
+                uint4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint2 lo = codes_f16<FMT>(row_in ? x.raw[i][2 * j] : 0u);
+                    const uint2 hi = codes_f16<FMT>(row_in ? x.raw[i][2 * j + 1] : 0u);
+                    v[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(dst + 8 * i * 128 +
+                                              (((4 * (k4 & 1) + (j ^ (k4 & 2))) ^ r8) << 4)) =
+                        k4 & 2 ? v[j ^ 2] : v[j];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + piece]);
+            if constexpr (kParts == 2) {
+                // the rope block held tile t - 2's W_hi, which all of its products read
+                if (t >= 2) ok = mbar_wait(&freed[buf * kLatentBlocks + kLatentBlocks - 1], phase, kWaitNs);
+                if (!ok) return;
+                const bool row_in = (x.has >> (8 * piece + r8)) & 1u;
+                const uint2 a0 = codes_f16<FMT>(row_in ? x.rope.x : 0u), a1 = codes_f16<FMT>(row_in ? x.rope.y : 0u);
+                const uint2 a2 = codes_f16<FMT>(row_in ? x.rope.z : 0u), a3 = codes_f16<FMT>(row_in ? x.rope.w : 0u);
+                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + 8 * piece + r8) * 128;
+                *reinterpret_cast<uint4*>(rope + (((2 * k4) ^ r8) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                *reinterpret_cast<uint4*>(rope + (((2 * k4 + 1) ^ r8) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + kLatentBlocks]);
+            }
+            // the codes last: a wait for a load can be one for newer loads too
+            const int32_t r = e1, page = p1;
+            p1 = page_of_row(e2);
+            e1 = e2;
+            e2 = entry(t + 3, j1);
+            load(x, t + 1, r, page);
+        };
+        for (int t = 0; t < n_tiles && ok; ++t) step(x, t);
         if (!ok && threadIdx.x == kSoftmaxThreads) record_error(err, kDevTimeout, (int32_t)q, /*where=*/35);
-    } else if (warp == kMmaWarp) {                                    // ---- query load, MMA issue
-        if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, C::kCB * kBlock);
-            for (int cb = 0; cb < C::kCB; ++cb)
-                tma_load_2d(smem + C::kOffQ + cb * kBlock, &tm_q, q_full, 64 * cb, (int32_t)(q * kHeads));
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kHeads);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32_major(128, kHeads, 1, 1);
-            constexpr uint32_t idesc_pv2 = idesc_bf16_f32_major(128, 2 * kHeads, 1, 1);
+    } else if (warp == kMmaWarp) {                                    // ---- MMA issue
+        if (elect_one()) {
+            constexpr uint32_t idesc_s = idesc_f16_f32_major(kTileRows, kHeads, 0, 0);
+            constexpr uint32_t idesc_pv = idesc_f16_f32_major(128, kHeads, 1, 1);
+            constexpr uint32_t idesc_pv2 = idesc_f16_f32_major(128, 2 * kHeads, 1, 1);
             const uint32_t base = smem_u32(smem);
             const uint64_t d_q = sdesc_kmajor_sw128(base + C::kOffQ);
             bool ok = mbar_wait(q_full, 0, kWaitNs);
+            // Whatever is ready is issued: a tile's scores, from its first piece on
+            // (in straight line: the compiler keeps the descriptors in uniform
+            // registers only there), and the values of the tile whose weights are in.
             int next_s = 0, next_v = 0;
-            uint64_t t_prog = globaltimer_ns();
+            uint32_t idle = 0;
+            uint64_t t_prog = 0;
             while (ok && next_v < n_tiles) {
                 bool progressed = false;
                 if (next_s < n_tiles && next_s <= next_v + 1 &&
-                    mbar_test_wait(&r_full[(next_s & 1) * C::kPieces], (uint32_t)((next_s >> 1) & 1))) {
-                    // S^T(s) = R(s) Q^T, piece by piece as they come in
+                    mbar_test_wait(&r_full[(next_s & 1) * C::kPieces], (uint32_t)((next_s >> 1) & 1)) &&
+                    (next_s == 0 || mbar_test_wait(s_free, (uint32_t)((next_s - 1) & 1)))) {
+                    // S^T(s) = R(s) Q^T
                     const int bs = next_s & 1;
                     const uint64_t d_r = sdesc_kmajor_sw128(base + C::kOffR + bs * C::kBufBytes);
 #pragma unroll
@@ -399,18 +500,19 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
                             const int cb = 2 * g + k / 4, kk = k & 3;
                             if (cb >= C::kCB) continue;
                             const uint64_t o = (cb * kBlock + kk * 32) >> 4;
-                            mma_bf16_ss(tmem_base + kSCol + 64 * bs, d_r + o, d_q + o, idesc_s,
-                                        (cb | kk) != 0 ? 1u : 0u);
+                            const bool rope = cb >= kLatent / 64;
+                            mma_bf16_ss(tmem_base + (rope ? kSRopeCol : kSCol), d_r + o, d_q + o, idesc_s,
+                                        kk != 0 || (cb != 0 && !rope) ? 1u : 0u);
                         }
                     }
-                    mma_commit(&s_full[bs]);
+                    mma_commit(s_full);
                     ++next_s;
                     progressed = true;
                 }
                 if (next_v < next_s &&
                     mbar_test_wait(&p_full[next_v & 1], (uint32_t)((next_v >> 1) & 1))) {
                     // A = R^T: MN-major, 64-column blocks 8 KB apart, 8-row
-                    // groups 1 KB apart.  B = P^T: MN-major, 64 heads a block,
+                    // groups 1 KB apart.  B = W^T: MN-major, 64 heads a block,
                     // lo's block behind hi's.
                     tc_fence_after();
                     const int bv = next_v & 1;
@@ -425,13 +527,13 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
 #pragma unroll
                             for (int kk = 0; kk < kTileRows / 16; ++kk) {
                                 const uint64_t oa = (2 * i * kBlock + kk * 2048) >> 4, ob = (kk * 2048) >> 4;
-                                if (i < kWideBlocks) {
-                                    mma_bf16_ss(tmem_base + o_col(i), d_a + oa, d_both + ob, idesc_pv2,
+                                if (i < C::kWide) {
+                                    mma_bf16_ss(tmem_base + C::o_col(i), d_a + oa, d_both + ob, idesc_pv2,
                                                 kk > 0 ? 1u : acc);
                                 } else {
-                                    mma_bf16_ss(tmem_base + o_col(i), d_a + oa, d_hi + ob, idesc_pv,
+                                    mma_bf16_ss(tmem_base + C::o_col(i), d_a + oa, d_hi + ob, idesc_pv,
                                                 kk > 0 ? 1u : acc);
-                                    mma_bf16_ss(tmem_base + o_col(i), d_a + oa, d_lo + ob, idesc_pv, 1u);
+                                    mma_bf16_ss(tmem_base + C::o_col(i), d_a + oa, d_lo + ob, idesc_pv, 1u);
                                 }
                             }
                         }
@@ -440,8 +542,13 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
                     ++next_v;
                     progressed = true;
                 }
-                if (progressed) t_prog = globaltimer_ns();
-                else if (globaltimer_ns() - t_prog > kWaitNs) ok = false;
+                // the clock is slow to read: once in 256 idle rounds
+                if (progressed) idle = 0;
+                else if ((++idle & 255u) == 0) {
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 256u) t_prog = now;
+                    else if (now - t_prog > kWaitNs) ok = false;
+                }
             }
             if (!ok) record_error(err, kDevTimeout, (int32_t)q, /*where=*/36);
             mma_commit(drain);
@@ -449,119 +556,191 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
         }
     } else {                                                          // ---- softmax
         // The scores of an M = 64 tile sit in lanes 0..15 of TMEM quadrant wq;
-        // lane l of warp wq takes row 16 wq + (l >> 2) + 8 (l & 1) and the heads
-        // of parity p = (l >> 1) & 1.
-        const int wq = warp;
+        // lane l of warps wq and wq + 4 takes row 16 wq + (l >> 2) + 8 (l & 1) and
+        // 16 heads.
+        regs_dec<kSoftmaxRegs>();
+        {
+            uint4 v[kQPer];
+            load_query(v);
+            store_query(v);
+        }
+        const int wq = warp & 3;
         const int p = (lane >> 1) & 1;
         const int srow = 16 * wq + (lane >> 2) + 8 * (lane & 1);
+        const int hb = 32 * (warp >> 2) + 16 * p;    // this lane's first head
         const uint32_t lane_addr = tmem_base + ((uint32_t)(32 * wq) << 16);
-        const float c2 = scale * kLog2e;
-        float l_part[32];                            // row sums of heads 32 p .. 32 p + 31
+        const uint32_t s_addr = lane_addr + 32 * (warp >> 2);
+        // logits in log2 units, the query's power of two taken off again
+        const float c2 = scale * kLog2e * exp2i(-query_shift(*q_max));
+        float l_part[16];                            // sums of p over this lane's rows
 #pragma unroll
-        for (int e = 0; e < 32; ++e) l_part[e] = 0.f;
-        float* m_sh = m_fin;                         // running maxima, one writer per head
+        for (int e = 0; e < 16; ++e) l_part[e] = 0.f;
         float* alpha_s = l_fin;                      // rescale factors
-        bool ok = true;
+        int e_base = 0;                              // an exponent of the query's rows, taken off theirs
+        float m[16];                                 // the heads' running maxima
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m[e] = kNoMax;
+        bool have_max = false, ok = true;
+        uint32_t vote_phase = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int bf = t & 1;
-            if (ok) ok = mbar_wait(&s_full[bf], (uint32_t)((t >> 1) & 1), kWaitNs);
+            if (ok) ok = mbar_wait(s_full, (uint32_t)(t & 1), kWaitNs);
             tc_fence_after();
-            const bool has_row = valid[bf * kTileRows + srow] != 0;
-            float x[32];                             // x[k]: head p + 2 k
-            {
-                float v[32];
-                tmem_ld_16x64b_32(lane_addr + kSCol + 64 * bf, v);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = has_row ? v[e] * c2 : -INFINITY;
-            }
-            bool exceed = false;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) exceed |= x[e] > m_sh[p + 2 * e] + kSlack;
-            bool any_raised = false;
-            if (softmax_any(exceed)) {
-                const float2 mx = halving_max(x, lane);
-                const int e0 = 2 * (lane & 1) + 4 * ((lane >> 2) & 7);
-                int* rb = red + wq * kHeads;
-                rb[p + 2 * e0] = fkey(mx.x);
-                rb[p + 2 * e0 + 2] = fkey(mx.y);
+            const uint32_t info = rinfo[bf * kTileRows + srow];
+            const bool has = (info & kHasRow) != 0;
+            const int e_row = (int)(info & 255u) - 127;
+            if (t == 0) {                            // the first tile's largest
+                const int mx = __reduce_max_sync(0xffffffffu, has ? e_row : -1000);
+                if (lane == 0 && warp < 4) e_first[wq] = mx;
                 softmax_sync();
-                bool raised = false;
-                if (threadIdx.x < kHeads) {            // raise this head's running maximum?
+                const int em = max(max(e_first[0], e_first[1]), max(e_first[2], e_first[3]));
+                e_base = em == -1000 ? 0 : min(max(em, -120), 120);
+            }
+            // x = z + (e - e_base), -inf without a row; a factor beyond float32
+            // (which multiplies zeros, or gives an infinite logit either way) is capped
+            float fa = has ? c2 * e8m0(info & 255u) : 0.f;
+            if (fa > 3.4028234e38f) fa = 3.4028234e38f;
+            const float ev = has ? (float)(e_row - e_base) : -INFINITY;
+            float x[16];                             // x[k]: head hb + k
+            if constexpr (kParts == 2) {
+                float fb = has ? c2 * e8m0((info >> 8) & 255u) : 0.f;
+                if (fb > 3.4028234e38f) fb = 3.4028234e38f;
+                float u[16];
+                tmem_ld_16x64b_16_x2(s_addr + kSCol, s_addr + kSRopeCol, x, u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = fmaf(u[e], fb, fmaf(x[e], fa, ev));
+            } else {
+                tmem_ld_16x64b_16(s_addr + kSCol, x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], fa, ev);
+            }
+            tc_fence_before();
+            mbar_arrive(s_free);                     // the next tile's scores may be formed
+            // The warps vote on whether any logit exceeds its maximum's slack, and
+            // take the exponentials of the present maxima while the votes come in.
+            float w[16];
+            bool raise = !have_max;
+            if (have_max) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    x[e] -= m[e];
+                    top = fmaxf(top, x[e]);
+                }
+                const bool any = __any_sync(0xffffffffu, top > kSlack);
+                if (lane == 0) {
+                    if (any) vote[t % 3] = 1;
+                    mbar_arrive(votes);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = ex2(x[e]);
+                if (ok) ok = mbar_wait(votes, vote_phase, kWaitNs);
+                vote_phase ^= 1u;
+                raise = vote[t % 3] != 0;
+                // the last tile's vote, which every warp has read, for the one after next
+                if (threadIdx.x == 0) vote[(t + 2) % 3] = 0;
+                if (raise) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] += m[e];
+                }
+            }
+            if (raise) {
+                const float mx = halving_max(x, lane);
+                // in the block that W_hi takes below, free once the scores are formed
+                int* red = reinterpret_cast<int*>(smem + C::off_p(bf));
+                red[wq * kHeads + hb + ((lane >> 1) & 8) + ((lane >> 1) & 4) + ((lane >> 1) & 2) + (lane & 1)] =
+                    fkey(mx);
+                softmax_sync();
+                if (threadIdx.x < kHeads) {          // raise this head's running maximum?
                     const int h = threadIdx.x;
                     const float tmax = fval(max(max(red[h], red[kHeads + h]),
                                                 max(red[2 * kHeads + h], red[3 * kHeads + h])));
-                    const float m_old = m_sh[h];
+                    const bool up = tmax > m_fin[h] + kSlack;
                     float a = 1.f;
-                    if (tmax > m_old + kSlack) {
-                        a = exp2f(m_old - tmax);       // 0 from kNoMax
-                        m_sh[h] = tmax;
-                        raised = true;
+                    if (up) {
+                        a = exp2f(m_fin[h] - tmax);  // 0 from kNoMax
+                        m_fin[h] = tmax;
                     }
                     alpha_s[h] = a;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, up);
+                    if (lane == 0) raised_s[warp] = mask;
                 }
-                any_raised = softmax_any(raised);
-            }
-            if (any_raised) {
+                softmax_sync();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) l_part[e] *= alpha_s[32 * p + e];
-                if (t > 0) {                           // O^T follows the new maxima
+                for (int e = 0; e < 16; ++e) l_part[e] *= alpha_s[hb + e];
+                have_max = have_max || (raised_s[0] | raised_s[1]) != 0;
+                const uint32_t mask = raised_s[warp >> 2];
+                if (t > 0 && mask != 0) {            // their columns of O^T follow
                     const int pb = (t - 1) & 1;
                     if (ok) ok = mbar_wait(&freed[pb * kLatentBlocks + kLatentBlocks - 1],
                                            (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
                     tc_fence_after();
-                    // 32 columns at a time: four of each wide block, two of the others
+                    // eight heads at a time, in each of O^T's blocks of 64 columns
+                    constexpr int kOBlocks = kLatentBlocks + C::kWide;
 #pragma unroll 1
-                    for (int k = 0; k < 2 * (kLatentBlocks + kWideBlocks); ++k) {
-                        const int blk = k < 4 * kWideBlocks ? k >> 2 : kWideBlocks + ((k - 4 * kWideBlocks) >> 1);
-                        if (!owns(blk)) continue;
-                        const uint32_t a = lane_addr + kOCol + 32 * k;
-                        const int hh = 32 * (k & 1);
-                        float v[32];
-                        tmem_ld_32cols(a, v);
+                    for (int g = 0; g < 4; ++g) {
+                        if (((mask >> (8 * g)) & 255u) == 0) continue;
+                        const int h = 32 * (warp >> 2) + 8 * g;
+#pragma unroll 1
+                        for (int j = 0; j < kOBlocks; j += 4) {
+                            uint32_t a[4];           // the last one again past the end
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] *= alpha_s[hh + c];
-                        tmem_st_32cols(a, v);
+                            for (int i = 0; i < 4; ++i)
+                                a[i] = lane_addr + C::kOCol + 64 * min(j + i, kOBlocks - 1) + h;
+                            float v[32];
+                            tmem_ld_4x8cols(a, v);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) v[c] *= alpha_s[h + (c & 7)];
+                            tmem_st_4x8cols(a, v);
+                        }
                     }
                     tc_fence_before();
                 }
-                softmax_sync();                        // alpha_s is read, O^T rescaled
-            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = exp2f(x[e] - m_sh[p + 2 * e]);
-            // P^T row: this lane and lane ^ 2 (same row, other parity) swap
-            // halves, so that this lane holds heads 32 p .. 32 p + 31 in pairs;
-            // p = hi + lo with hi = bf16(p), lo = bf16(p - hi).
+                for (int e = 0; e < 16; ++e) {
+                    m[e] = m_fin[hb + e];
+                    x[e] -= m[e];
+                    w[e] = ex2(x[e]);
+                }
+                softmax_sync();                      // alpha_s and m_fin are read, O^T rescaled
+            }
+            // w = 2^(x - m) for the values, p = w 2^-ev for their sum -- by an
+            // exponential of its own where the page's scale is so small that w may
+            // be below float32 where p counts
+            if (__all_sync(0xffffffffu, !has || ev > -60.f)) {
+                const float f = has ? exp2i(e_base - e_row) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) l_part[e] = fmaf(w[e], f, l_part[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) l_part[e] += has ? ex2(x[e] - ev) : 0.f;
+            }
             uint8_t* prow = smem + C::off_p(bf) + srow * 128;
             uint8_t* plow = smem + C::kOffPlo + srow * 128;
-            uint32_t lo4[4][4];
+            uint32_t lo[8];
 #pragma unroll
-            for (int c16 = 0; c16 < 4; ++c16) {
-                uint32_t w4[4];
+            for (int c8 = 0; c8 < 2; ++c8) {
+                uint32_t hi[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int k = 4 * c16 + e;
-                    const float r = __shfl_xor_sync(0xffffffffu, p ? x[k] : x[k + 16], 2);
-                    const float a = p ? r : x[k], c = p ? x[k + 16] : r;
-                    const __nv_bfloat162 hi = __floats2bfloat162_rn(a, c);
-                    const float2 hf = __bfloat1622float2(hi);
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(a - hf.x, c - hf.y);
-                    const float2 lf = __bfloat1622float2(lo);
-                    l_part[2 * k] += hf.x + lf.x;      // the weights the products use
-                    l_part[2 * k + 1] += hf.y + lf.y;
-                    w4[e] = *reinterpret_cast<const uint32_t*>(&hi);
-                    lo4[c16][e] = *reinterpret_cast<const uint32_t*>(&lo);
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 8 * c8 + 2 * i;
+                    const __half2 h2 = __floats2half2_rn(w[k], w[k + 1]);
+                    const float2 hf = __half22float2(h2);
+                    const __half2 l2 = __floats2half2_rn(w[k] - hf.x, w[k + 1] - hf.y);
+                    hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                    lo[4 * c8 + i] = *reinterpret_cast<const uint32_t*>(&l2);
                 }
-                *reinterpret_cast<uint4*>(prow + (((4 * p + c16) ^ (srow & 7)) << 4)) =
-                    make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                *reinterpret_cast<uint4*>(prow + ((((hb >> 3) + c8) ^ (srow & 7)) << 4)) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
             }
-            // the previous tile's value products read P_lo
+            // the previous tile's value products read W_lo
             if (t > 0 && ok)
                 ok = mbar_wait(&freed[((t - 1) & 1) * kLatentBlocks + kLatentBlocks - 1],
                                (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
 #pragma unroll
-            for (int c16 = 0; c16 < 4; ++c16)
-                *reinterpret_cast<uint4*>(plow + (((4 * p + c16) ^ (srow & 7)) << 4)) =
-                    make_uint4(lo4[c16][0], lo4[c16][1], lo4[c16][2], lo4[c16][3]);
+            for (int c8 = 0; c8 < 2; ++c8)
+                *reinterpret_cast<uint4*>(plow + ((((hb >> 3) + c8) ^ (srow & 7)) << 4)) =
+                    make_uint4(lo[4 * c8], lo[4 * c8 + 1], lo[4 * c8 + 2], lo[4 * c8 + 3]);
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(&p_full[bf]);
@@ -575,26 +754,27 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
         // row sums to shared memory (the row buffers are free now)
         float* lsc = reinterpret_cast<float*>(smem + C::kOffR);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) lsc[srow * (kHeads + 1) + 32 * p + e] = l_part[e];
+        for (int e = 0; e < 16; ++e) lsc[srow * (kHeads + 1) + hb + e] = l_part[e];
+        softmax_sync();
+        if (threadIdx.x < kHeads) {
+            // the head's weight: out = O^T 2^e_base / l, log2 of it m + log2 l
+            const int h = threadIdx.x;
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < kTileRows; ++r) s4[r & 3] += lsc[r * (kHeads + 1) + h];
+            const float l = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            inv_fin[h] = l == 0.f ? 0.f : exp2i(e_base) / l;
+            m_fin[h] = l == 0.f ? kNoMax : m_fin[h] + log2f(l);
+            l_fin[h] = l == 0.f ? 0.f : 1.f;
+        }
     }
 
-    // ---- epilogue, warps 0-7: per-head sums, then O^T read out of TMEM
+    // ---- epilogue, warps 0-7: O^T read out of TMEM, times 2^e_base / l
     if (warp < 8) {
         asm volatile("bar.sync 3, 256;" ::: "memory");
         tc_fence_after();
-        const int wq = warp & 3, sg = warp >> 2;
-        const int hb = 32 * sg;                      // this warp's heads
-        const bool head_owner = warp < 2;            // head 32 warp + lane
-        const int ho = threadIdx.x;
+        const int wq = warp & 3, hb = 32 * (warp >> 2);      // this warp's heads
         const uint32_t lane_addr = tmem_base + ((uint32_t)(32 * wq) << 16);
-        const float* lsc = reinterpret_cast<const float*>(smem + C::kOffR);
-        if (head_owner) {
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int r = 0; r < kTileRows; ++r) s4[r & 3] += lsc[r * (kHeads + 1) + ho];
-            l_fin[ho] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        }
-        asm volatile("bar.sync 3, 256;" ::: "memory");
         const bool final_out = n_split == 1;
         const int64_t part = q * n_split + split;
         float* dst = pair ? stage
@@ -605,28 +785,25 @@ paged_mla_tc(const __grid_constant__ CUtensorMap tm_q, PagedCache pc, BatchDev b
             if (!owns(i)) continue;
             const int c = 128 * i + 32 * wq + lane;
             float v[32];
-            if (i < kWideBlocks) {                   // hi and lo halves
+            if (i < C::kWide) {                      // hi and lo halves
                 float u[32];
-                tmem_ld_32cols_x2(lane_addr + o_col(i) + hb, lane_addr + o_col(i) + 64 + hb, v, u);
+                tmem_ld_32cols_x2(lane_addr + C::o_col(i) + hb, lane_addr + C::o_col(i) + 64 + hb, v, u);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] += u[e];
             } else {
-                tmem_ld_32cols(lane_addr + o_col(i) + hb, v);
+                tmem_ld_32cols(lane_addr + C::o_col(i) + hb, v);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const float l = l_fin[hb + e];
-                const float inv = final_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                dst[(hb + e) * kLatent + c] = v[e] * inv;
-            }
+            for (int e = 0; e < 32; ++e) dst[(hb + e) * kLatent + c] = v[e] * inv_fin[hb + e];
         }
-        if (head_owner && !pair && half == 0) {
-            const float l = l_fin[ho], m = m_fin[ho];
+        if (threadIdx.x < kHeads && !pair && half == 0) {
+            const int h = threadIdx.x;
+            const float l = l_fin[h], m = l == 0.f ? -INFINITY : m_fin[h] * kLn2;
             if (final_out) {
-                if (lse != nullptr) lse[q * kHeads + ho] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                if (lse != nullptr) lse[q * kHeads + h] = m;
             } else {
-                part_ml[(part * kHeads + ho) * 2] = l == 0.f ? -INFINITY : m * kLn2;
-                part_ml[(part * kHeads + ho) * 2 + 1] = l;
+                part_ml[(part * kHeads + h) * 2] = m;
+                part_ml[(part * kHeads + h) * 2 + 1] = l;
             }
         }
     }
@@ -645,11 +822,6 @@ cudaError_t launch_w(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
                      float* part_o, float* part_ml, int32_t rps, int32_t n_split, int32_t* err,
                      cudaStream_t st) {
     using C = Cfg<W>;
-    CUtensorMap tm_q;
-    const uint64_t dims[2] = {(uint64_t)W, (uint64_t)b.n_q * kHeads};
-    const uint64_t strides[1] = {(uint64_t)W * 2};
-    const uint32_t box[2] = {64, kHeads};
-    if (!encode_bf16_map(&tm_q, q_abs, 2, dims, strides, box)) return cudaErrorInvalidValue;
     auto kern = paged_mla_tc<FMT, W>;
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)C::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -671,7 +843,7 @@ cudaError_t launch_w(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pair ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tm_q, pc, b, sh.scale, idx, n_sel, sh.index_row_width(), rps,
+    e = cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q_abs), pc, b, sh.scale, idx, n_sel, sh.index_row_width(), rps,
                            n_split, pair, out, lse, part_o, part_ml, err);
     if (e != cudaSuccess || n_split <= 2) return e;
     return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st);

@@ -418,7 +418,8 @@ dsa_status dsa_page_plan(const dsa_pages *pages, int32_t n_seq, int64_t max_new,
  * a NaN the e4m3 NaN or s8 0, and either sets the error word (code 5), as does a
  * page whose exponent is above 119 already, which is left as it was.  A slot
  * outside the pool, or slots that do not follow one another, set the error word
- * and leave the page as it was.  rows and codes 16-byte, slots 8-byte aligned.
+ * and leave the page as it was.  rows 16-byte, codes 32-byte,
+ * slots 8-byte aligned.
  * n_seq <= 65535; n_q is not limited to 65535 here.  Workspace:
  * DSA_OP_CACHE_APPEND (the error word). */
 dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, const dsa_pages *pages,
@@ -433,8 +434,11 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  *   codes, scales, block_table as above
  * An index outside [0, L), or one whose block-table entry is no page of the
  * pool, sets the error word and its row is skipped.  A NaN code or scale of an
- * attended row gives NaN outputs.  float32 accumulation and softmax.  Pointers
- * 16-byte aligned (lse, n_sel and block_table 4-byte, scales any).  Workspace:
+ * attended row gives NaN outputs.  float32 accumulation and softmax.  bf16
+ * queries run on the tensor cores: the query as f16 times a power of two (exact
+ * for elements within 2^-32 of its largest), a row's weight in the output as two
+ * f16 parts (2^-22 of it, or 2^-25 of the largest).  Pointers 16-byte aligned
+ * (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
  * DSA_OP_PAGED_MLA. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,
                               const dsa_pages *pages, const void *q_abs, const void *codes,

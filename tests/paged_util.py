@@ -132,34 +132,46 @@ def append(page, kv, q, rows, slots, codes, scales, fmt):
     return codes, scales
 
 
-def attention(q_abs, rows, at, scale):
-    """(out [H, 512], lse [H], weight [H, 512], reach) of one query over rows[at]:
-    weight = sum_j p_j |row_j|, reach = max_hj scale * sum_c |q_hc row_jc|."""
+def attention(q_abs, rows, at, scale, unit=None):
+    """(out [H, 512], lse [H], weight [H, 512], reach, floor [H, 512]) of one query
+    over rows[at]: weight = sum_j p_j |row_j|, reach = max_hj scale sum_c |q_hc
+    row_jc|, floor = max_j (p_j unit_j) sum_j |row_j| / unit_j with unit the rows'
+    latent scales (0 without them)."""
     H = q_abs.shape[0]
     if len(at) == 0:
-        return (np.zeros((H, LATENT)), np.full(H, -np.inf), np.zeros((H, LATENT)), 0.0)
+        z = np.zeros((H, LATENT))
+        return z, np.full(H, -np.inf), z, 0.0, z
     r = rows[at]
     z = scale * q_abs @ r.T
     m = z.max(1, keepdims=True)
     p = np.exp(z - m)
     tot = p.sum(1, keepdims=True)
     p /= tot
+    floor = np.zeros((H, LATENT))
+    if unit is not None:
+        u = unit[at]
+        floor = (p * u).max(1)[:, None] * (np.abs(r[:, :LATENT]) / u[:, None]).sum(0)
     return (p @ r[:, :LATENT], (m + np.log(tot))[:, 0], p @ np.abs(r[:, :LATENT]),
-            float((scale * np.abs(q_abs) @ np.abs(r).T).max()))
+            float((scale * np.abs(q_abs) @ np.abs(r).T).max()), floor)
 
 
-def attention_bounds(dtype, width, n_rows, weight, reach, lse):
+def attention_bounds(dtype, width, n_rows, weight, reach, lse, floor):
     """Element-wise bounds of the library's error.
 
     A logit is a float32 sum of W products, |error| <= W 2^-23 sum|q r| scale
     (half of that with rounding, all of it where the tensor cores truncate);
-    the exponential adds 2^-21 and, through the float32 argument, 2^-23 of it;
-    with bf16 queries a weight is carried as hi + lo bf16, each off by half a
-    step: 2^-9 * 2^-9 = 2^-18 of it.  The output's numerator and denominator
-    each take that relative error per weight, and the float32 sums over the
-    rows n 2^-23 of the sum of magnitudes."""
+    the exponential adds 2^-21 and, through the float32 argument, 2^-23 of it.
+    With bf16 queries a row's weight w = p 2^e is carried as hi + lo in f16:
+    each is off by half a step, 2^-11 * 2^-11 = 2^-22 of w, but by no less than
+    half of f16's smallest step, 2^-25, where w is relative to a running maximum
+    that is at most the largest w; times the row's codes, |row| / 2^e, that is
+    2^-25 of `floor`.  The output's numerator and denominator each take the
+    relative error per weight, and the float32 sums over the rows n 2^-23 of the
+    sum of magnitudes."""
     logit = width * 2.0 ** -23 * reach
-    per_weight = logit + 2.0 ** -21 + 2.0 ** -23 * reach + (2.0 ** -18 if dtype == "bf16" else 0.0)
+    per_weight = logit + 2.0 ** -21 + 2.0 ** -23 * reach + (2.0 ** -22 if dtype == "bf16" else 0.0)
     rel = 2 * per_weight + (n_rows + 2) * 2.0 ** -23
     finite = np.where(np.isfinite(lse), np.abs(lse), 0.0)
-    return rel * weight + 1e-37, logit + per_weight + n_rows * 2.0 ** -23 + 2.0 ** -22 * (finite + 1)
+    least = 2.0 ** -25 * floor if dtype == "bf16" else 0.0
+    return (rel * weight + least + 1e-37,
+            logit + per_weight + n_rows * 2.0 ** -23 + 2.0 ** -22 * (finite + 1))

@@ -457,25 +457,27 @@ class AttnCase:
         """The rows query i may attend over, float64."""
         pool = ref.widen(self.codes, self.scales, self.fmt)
         pos = np.arange(self.L[i])
-        return pool[self.table[self.seq[i]][pos // self.page], pos % self.page]
+        page = self.table[self.seq[i]][pos // self.page]
+        return pool[page, pos % self.page], np.exp2(self.scales[page, 0].astype(np.float64) - 127)
 
     def expect(self, i, drop=()):
         at = np.arange(self.L[i]) if self.dense else self.idx[i, :self.n_sel[i]]
         at = np.array([j for j in at if j not in drop], dtype=np.int64)
-        return ref.attention(self.q_abs[i].double().numpy(), self.rows_of(i), at, SCALE), len(at)
+        rows, unit = self.rows_of(i)
+        return ref.attention(self.q_abs[i].double().numpy(), rows, at, SCALE, unit), len(at)
 
     def check(self, out, lse, queries=None, drop=()):
         num = den = 0.0
         for i in range(self.n_q) if queries is None else queries:
-            (o, l, weight, reach), n = self.expect(i, drop)
-            tol, tol_lse = ref.attention_bounds(self.dtype, self.width, n, weight, reach, l)
+            (o, l, weight, reach, floor), n = self.expect(i, drop)
+            tol, tol_lse = ref.attention_bounds(self.dtype, self.width, n, weight, reach, l, floor)
             assert np.all(np.abs(out[i] - o) <= tol), (i, np.abs(out[i] - o).max())
             empty = np.isneginf(l)
             assert np.array_equal(np.isneginf(lse[i]), empty)
             assert np.all(np.abs(lse[i][~empty] - l[~empty]) <= tol_lse[~empty]), i
             num += ((out[i] - o) ** 2).sum()
             den += (o ** 2).sum()
-        # bf16 queries: weights to 2^-18, everything else to float32
+        # everything to about float32
         assert num <= (1e-5) ** 2 * den
 
 
@@ -737,7 +739,9 @@ def test_plan_append_select_and_attend(fmt):
                 L = kv[s] - q[s] + i + 1
                 at = sel[t, :cnt[t]]
                 assert cnt[t] == min(L, top_k) and (np.diff(at) > 0).all() and at.max() < L
-                want, want_l, weight, reach = ref.attention(q_abs[t].double().numpy(), got, at, SCALE)
-                tol, tol_l = ref.attention_bounds("bf16", 576, cnt[t], weight, reach, want_l)
+                unit = np.exp2(host(scales)[tab[s][pos // page], 0].astype(np.float64) - 127)
+                want, want_l, weight, reach, floor = ref.attention(q_abs[t].double().numpy(), got, at,
+                                                                   SCALE, unit)
+                tol, tol_l = ref.attention_bounds("bf16", 576, cnt[t], weight, reach, want_l, floor)
                 assert np.all(np.abs(o[t] - want) <= tol) and np.all(np.abs(l[t] - want_l) <= tol_l)
                 t += 1

@@ -87,7 +87,7 @@ def test_page_plan_rejects_before_enqueue(lib):
 def test_cache_append_rejects_before_enqueue(lib):
     for i in range(4):
         assert _append(lib, ptrs=_without(4, i)) == 1
-    for i, bad in ((0, P(264)), (1, P(260)), (2, P(264))):
+    for i, bad in ((0, P(264)), (1, P(260)), (2, P(272))):
         assert _append(lib, ptrs=_without(4, i, bad)) == 1
     assert _append(lib, sh=dsa.make_shape(rope_dim=32)) == 2
     assert _append(lib, b=_batch(max_q=2, max_kv=1)) == 1
@@ -100,7 +100,7 @@ def test_cache_append_rejects_before_enqueue(lib):
 def test_paged_attention_rejects_before_enqueue(lib):
     for i in range(7):                                                       # lse may be missing
         assert _attn(lib, ptrs=_without(8, i)) == 1
-    for i, bad in ((0, P(264)), (1, P(264)), (3, P(258)), (4, P(264)), (5, P(258)), (6, P(264)),
+    for i, bad in ((0, P(264)), (1, P(272)), (3, P(258)), (4, P(264)), (5, P(258)), (6, P(264)),
                    (7, P(258))):
         assert _attn(lib, ptrs=_without(8, i, bad)) == 1
     assert _attn(lib, sh=dsa.make_shape(heads=32)) == 2
@@ -194,9 +194,9 @@ def test_reference_attention_reduces_to_closed_forms():
     rng = np.random.default_rng(0)
     rows = rng.normal(size=(5, 576))
     q = rng.normal(size=(64, 576))
-    o, l, _, _ = ref.attention(q, rows, [3], 0.25)
+    o, l, *_ = ref.attention(q, rows, [3], 0.25)
     assert np.allclose(o, rows[3, :512]) and np.allclose(l, 0.25 * q @ rows[3])
-    o, l, _, _ = ref.attention(np.zeros_like(q), rows, [0, 1, 4], 1.0)
+    o, l, *_ = ref.attention(np.zeros_like(q), rows, [0, 1, 4], 1.0)
     assert np.allclose(o, rows[[0, 1, 4], :512].mean(0)) and np.allclose(l, math.log(3))
-    o, l, _, _ = ref.attention(q, rows, [], 1.0)
+    o, l, *_ = ref.attention(q, rows, [], 1.0)
     assert not o.any() and np.isneginf(l).all()
