@@ -149,16 +149,22 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle; torch.cuda.current_stream() wraps it in an object,
+# which costs a microsecond or more per call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
 
 
 def _call(name: str, *args) -> int:
-    rc = getattr(load(), name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != 0:
         raise DsaError(name, rc)
     return rc
@@ -303,28 +309,41 @@ def make_pages(page_rows: int, n_pages: int, table_ld: int, fmt=CACHE_E4M3) -> P
     return Pages(int(page_rows), int(fmt), int(n_pages), int(table_ld))
 
 
-def _typed(t: Optional[torch.Tensor], dtype, what: str):
-    """Pointer of a tensor whose element type the call fixes."""
-    if t is not None and t.dtype != dtype:
+def _refuse(t, dtype, device: int, least: int, what: str):
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    if t.dtype is not dtype:
         raise ValueError(f"{what} is {dtype}, not {t.dtype}")
-    return _ptr(t)
+    if t.numel() < least:
+        raise ValueError(f"{what} holds at least {least} elements")
+    if not t.is_cuda:
+        raise ValueError("libdsa takes CUDA tensors only")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on another device than the call's: make its device current")
+    raise ValueError("libdsa takes contiguous tensors only")
 
 
-def _codes(pages: Pages, t: torch.Tensor, width: int):
-    if t.element_size() != 1 or t.numel() != pages.n_pages * pages.page_rows * width:
-        raise ValueError("codes holds n_pages x page_rows x width one-byte elements")
-    return _ptr(t)
+def _at(t, dtype, device: int, least: int, what: str) -> int:
+    """Address of a tensor of the call: its type, size and device are checked."""
+    if (t is None or t.dtype is not dtype or t.numel() < least or t.get_device() != device or
+            not t.is_contiguous()):
+        _refuse(t, dtype, device, least, what)
+    return t.data_ptr()
 
 
-def _scales(shape: Shape, pages: Pages, t: torch.Tensor):
-    if t.element_size() != 1 or t.numel() != pages.n_pages * (2 if shape.rope_dim else 1):
-        raise ValueError("scales holds one byte per page and part of a row")
-    return _ptr(t)
+def _bytes_at(t, device: int, count: int, what: str) -> int:
+    """Address of a tensor of `count` one-byte elements of any type."""
+    if t.element_size() != 1 or t.numel() != count:
+        raise ValueError(f"{what} holds {count} one-byte elements")
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse(t, t.dtype, device, 0, what)
+    return t.data_ptr()
 
 
-def _at_least(t: Optional[torch.Tensor], n: int, what: str) -> None:
-    if t is None or t.numel() < n:
-        raise ValueError(f"{what} holds at least {n} elements")
+def _stream_at(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def dsa_page_plan(pages, held_len, kv_len, q_len, free_pages, n_free, block_table, row_off, q_off,
@@ -332,44 +351,47 @@ def dsa_page_plan(pages, held_len, kv_len, q_len, free_pages, n_free, block_tabl
     """Block tables, slot map (``slots``, one entry per new token) and batch
     offsets from request lengths (see dsa.h); ``n_free_out=None`` updates
     ``n_free`` in place."""
-    n_seq, i64, i32 = held_len.numel(), torch.int64, torch.int32
-    n_free_out = n_free if n_free_out is None else n_free_out
-    _at_least(kv_len, n_seq, "kv_len")
-    _at_least(q_len, n_seq, "q_len")
-    _at_least(row_off, n_seq + 1, "row_off")
-    _at_least(q_off, n_seq + 1, "q_off")
-    _at_least(free_pages, pages.n_pages, "free_pages")
-    _at_least(block_table, n_seq * pages.table_ld, "block_table")
-    _call("dsa_page_plan", ctypes.byref(pages), n_seq, slots.numel(),
-          _typed(held_len, i64, "held_len"), _typed(kv_len, i64, "kv_len"),
-          _typed(q_len, i64, "q_len"), _typed(free_pages, i32, "free_pages"),
-          _typed(n_free, i32, "n_free"), _typed(n_free_out, i32, "n_free_out"),
-          _typed(block_table, i32, "block_table"), _typed(row_off, i64, "row_off"),
-          _typed(q_off, i64, "q_off"), _typed(slots, i64, "slots"), _ptr(ws), ws.numel(),
-          _stream(stream))
+    n, i64, i32, d = held_len.numel(), torch.int64, torch.int32, torch.cuda.current_device()
+    free = _at(n_free, i32, d, 1, "n_free")
+    _call("dsa_page_plan", pages, n, slots.numel(), _at(held_len, i64, d, n, "held_len"),
+          _at(kv_len, i64, d, n, "kv_len"), _at(q_len, i64, d, n, "q_len"),
+          _at(free_pages, i32, d, pages.n_pages, "free_pages"), free,
+          free if n_free_out is None else _at(n_free_out, i32, d, 1, "n_free_out"),
+          _at(block_table, i32, d, n * pages.table_ld, "block_table"),
+          _at(row_off, i64, d, n + 1, "row_off"), _at(q_off, i64, d, n + 1, "q_off"),
+          _at(slots, i64, d, 0, "slots"), _at(ws, torch.uint8, d, 0, "ws"), ws.numel(),
+          _stream_at(stream, d))
 
 
 def dsa_cache_append(shape, batch, pages, rows, slots, codes, scales, ws, stream=None) -> None:
     """The batch's new rows [n_q, W] rounded into their slots (see dsa.h)."""
-    width = shape.kv_lora + shape.rope_dim
-    _at_least(rows, batch.n_q * width, "rows")
-    _at_least(slots, batch.n_q, "slots")
-    _call("dsa_cache_append", ctypes.byref(shape), ctypes.byref(batch), ctypes.byref(pages),
-          _typed(rows, _TORCH_DTYPE[shape.dtype], "rows"), _typed(slots, torch.int64, "slots"),
-          _codes(pages, codes, width), _scales(shape, pages, scales), _ptr(ws), ws.numel(),
-          _stream(stream))
+    width, d = shape.kv_lora + shape.rope_dim, torch.cuda.current_device()
+    n_q, n_pages = batch.n_q, pages.n_pages
+    _call("dsa_cache_append", shape, batch, pages,
+          _at(rows, _TORCH_DTYPE[shape.dtype], d, n_q * width, "rows"),
+          _at(slots, torch.int64, d, n_q, "slots"),
+          _bytes_at(codes, d, n_pages * pages.page_rows * width, "codes"),
+          _bytes_at(scales, d, n_pages * (2 if shape.rope_dim else 1), "scales"),
+          _at(ws, torch.uint8, d, 0, "ws"), ws.numel(), _stream_at(stream, d))
 
 
 def dsa_paged_mla_attn(shape, batch, pages, q_abs, codes, scales, block_table, idx, n_sel, out,
                        lse, ws, stream=None) -> None:
     """Step 3 over the paged 8-bit cache (see dsa.h)."""
-    _at_least(block_table, batch.n_seq * pages.table_ld, "block_table")
-    _call("dsa_paged_mla_attn", ctypes.byref(shape), ctypes.byref(batch), ctypes.byref(pages),
-          _typed(q_abs, _TORCH_DTYPE[shape.dtype], "q_abs"),
-          _codes(pages, codes, shape.kv_lora + shape.rope_dim), _scales(shape, pages, scales),
-          _typed(block_table, torch.int32, "block_table"), _typed(idx, torch.int32, "idx"),
-          _typed(n_sel, torch.int32, "n_sel"), _typed(out, torch.float32, "out"),
-          _typed(lse, torch.float32, "lse"), _ptr(ws), ws.numel(), _stream(stream))
+    d, i32, f32 = torch.cuda.current_device(), torch.int32, torch.float32
+    n_q, heads, n_pages = batch.n_q, shape.heads, pages.n_pages
+    width = shape.kv_lora + shape.rope_dim
+    dense = idx is None
+    _call("dsa_paged_mla_attn", shape, batch, pages,
+          _at(q_abs, _TORCH_DTYPE[shape.dtype], d, n_q * heads * width, "q_abs"),
+          _bytes_at(codes, d, n_pages * pages.page_rows * width, "codes"),
+          _bytes_at(scales, d, n_pages * (2 if shape.rope_dim else 1), "scales"),
+          _at(block_table, i32, d, batch.n_seq * pages.table_ld, "block_table"),
+          None if dense else _at(idx, i32, d, n_q * (shape.top_k + shape.kpool - 1), "idx"),
+          None if dense else _at(n_sel, i32, d, n_q, "n_sel"),
+          _at(out, f32, d, n_q * heads * shape.kv_lora, "out"),
+          None if lse is None else _at(lse, f32, d, n_q * heads, "lse"),
+          _at(ws, torch.uint8, d, 0, "ws"), ws.numel(), _stream_at(stream, d))
 
 
 def dsa_check_device_error(ws: Optional[torch.Tensor], stream=None) -> int:

@@ -244,7 +244,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 // Kernels one call of `op` enqueues for this shape and batch bound.
 int32_t plan_launches(const Shape& sh, const BatchDev& bh, int32_t op, int32_t splits) {
-    if (op == DSA_OP_PAGE_PLAN) return page_plan_launches();
+    if (op == DSA_OP_PAGE_PLAN) return page_plan_launches(bh.n_seq);
     if (bh.n_q <= 0) return 0;
     // attention, then the split merge -- except for two tensor-core splits,
     // which merge inside the attention launch (a CTA pair)
@@ -525,8 +525,9 @@ dsa_status dsa_page_plan(const dsa_pages* pages, int32_t n_seq, int64_t max_new,
         return s;
     const PagePlanArgs a{pg,         n_seq,       max_new,   held_len, kv_len, q_len, free_pages,
                          n_free_in,  n_free_out,  block_table, row_off, q_off, slots};
-    return cuda_status(launch_page_plan(a, bytes(ws) + scratch_off(), static_cast<int32_t*>(ws),
-                                        static_cast<cudaStream_t>(stream)),
+    return cuda_status(launch_page_plan(a, bytes(ws) + scratch_off(),
+                                        reinterpret_cast<uint32_t*>(bytes(ws) + kWsPlanTicketOffset),
+                                        static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)),
                        "page_plan");
 }
 

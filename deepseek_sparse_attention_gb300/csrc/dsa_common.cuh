@@ -27,6 +27,10 @@ constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 // per-query state a launch uses.
 constexpr size_t kWsLaunchCountOffset = 192;
 
+// Byte offset in the header of the page plan's CTA ticket (32 bits): the plan's
+// CTAs count themselves in it, and the last one zeroes it.
+constexpr size_t kWsPlanTicketOffset = 224;
+
 enum DeviceError : int32_t {
     kDevOk = 0,
     kDevBadIndex = 1,      // a selected index outside [0, L)

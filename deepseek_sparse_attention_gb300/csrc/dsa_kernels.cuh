@@ -203,7 +203,7 @@ cudaError_t launch_sparse_mla(const Shape& sh, const BatchDev& b, const void* q_
 
 // The paged 8-bit cache.  Page plan (page_plan.cu): offsets, block table, free
 // pages and slot map from request lengths; `scratch` holds
-// page_plan_scratch_bytes() bytes.
+// page_plan_scratch_bytes() bytes, `ticket` is a word that calls leave zero.
 struct PagePlanArgs {
     PagesDev pg;
     int64_t n_seq, max_new;
@@ -215,8 +215,9 @@ struct PagePlanArgs {
     int64_t *row_off, *q_off, *slots;
 };
 size_t page_plan_scratch_bytes(int64_t n_seq);
-int32_t page_plan_launches();
-cudaError_t launch_page_plan(const PagePlanArgs& a, void* scratch, int32_t* err, cudaStream_t st);
+int32_t page_plan_launches(int64_t n_seq);
+cudaError_t launch_page_plan(const PagePlanArgs& a, void* scratch, uint32_t* ticket, int32_t* err,
+                             cudaStream_t st);
 
 // Append (cache_append.cu): the batch's new rows rounded into their slots.
 cudaError_t launch_cache_append(const Shape& sh, const BatchDev& b, const PagesDev& pg,

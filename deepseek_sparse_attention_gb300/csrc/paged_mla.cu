@@ -8,11 +8,16 @@
 // ("GLM 5.2 in one C file", "Attention: Multi head Latent Attention With a Tiny
 // KV Cache"; "GLM-5.x (glm-dsa, glm5next)", "The block").
 //
-// A CTA takes a range of one query's rows, 16 at a time: the rows are widened
-// to float in shared memory, the 64 x 16 logits formed against the staged
-// query, and an online softmax folds them into a 64 x 512 float accumulator in
-// registers.  Rows whose index or page is out of range are zero and take no
-// weight.  Splits of a query are combined by the log-sum-exp merge.
+// A CTA takes 16 heads and a range of one query's rows, 16 at a time: the rows
+// are widened to float in shared memory, and the 16 lanes of a half warp belong
+// to one head -- a lane forms one row's logit, the half warp folds the tile into
+// its running maximum and sum by shuffles, and each lane accumulates 32 of the
+// head's 512 outputs.  Bound by shared-memory reads (a float4 for four
+// multiply-adds); small float32 steps are bound by latency, which is why the
+// heads are spread over CTAs (one query of 256 rows: 27 us with all 64 heads in
+// a CTA and the softmax through shared memory, 13 us so).  Rows whose index or
+// page is out of range are zero and take no weight.  Splits of a query are
+// combined by the log-sum-exp merge.
 #include <math.h>
 
 #include "dsa_kernels.cuh"
@@ -22,26 +27,20 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 64;
+constexpr int kGroup = 16;                       // heads of a CTA
 constexpr int kTile = 16;                        // rows per tile
 constexpr int kLatent = kLatentCols;
-constexpr int kSsStride = kTile + 1;
 
 template <int W>
 struct Smem {
-    static constexpr int kQStride = W + 4;
-    static constexpr int kRStride = W + 4;
-    static constexpr size_t kQ = (size_t)kHeads * kQStride * sizeof(float);
-    static constexpr size_t kR = (size_t)kTile * kRStride * sizeof(float);
-    static constexpr size_t kS = (size_t)kHeads * kSsStride * sizeof(float);
-    static constexpr size_t kStats = 3 * kHeads * sizeof(float);
+    static constexpr int kStride = W + 4;        // floats: eight rows' float4s on distinct banks
     static constexpr size_t kRows = kTile * (2 * sizeof(int64_t));
-    static constexpr size_t kTotal = kQ + kR + kS + kStats + kRows;
+    static constexpr size_t kQ = (size_t)kGroup * kStride * sizeof(float);
+    static constexpr size_t kR = (size_t)kTile * kStride * sizeof(float);
+    static constexpr size_t kP = (size_t)kGroup * kTile * sizeof(float);
+    static constexpr size_t kTotal = kRows + kQ + kR + kP;
 };
 
-__device__ __forceinline__ void widen4(const float* p, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
 template <int FMT, int W>
 __global__ void __launch_bounds__(kThreads)
 paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__ q_abs,
@@ -57,19 +56,20 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
     float2* row_scale = reinterpret_cast<float2*>(row_at + kTile);
     float* Qs = reinterpret_cast<float*>(smem + S::kRows);
     float* Rs = reinterpret_cast<float*>(smem + S::kRows + S::kQ);
-    float* Ss = reinterpret_cast<float*>(smem + S::kRows + S::kQ + S::kR);
-    float* m_s = reinterpret_cast<float*>(smem + S::kRows + S::kQ + S::kR + S::kS);
-    float* l_s = m_s + kHeads;
-    float* alpha_s = l_s + kHeads;
+    float* Ps = reinterpret_cast<float*>(smem + S::kRows + S::kQ + S::kR);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int tid = threadIdx.x;
     const int64_t q = blockIdx.y;
-    const int split = blockIdx.x;
+    const int split = blockIdx.x, h0 = kGroup * blockIdx.z;
+    const int hl = tid >> 4, j = tid & 15, h = h0 + hl;  // this lane's head; its row, its columns
+    const int64_t part = q * n_split + split;
     QueryInfo qi;
     if (!query_info(b, q, qi, err, /*where=*/33)) {
-        if (n_split > 1 && tid < kHeads) {             // no weight in the merge
-            part_ml[((q * n_split + split) * kHeads + tid) * 2 + 0] = -INFINITY;
-            part_ml[((q * n_split + split) * kHeads + tid) * 2 + 1] = 0.f;
+        if (n_split > 1 && j == 0) {                   // no weight in the merge
+            part_ml[(part * kHeads + h) * 2 + 0] = -INFINITY;
+            part_ml[(part * kHeads + h) * 2 + 1] = 0.f;
         }
         return;
     }
@@ -78,27 +78,25 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
     const int64_t j_begin = (int64_t)split * rows_per_split;
     const int64_t j_end = j_begin + rows_per_split < ns ? j_begin + rows_per_split : ns;
 
-    constexpr int kQVec = 4;
-    const float* qsrc = q_abs + q * (int64_t)kHeads * W;
-    for (int v = tid; v < kHeads * (W / kQVec); v += kThreads) {
-        const int h = v / (W / kQVec), c = (v % (W / kQVec)) * kQVec;
-        *reinterpret_cast<uint4*>(Qs + h * S::kQStride + c) =
-            __ldg(reinterpret_cast<const uint4*>(qsrc + (int64_t)h * W + c));
+    const float* qsrc = q_abs + (q * kHeads + h0) * (int64_t)W;
+    for (int v = tid; v < kGroup * (W / 4); v += kThreads) {
+        const int r = v / (W / 4), c = (v % (W / 4)) * 4;
+        *reinterpret_cast<float4*>(Qs + r * S::kStride + c) =
+            __ldg(reinterpret_cast<const float4*>(qsrc + (int64_t)r * W + c));
     }
-    if (tid < kHeads) { m_s[tid] = -INFINITY; l_s[tid] = 0.f; }
 
-    const int oh = tid >> 2, ocg = tid & 3;            // accumulator owner: head, column group
-    float o[kLatent / 4];
+    float m = -INFINITY, l = 0.f;                      // the same in a head's 16 lanes
+    float o[kLatent / 16];                             // columns 4 j + 64 i + (0..3)
 #pragma unroll
-    for (int i = 0; i < kLatent / 4; ++i) o[i] = 0.f;
+    for (int i = 0; i < kLatent / 16; ++i) o[i] = 0.f;
 
-    for (int64_t j0 = j_begin; j0 < j_end; j0 += kTile) {
-        const int nrows = (int)(j_end - j0 < kTile ? j_end - j0 : kTile);
+    for (int64_t t0 = j_begin; t0 < j_end; t0 += kTile) {
+        const int nrows = (int)(j_end - t0 < kTile ? j_end - t0 : kTile);
         if (tid < kTile) {
             int64_t at = -1;
             float2 f = make_float2(0.f, 0.f);
             if (tid < nrows) {
-                const int32_t r = idx == nullptr ? (int32_t)(j0 + tid) : idx[q * idx_width + j0 + tid];
+                const int32_t r = idx == nullptr ? (int32_t)(t0 + tid) : idx[q * idx_width + t0 + tid];
                 const int32_t page = r >= 0 && r < qi.L ? page_of(pc.pg, pc.block_table, qi.seq, r) : -1;
                 if (page >= 0) {
                     at = ((int64_t)page << pc.pg.shift) + (r & (pc.pg.page_rows - 1));
@@ -113,96 +111,78 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
         }
         __syncthreads();
         for (int v = tid; v < kTile * kRowVecs; v += kThreads) {
-            const int j = v / kRowVecs, c = (v % kRowVecs) * 16;
-            const int64_t at = row_at[j];
+            const int r = v / kRowVecs, c = (v % kRowVecs) * 16;
+            const int64_t at = row_at[r];
             uint4 w = make_uint4(0, 0, 0, 0);
             if (at >= 0) w = __ldg(reinterpret_cast<const uint4*>(pc.codes + at * W + c));
-            const float f = at < 0 ? 0.f : (c < kLatent ? row_scale[j].x : row_scale[j].y);
+            const float f = at < 0 ? 0.f : (c < kLatent ? row_scale[r].x : row_scale[r].y);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float x[4];
                 widen_codes<FMT>(u[k], x);
-                *reinterpret_cast<float4*>(Rs + j * S::kRStride + c + 4 * k) =
+                *reinterpret_cast<float4*>(Rs + r * S::kStride + c + 4 * k) =
                     make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
             }
         }
         __syncthreads();
-        {                                              // logits: row j, heads h0 + 16 i
-            const int j = tid & (kTile - 1), h0 = tid >> 4;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int c = 0; c < W; c += 4) {
-                float rf[4];
-                widen4(Rs + j * S::kRStride + c, rf);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float qf[4];
-                    widen4(Qs + (h0 + 16 * i) * S::kQStride + c, qf);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[i] = fmaf(qf[k], rf[k], acc[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                Ss[(h0 + 16 * i) * kSsStride + j] = row_at[j] >= 0 ? acc[i] * scale : -INFINITY;
+        // the logit of row j and head h
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int c = 0; c < W; c += 4) {
+            const float4 r4 = *reinterpret_cast<const float4*>(Rs + j * S::kStride + c);
+            const float4 q4 = *reinterpret_cast<const float4*>(Qs + hl * S::kStride + c);
+            acc[0] = fmaf(q4.x, r4.x, acc[0]);
+            acc[1] = fmaf(q4.y, r4.y, acc[1]);
+            acc[2] = fmaf(q4.z, r4.z, acc[2]);
+            acc[3] = fmaf(q4.w, r4.w, acc[3]);
         }
-        __syncthreads();
-        if (tid < kHeads) {                            // online softmax, one thread per head
-            float* srow = Ss + tid * kSsStride;
-            const float m_old = m_s[tid];
-            float mx = -INFINITY;
-            for (int j = 0; j < kTile; ++j) mx = fmaxf(mx, srow[j]);
-            const float m_new = fmaxf(m_old, mx);
-            float alpha = 1.f, psum = 0.f;
-            for (int j = 0; j < kTile; ++j) {
-                // no finite maximum yet: rows without weight, or a NaN logit to pass on
-                const float p = srow[j] == -INFINITY ? 0.f : expf(srow[j] - m_new);
-                srow[j] = p;
-                psum += p;
-            }
-            if (m_new != -INFINITY) alpha = expf(m_old - m_new);
-            l_s[tid] = l_s[tid] * alpha + psum;
-            m_s[tid] = m_new;
-            alpha_s[tid] = alpha;
-        }
-        __syncthreads();
-        {                                              // rescale and accumulate P . R_latent
-            const float a = alpha_s[oh];
+        const float z = row_at[j] >= 0 ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale : -INFINITY;
+        float mx = z;
 #pragma unroll
-            for (int i = 0; i < kLatent / 4; ++i) o[i] *= a;
-            for (int j = 0; j < nrows; ++j) {
-                const float p = Ss[oh * kSsStride + j];
-                const float* rrow = Rs + j * S::kRStride + 4 * ocg;
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float m_new = fmaxf(m, mx);
+        // no maximum yet: rows without weight, or a NaN logit to pass on
+        const float p = z == -INFINITY ? 0.f : expf(z - m_new);
+        const float alpha = m_new == -INFINITY ? 1.f : expf(m - m_new);
+        float sum = p;
 #pragma unroll
-                for (int i = 0; i < kLatent / 16; ++i) {
-                    const float4 r4 = *reinterpret_cast<const float4*>(rrow + 16 * i);
-                    o[4 * i + 0] = fmaf(p, r4.x, o[4 * i + 0]);
-                    o[4 * i + 1] = fmaf(p, r4.y, o[4 * i + 1]);
-                    o[4 * i + 2] = fmaf(p, r4.z, o[4 * i + 2]);
-                    o[4 * i + 3] = fmaf(p, r4.w, o[4 * i + 3]);
-                }
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l = l * alpha + sum;
+        m = m_new;
+        Ps[hl * kTile + j] = p;                        // read by this half warp alone
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kLatent / 16; ++i) o[i] *= alpha;
+        for (int r = 0; r < nrows; ++r) {
+            const float w = Ps[hl * kTile + r];
+            const float* rrow = Rs + r * S::kStride + 4 * j;
+#pragma unroll
+            for (int i = 0; i < kLatent / 64; ++i) {
+                const float4 r4 = *reinterpret_cast<const float4*>(rrow + 64 * i);
+                o[4 * i + 0] = fmaf(w, r4.x, o[4 * i + 0]);
+                o[4 * i + 1] = fmaf(w, r4.y, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(w, r4.z, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(w, r4.w, o[4 * i + 3]);
             }
         }
         __syncthreads();
     }
-    __syncthreads();
 
-    const float m = m_s[oh], l = l_s[oh];
     const bool last = n_split == 1;
     const float inv = last ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-    const int64_t part = q * n_split + split;
-    float* dst = (last ? out + (q * kHeads + oh) * (int64_t)kLatent
-                       : part_o + (part * kHeads + oh) * (int64_t)kLatent) + 4 * ocg;
+    float* dst = (last ? out + (q * kHeads + h) * (int64_t)kLatent
+                       : part_o + (part * kHeads + h) * (int64_t)kLatent) + 4 * j;
 #pragma unroll
-    for (int i = 0; i < kLatent / 16; ++i)
-        *reinterpret_cast<float4*>(dst + 16 * i) =
+    for (int i = 0; i < kLatent / 64; ++i)
+        *reinterpret_cast<float4*>(dst + 64 * i) =
             make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-    if (ocg == 0) {
+    if (j == 0) {
         if (last) {
-            if (lse != nullptr) lse[q * kHeads + oh] = l == 0.f ? -INFINITY : m + logf(l);
+            if (lse != nullptr) lse[q * kHeads + h] = l == 0.f ? -INFINITY : m + logf(l);
         } else {
-            part_ml[(part * kHeads + oh) * 2 + 0] = m;
-            part_ml[(part * kHeads + oh) * 2 + 1] = l;
+            part_ml[(part * kHeads + h) * 2 + 0] = m;
+            part_ml[(part * kHeads + h) * 2 + 1] = l;
         }
     }
 }
@@ -220,9 +200,10 @@ void paged_rows(const Shape& sh, const BatchDev& b, int64_t* main_rows, int64_t*
     if (*main_rows < 1 || *main_rows > *max_rows) *main_rows = *max_rows;
 }
 
-// CUDA-core splits: enough CTAs to fill the GPU about twice, at least one tile each.
+// CUDA-core splits: with the four head groups enough CTAs to fill the GPU four
+// times (three are resident per multiprocessor), at least one tile each.
 void plan_splits_simt(int32_t n_q, int64_t max_rows, int32_t* rows_per_split, int32_t* n_split) {
-    const int64_t target = 2 * (int64_t)sm_count();
+    const int64_t target = 4 * (int64_t)sm_count() / (kHeads / kGroup);
     const int64_t tiles = (max_rows + kTile - 1) / kTile;
     int64_t splits = (target + n_q - 1) / n_q;
     if (splits > tiles) splits = tiles;
@@ -241,9 +222,9 @@ cudaError_t launch_t(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
     auto kern = paged_mla_simt<FMT, W>;
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)S::kTotal);
     if (e != cudaSuccess) return e;
-    e = launch_plain(kern, dim3((unsigned)n_split, (unsigned)b.n_q), dim3(kThreads), S::kTotal, st,
-                     b, pc, sh.scale, static_cast<const float*>(q_abs), idx, n_sel,
-                     sh.index_row_width(), rps, n_split, out, lse, part_o, part_ml, err);
+    e = launch_pdl(kern, dim3((unsigned)n_split, (unsigned)b.n_q, kHeads / kGroup), dim3(kThreads),
+                   S::kTotal, st, b, pc, sh.scale, static_cast<const float*>(q_abs), idx, n_sel,
+                   sh.index_row_width(), rps, n_split, out, lse, part_o, part_ml, err);
     if (e != cudaSuccess || n_split == 1) return e;
     return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st);
 }

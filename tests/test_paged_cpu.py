@@ -138,29 +138,45 @@ def test_sizes_and_plans(lib):
     assert dsa.dsa_plan(dsa.make_shape(), _batch(), dsa.OP_PAGE_PLAN)["kernel_launches"] >= 1
 
 
-def test_binding_checks_types_and_sizes(lib):
-    """The binding refuses tensors whose element type or size the call fixes,
-    before it touches a device."""
+def test_binding_checks_types_and_sizes(lib, monkeypatch):
+    """The binding refuses tensors whose element type, size or device the call
+    fixes, before it touches a device."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     sh, b, pg = dsa.make_shape(), _batch(), _pages(64, 2, 4)
     z = torch.zeros
     codes, scales = z(2, 64, 576, dtype=torch.uint8), z(2, 2, dtype=torch.uint8)
+    i64, i32 = torch.int64, torch.int32
     with pytest.raises(ValueError, match="rows is torch.bfloat16"):
-        dsa.dsa_cache_append(sh, b, pg, z(1, 576), z(1, dtype=torch.int64), codes, scales, None)
-    with pytest.raises(ValueError, match="rows holds"):
-        dsa.dsa_cache_append(sh, b, pg, z(1, 512), z(1, dtype=torch.int64), codes, scales, None)
-    with pytest.raises(ValueError, match="slots holds"):
-        dsa.dsa_cache_append(sh, b, pg, z(1, 576), z(0, dtype=torch.int64), codes, scales, None)
-    with pytest.raises(ValueError, match="block_table holds"):
-        dsa.dsa_paged_mla_attn(sh, b, pg, z(1, 64, 576), codes, scales, z(3, dtype=torch.int32),
-                               None, None, None, None, None)
-    with pytest.raises(ValueError, match="codes holds"):
-        dsa._codes(pg, z(2, 64, 512, dtype=torch.uint8), 576)
-    with pytest.raises(ValueError, match="scales holds"):
-        dsa._scales(sh, pg, z(2, 1, dtype=torch.uint8))
-    lens = z(3, dtype=torch.int64)
-    with pytest.raises(ValueError, match="row_off holds"):
-        dsa.dsa_page_plan(pg, lens, lens, lens, z(2, dtype=torch.int32), z(1, dtype=torch.int32),
-                          z(3, 4, dtype=torch.int32), lens, z(4, dtype=torch.int64), lens, None)
+        dsa.dsa_cache_append(sh, b, pg, z(1, 576), z(1, dtype=i64), codes, scales, None)
+    with pytest.raises(ValueError, match="rows holds at least 576"):
+        dsa.dsa_cache_append(sh, b, pg, z(1, 512, dtype=torch.bfloat16), z(1, dtype=i64), codes, scales,
+                             None)
+    with pytest.raises(ValueError, match="CUDA tensors only"):
+        dsa.dsa_cache_append(sh, b, pg, z(1, 576, dtype=torch.bfloat16), z(1, dtype=i64), codes, scales,
+                             None)
+    with pytest.raises(ValueError, match="q_abs is torch.bfloat16"):
+        dsa.dsa_paged_mla_attn(sh, b, pg, z(1, 64, 576), codes, scales, z(4, dtype=i32), None, None, None,
+                               None, None)
+    with pytest.raises(ValueError, match="slots is missing"):
+        dsa._at(None, i64, 0, 1, "slots")
+    with pytest.raises(ValueError, match="slots holds at least 3"):
+        dsa._at(z(2, dtype=i64), i64, 0, 3, "slots")
+    with pytest.raises(ValueError, match="codes holds 73728 one-byte"):
+        dsa._bytes_at(z(2, 64, 512, dtype=torch.uint8), 0, 73728, "codes")
+    with pytest.raises(ValueError, match="scales holds 4 one-byte"):
+        dsa._bytes_at(z(4, dtype=torch.int16), 0, 4, "scales")
+
+    class OnAnother:                                  # a tensor of a second GPU
+        dtype, is_cuda = i64, True
+        numel = staticmethod(lambda: 8)
+        get_device = staticmethod(lambda: 1)
+        is_contiguous = staticmethod(lambda: True)
+    with pytest.raises(ValueError, match="another device"):
+        dsa._at(OnAnother(), i64, 0, 4, "kv_len")
+    lens = z(3, dtype=i64)
+    with pytest.raises(ValueError, match="n_free is torch.int32"):
+        dsa.dsa_page_plan(pg, lens, lens, lens, z(2, dtype=i32), z(1, dtype=i64), z(3, 4, dtype=i32),
+                          z(4, dtype=i64), z(4, dtype=i64), lens, None)
 
 
 # ------------------------------------------------------------ the reference itself
