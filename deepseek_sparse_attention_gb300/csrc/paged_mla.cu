@@ -15,7 +15,7 @@
 // head's 512 outputs.  Bound by shared-memory reads (a float4 for four
 // multiply-adds); small float32 steps are bound by latency, which is why the
 // heads are spread over CTAs (one query of 256 rows: 27 us with all 64 heads in
-// a CTA and the softmax through shared memory, 13 us so).  Rows whose index or
+// a CTA and the softmax through shared memory, 14 us so).  Rows whose index or
 // page is out of range are zero and take no weight.  Splits of a query are
 // combined by the log-sum-exp merge.
 #include <math.h>
