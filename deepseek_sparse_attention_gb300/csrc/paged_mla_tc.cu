@@ -68,6 +68,7 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kLoaders = 256;
 constexpr int kThreads = kSoftmaxThreads + kLoaders + 32;
 constexpr int kMmaWarp = (kSoftmaxThreads + kLoaders) / 32;
+constexpr int kMergers = kSoftmaxThreads + kLoaders;  // threads of the epilogue and the pair merge
 
 template <int W>
 struct Cfg {
@@ -204,25 +205,40 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         const float* m1p = cl.map_shared_rank(m_fin, rank ^ 1);
         const float* l1p = cl.map_shared_rank(l_fin, rank ^ 1);
         float4* o4 = reinterpret_cast<float4*>(out);
-        constexpr int kC4 = kLatent / 4;
-        for (int i = threadIdx.x; i < (kHeads / 2) * kC4; i += blockDim.x) {
-            const int h = (kHeads / 2) * rank + i / kC4, c4 = i % kC4;
-            const float l0 = l_fin[h], l1 = l1p[h];
-            const float M = fmaxf(m_fin[h], m1p[h]);  // kNoMax where there was no row
-            const float f0 = l0 != 0.f ? exp2f(m_fin[h] - M) : 0.f;
-            const float f1 = l1 != 0.f ? exp2f(m1p[h] - M) : 0.f;
-            const float L = f0 + f1;
-            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (L != 0.f) {
-                const float inv = 1.f / L;
-                const float4 a = l0 != 0.f ? st0[h * kC4 + c4] : r;
-                const float4 c = l1 != 0.f ? st1[h * kC4 + c4] : r;
-                r = make_float4((a.x * f0 + c.x * f1) * inv, (a.y * f0 + c.y * f1) * inv,
-                                (a.z * f0 + c.z * f1) * inv, (a.w * f0 + c.w * f1) * inv);
+        constexpr int kC4 = kLatent / 4, kEach = (kHeads / 2) * kC4 / kMergers;
+        static_assert(kEach * kMergers == (kHeads / 2) * kC4, "a whole number each");
+        if (threadIdx.x < kMergers) {
+            // all of a thread's reads from the other CTA are in flight at once
+            // (one after the other the merge took 8 us)
+            float4 theirs[kEach];
+            float f0[kEach], f1[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kMergers, h = (kHeads / 2) * rank + i / kC4;
+                theirs[k] = st1[h * kC4 + i % kC4];
+                f0[k] = m1p[h];
+                f1[k] = l1p[h];
             }
-            o4[(q * kHeads + h) * kC4 + c4] = r;
-            if (c4 == 0 && lse != nullptr)
-                lse[q * kHeads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kMergers, h = (kHeads / 2) * rank + i / kC4, c4 = i % kC4;
+                const float l0 = l_fin[h], l1 = f1[k];
+                const float M = fmaxf(m_fin[h], f0[k]);  // kNoMax where there was no row
+                const float g0 = l0 != 0.f ? exp2f(m_fin[h] - M) : 0.f;
+                const float g1 = l1 != 0.f ? exp2f(f0[k] - M) : 0.f;
+                const float L = g0 + g1;
+                float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (L != 0.f) {
+                    const float inv = 1.f / L;
+                    const float4 a = l0 != 0.f ? st0[h * kC4 + c4] : r;
+                    const float4 c = l1 != 0.f ? theirs[k] : r;
+                    r = make_float4((a.x * g0 + c.x * g1) * inv, (a.y * g0 + c.y * g1) * inv,
+                                    (a.z * g0 + c.z * g1) * inv, (a.w * g0 + c.w * g1) * inv);
+                }
+                o4[(q * kHeads + h) * kC4 + c4] = r;
+                if (c4 == 0 && lse != nullptr)
+                    lse[q * kHeads + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            }
         }
         cl.sync();                                    // the peer's reads of this stage are done
     };
@@ -285,32 +301,6 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         e1 = entry(1, end);
         e2 = entry(2, end);
     }
-    int64_t ns = dense ? 0 : n_sel[q];
-    QueryInfo qi;
-    const bool known = query_info(b, q, qi, err, /*where=*/34);
-    if (dense) ns = known ? qi.L : 0;
-    else ns = ns < 0 ? 0 : (ns > idx_width ? idx_width : ns);
-    const int64_t j1 = j0 + rows_per_split < ns ? j0 + rows_per_split : ns;
-    if (!known || j0 >= j1) {
-        if (pair) {                                   // no weight from this half
-            __syncthreads();
-            if (known) pair_merge();
-        } else if (n_split == 1) {                    // no rows: out = 0, lse = -inf
-            if (known) {
-                for (int i = threadIdx.x; i < kHeads * kLatent; i += blockDim.x)
-                    out[q * kHeads * kLatent + i] = 0.f;
-                if (lse != nullptr && threadIdx.x < kHeads) lse[q * kHeads + threadIdx.x] = -INFINITY;
-            }
-        } else if (threadIdx.x < kHeads && half == 0) {  // no weight in the merge
-            const int64_t part = q * n_split + split;
-            part_ml[(part * kHeads + threadIdx.x) * 2] = -INFINITY;
-            part_ml[(part * kHeads + threadIdx.x) * 2 + 1] = 0.f;
-        }
-        leave();
-        return;
-    }
-    const int n_tiles = (int)((j1 - j0 + kTileRows - 1) / kTileRows);
-
     // The query as f16: loaded by every warp but the MMA warp, times 2^k with
     // its largest element in [2^14, 2^15), in the 128-byte swizzle.  Head
     // 32 i + 16 p + k lies in row 32 i + p + 2 k: a 16x64b load of 32 columns of
@@ -364,6 +354,47 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         mbar_arrive(q_full);
     };
 
+    // The query, and -- in a decode batch, where query q should be sequence q's --
+    // the pages of the first two tiles' entries, are requested with the batch's
+    // offsets rather than after them.
+    uint4 qv[kQPer];
+    if (warp < kMmaWarp) load_query(qv);
+    const int64_t guess_row = b.n_q == b.n_seq ? q : 0;
+    auto page_guess = [&](int32_t r) -> int32_t {
+        const int64_t c = r >> pc.pg.shift;          // any entry of the row if r is none
+        return pc.block_table[guess_row * pc.pg.table_ld + (r >= 0 && c < pc.pg.table_ld ? c : 0)];
+    };
+    int32_t p0 = 0, p1 = 0;
+    if (loader) {
+        p0 = page_guess(e0);
+        p1 = page_guess(e1);
+    }
+    int64_t ns = dense ? 0 : n_sel[q];
+    QueryInfo qi;
+    const bool known = query_info(b, q, qi, err, /*where=*/34);
+    if (dense) ns = known ? qi.L : 0;
+    else ns = ns < 0 ? 0 : (ns > idx_width ? idx_width : ns);
+    const int64_t j1 = j0 + rows_per_split < ns ? j0 + rows_per_split : ns;
+    if (!known || j0 >= j1) {
+        if (pair) {                                   // no weight from this half
+            __syncthreads();
+            if (known) pair_merge();
+        } else if (n_split == 1) {                    // no rows: out = 0, lse = -inf
+            if (known) {
+                for (int i = threadIdx.x; i < kHeads * kLatent; i += blockDim.x)
+                    out[q * kHeads * kLatent + i] = 0.f;
+                if (lse != nullptr && threadIdx.x < kHeads) lse[q * kHeads + threadIdx.x] = -INFINITY;
+            }
+        } else if (threadIdx.x < kHeads && half == 0) {  // no weight in the merge
+            const int64_t part = q * n_split + split;
+            part_ml[(part * kHeads + threadIdx.x) * 2] = -INFINITY;
+            part_ml[(part * kHeads + threadIdx.x) * 2 + 1] = 0.f;
+        }
+        leave();
+        return;
+    }
+    const int n_tiles = (int)((j1 - j0 + kTileRows - 1) / kTileRows);
+
     if (loader) {                                                     // ---- loads
         regs_inc<kLoaderRegs>();
         // A row's way to its codes is three dependent reads (list entry, block
@@ -403,15 +434,12 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
         };
         Tile x;
-        int32_t p1;
-        {
-            uint4 v[kQPer];
-            load_query(v);
-            const int32_t p0 = page_of_row(e0);
+        if (qi.seq != guess_row) {
+            p0 = page_of_row(e0);
             p1 = page_of_row(e1);
-            load(x, 0, e0, p0);
-            store_query(v);
         }
+        load(x, 0, e0, p0);
+        store_query(qv);
         bool ok = true;
         auto step = [&](Tile& x, int t) {
             const int buf = t & 1;
@@ -559,11 +587,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         // lane l of warps wq and wq + 4 takes row 16 wq + (l >> 2) + 8 (l & 1) and
         // 16 heads.
         regs_dec<kSoftmaxRegs>();
-        {
-            uint4 v[kQPer];
-            load_query(v);
-            store_query(v);
-        }
+        store_query(qv);
         const int wq = warp & 3;
         const int p = (lane >> 1) & 1;
         const int srow = 16 * wq + (lane >> 2) + 8 * (lane & 1);
@@ -769,32 +793,35 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         }
     }
 
-    // ---- epilogue, warps 0-7: O^T read out of TMEM, times 2^e_base / l
-    if (warp < 8) {
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+    // ---- epilogue, warps 0-15: O^T read out of TMEM, times 2^e_base / l
+    if (warp < kMmaWarp) {
+        asm volatile("bar.sync 3, %0;" ::"n"(kMergers) : "memory");
         tc_fence_after();
-        const int wq = warp & 3, hb = 32 * (warp >> 2);      // this warp's heads
+        const int wq = warp & 3, hb = 16 * (warp >> 2);      // this warp's heads
         const uint32_t lane_addr = tmem_base + ((uint32_t)(32 * wq) << 16);
         const bool final_out = n_split == 1;
         const int64_t part = q * n_split + split;
         float* dst = pair ? stage
                           : (final_out ? out + q * kHeads * kLatent : part_o + part * kHeads * kLatent);
+        float inv[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) inv[e] = inv_fin[hb + e];
         // lane 32 wq + lane of block i holds latent column 128 i + 32 wq + lane
 #pragma unroll
         for (int i = 0; i < kLatentBlocks; ++i) {
             if (!owns(i)) continue;
             const int c = 128 * i + 32 * wq + lane;
-            float v[32];
+            float v[16];
             if (i < C::kWide) {                      // hi and lo halves
-                float u[32];
-                tmem_ld_32cols_x2(lane_addr + C::o_col(i) + hb, lane_addr + C::o_col(i) + 64 + hb, v, u);
+                float u[16];
+                tmem_ld_16cols_x2(lane_addr + C::o_col(i) + hb, lane_addr + C::o_col(i) + 64 + hb, v, u);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] += u[e];
+                for (int e = 0; e < 16; ++e) v[e] += u[e];
             } else {
-                tmem_ld_32cols(lane_addr + C::o_col(i) + hb, v);
+                tmem_ld_16cols(lane_addr + C::o_col(i) + hb, v);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) dst[(hb + e) * kLatent + c] = v[e] * inv_fin[hb + e];
+            for (int e = 0; e < 16; ++e) dst[(hb + e) * kLatent + c] = v[e] * inv[e];
         }
         if (threadIdx.x < kHeads && !pair && half == 0) {
             const int h = threadIdx.x;
