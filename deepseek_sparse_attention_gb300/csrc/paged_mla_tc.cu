@@ -16,7 +16,7 @@
 //
 // One CTA takes a range of one query's rows in tiles of 64, two f16 row buffers
 // deep:
-//   warps 8-15  load the tile's rows through the block table, a tile ahead in
+//   warps 8-15  load the tile's rows through the block table, two tiles ahead in
 //               registers, widen them and store them in the 128-byte swizzle.  A
 //               buffer is handed over in pieces of 128 columns, a pair of warps
 //               to each: a piece is refilled as soon as the value product has
@@ -398,8 +398,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     if (loader) {                                                     // ---- loads
         regs_inc<kLoaderRegs>();
         // A row's way to its codes is three dependent reads (list entry, block
-        // table, codes and scales): the entries are read three tiles ahead, the
-        // table two, the codes one.
+        // table, codes and scales): the entries are read four tiles ahead, the
+        // table three, the codes two (a tile's time with the codes one ahead: 4,170
+        // cycles, of which 970 waited for them).
         // Every read is made, of some row where there is none to read, and what it
         // is worth is decided where it is used: a read within a branch is waited
         // for where the branch ends.
@@ -409,7 +410,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             return r >= 0 && r < qi.L && (r >> pc.pg.shift) < pc.pg.table_ld;
         };
         auto page_of_row = [&](int32_t r) -> int32_t { return table[in_table(r) ? r >> pc.pg.shift : 0]; };
-        const int r8 = lane >> 2, k4 = lane & 3;     // row of a group of eight, quarter of its piece
+        // row of a group of eight and quarter of its piece: eight lanes that store
+        // together have four rows and two quarters of a line, eight places of it
+        const int r8 = ((lane >> 1) & 3) | ((lane >> 2) & 4), k4 = (lane & 1) | ((lane >> 2) & 2);
         struct Tile {
             uint32_t raw[4][8];                      // 32 codes of rows rows0 + 8 i + r8
             uint4 rope;                              // 16 rope codes of row rows0 + 8 piece + r8
@@ -433,13 +436,17 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             x.b0 = __ldg(pc.scales + pg * kParts);
             x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
         };
-        Tile x;
+        Tile xa, xb;
         if (qi.seq != guess_row) {
             p0 = page_of_row(e0);
             p1 = page_of_row(e1);
         }
-        load(x, 0, e0, p0);
+        load(xa, 0, e0, p0);
         store_query(qv);
+        load(xb, 1, e1, p1);
+        p0 = page_of_row(e2);
+        e0 = e2;                                     // tile 2: entry and page
+        e1 = entry(3, j1);
         bool ok = true;
         auto step = [&](Tile& x, int t) {
             const int buf = t & 1;
@@ -451,24 +458,25 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const bool in = (x.has >> lane) & 1u;
             if (piece == 0) rinfo[buf * kTileRows + rows0 + lane] = in ? kHasRow | (x.b1 << 8) | x.b0 : 0u;
             if (piece == 0 && !in && in_list(t)) record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
-            // half of a 64-column block's line: four 16-byte pieces, in an order
-            // that keeps eight lanes on eight of the line's places
+            if (x.has != 0xffffffffu) {              // zeros for rows that do not exist
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((x.has >> (8 * i + r8)) & 1u) continue;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x.raw[i][j] = 0;
+                }
+                if (!((x.has >> (8 * piece + r8)) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
+            }
+            // half of a 64-column block's line: four 16-byte pieces
             uint8_t* dst = rbuf + (2 * piece + (k4 >> 1)) * kBlock + (rows0 + r8) * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool row_in = (x.has >> (8 * i + r8)) & 1u;
-                uint4 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint2 lo = codes_f16<FMT>(row_in ? x.raw[i][2 * j] : 0u);
-                    const uint2 hi = codes_f16<FMT>(row_in ? x.raw[i][2 * j + 1] : 0u);
-                    v[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    const uint2 lo = codes_f16<FMT>(x.raw[i][2 * j]), hi = codes_f16<FMT>(x.raw[i][2 * j + 1]);
+                    *reinterpret_cast<uint4*>(dst + 8 * i * 128 + (((4 * (k4 & 1) + j) ^ r8) << 4)) =
+                        make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(dst + 8 * i * 128 +
-                                              (((4 * (k4 & 1) + (j ^ (k4 & 2))) ^ r8) << 4)) =
-                        k4 & 2 ? v[j ^ 2] : v[j];
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -477,9 +485,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 // the rope block held tile t - 2's W_hi, which all of its products read
                 if (t >= 2) ok = mbar_wait(&freed[buf * kLatentBlocks + kLatentBlocks - 1], phase, kWaitNs);
                 if (!ok) return;
-                const bool row_in = (x.has >> (8 * piece + r8)) & 1u;
-                const uint2 a0 = codes_f16<FMT>(row_in ? x.rope.x : 0u), a1 = codes_f16<FMT>(row_in ? x.rope.y : 0u);
-                const uint2 a2 = codes_f16<FMT>(row_in ? x.rope.z : 0u), a3 = codes_f16<FMT>(row_in ? x.rope.w : 0u);
+                const uint2 a0 = codes_f16<FMT>(x.rope.x), a1 = codes_f16<FMT>(x.rope.y);
+                const uint2 a2 = codes_f16<FMT>(x.rope.z), a3 = codes_f16<FMT>(x.rope.w);
                 uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + 8 * piece + r8) * 128;
                 *reinterpret_cast<uint4*>(rope + (((2 * k4) ^ r8) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
                 *reinterpret_cast<uint4*>(rope + (((2 * k4 + 1) ^ r8) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
@@ -488,13 +495,16 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + kLatentBlocks]);
             }
             // the codes last: a wait for a load can be one for newer loads too
-            const int32_t r = e1, page = p1;
-            p1 = page_of_row(e2);
-            e1 = e2;
-            e2 = entry(t + 3, j1);
-            load(x, t + 1, r, page);
+            const int32_t r = e0, page = p0;
+            p0 = page_of_row(e1);
+            e0 = e1;
+            e1 = entry(t + 4, j1);
+            load(x, t + 2, r, page);
         };
-        for (int t = 0; t < n_tiles && ok; ++t) step(x, t);
+        for (int t = 0; t < n_tiles && ok; t += 2) {
+            step(xa, t);
+            if (t + 1 < n_tiles && ok) step(xb, t + 1);
+        }
         if (!ok && threadIdx.x == kSoftmaxThreads) record_error(err, kDevTimeout, (int32_t)q, /*where=*/35);
     } else if (warp == kMmaWarp) {                                    // ---- MMA issue
         if (elect_one()) {
