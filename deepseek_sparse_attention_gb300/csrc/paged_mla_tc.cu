@@ -63,6 +63,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 // A running maximum is raised (and O^T rescaled) only when it is exceeded by more
 // than this, in log2: w stays below 2^14, within f16.
 constexpr float kSlack = 14.f;
+// Tiles whose values are summed in TMEM before the sum moves to memory (to the
+// CTA's own part of the output or of the partials).  The tensor cores cut each
+// accumulation off instead of rounding it, so a sum's error grows with the tiles
+// in it: relative to the output, against 64 bits, 0.3e-6 for 2 tiles, 1.2e-6 for
+// 16, 1.6e-6 for 32, where float32 sums have 0.5e-6.  Moved every 11 tiles it is
+// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows took 602 us without,
+// 634 us with a move every 16 tiles and 670 us with one every 11.
+constexpr int kFlushTiles = 11;
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any row
 constexpr int kSoftmaxThreads = 256;
 constexpr int kLoaders = 256;
@@ -95,7 +103,8 @@ struct Cfg {
     static constexpr uint32_t kOffL = kOffRow + 2 * 64 * 4;     // [64] float
     static constexpr uint32_t kOffM = kOffL + 64 * 4;           // [64] float
     static constexpr uint32_t kOffMs = kOffM + 64 * 4;          // [64] float
-    static constexpr uint32_t kOffMisc = kOffMs + 64 * 4;
+    static constexpr uint32_t kOffMf = kOffMs + 64 * 4;         // [64] float
+    static constexpr uint32_t kOffMisc = kOffMf + 64 * 4;
     static constexpr uint32_t kSmemBytes = kOffMisc + 64 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     __host__ __device__ static constexpr uint32_t off_p(int b) {
@@ -176,6 +185,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     float* l_fin = reinterpret_cast<float*>(smem + C::kOffL);
     float* m_fin = reinterpret_cast<float*>(smem + C::kOffM);
     float* inv_fin = reinterpret_cast<float*>(smem + C::kOffMs);     // output factors
+    float* m_moved = reinterpret_cast<float*>(smem + C::kOffMf);     // maxima that the moved sums go by
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     uint32_t* q_max = tmem_slot + 1;
     uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
@@ -394,6 +404,12 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         return;
     }
     const int n_tiles = (int)((j1 - j0 + kTileRows - 1) / kTileRows);
+    const int64_t part = q * n_split + split;
+    // Where this CTA's output goes, unnormalised sums of its first tiles before it
+    // (a pair's outputs stay in shared memory; its sums go to the partials).
+    auto sums_at = [&]() {
+        return n_split == 1 ? out + q * kHeads * kLatent : part_o + part * kHeads * kLatent;
+    };
 
     if (loader) {                                                     // ---- loads
         regs_inc<kLoaderRegs>();
@@ -558,7 +574,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     const uint64_t d_a = sdesc_sw128(base + C::kOffR + bv * C::kBufBytes, kBlock, 1024);
                     const uint64_t d_both = sdesc_sw128(p_hi, p_lo - p_hi, 1024);
                     const uint64_t d_hi = sdesc_sw128(p_hi, 1024, 1024), d_lo = sdesc_sw128(p_lo, 1024, 1024);
-                    const uint32_t acc = next_v > 0 ? 1u : 0u;
+                    const uint32_t acc = next_v % kFlushTiles != 0 ? 1u : 0u;
 #pragma unroll
                     for (int i = 0; i < kLatentBlocks; ++i) {
                         if (owns(i)) {
@@ -609,6 +625,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         float l_part[16];                            // sums of p over this lane's rows
 #pragma unroll
         for (int e = 0; e < 16; ++e) l_part[e] = 0.f;
+        constexpr int kOBlocks = kLatentBlocks + C::kWide;   // O^T's blocks of 64 columns
         float* alpha_s = l_fin;                      // rescale factors
         int e_base = 0;                              // an exponent of the query's rows, taken off theirs
         float m[16];                                 // the heads' running maxima
@@ -618,6 +635,57 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         uint32_t vote_phase = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int bf = t & 1;
+            if (t > 0 && t % kFlushTiles == 0) {
+                // O^T moves to memory, as multiples of 2^m of the move that began a
+                // head's sum: added to it, or beginning it anew where m has grown so
+                // far that what is there no longer counts.
+                const int pb = (t - 1) & 1;
+                if (ok) ok = mbar_wait(&freed[pb * kLatentBlocks + kLatentBlocks - 1],
+                                       (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
+                tc_fence_after();
+                if (threadIdx.x < kHeads) {
+                    const int h = threadIdx.x;
+                    const float grown = m_fin[h] - m_moved[h];
+                    const bool anew = t == kFlushTiles || grown > 80.f;
+                    if (anew) m_moved[h] = m_fin[h];
+                    alpha_s[h] = anew ? 1.f : exp2f(grown);
+                    const uint32_t mask = __ballot_sync(0xffffffffu, anew);
+                    if (lane == 0) raised_s[warp] = mask;
+                }
+                softmax_sync();
+                const uint32_t mask = raised_s[warp >> 2];
+                float* const sums = sums_at();
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    const int h = 32 * (warp >> 2) + 8 * g;
+#pragma unroll
+                    for (int j = 0; j < kOBlocks; j += 4) {
+                        uint32_t a[4];               // the last one again past the end
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = lane_addr + C::kOCol + 64 * min(j + i, kOBlocks - 1) + h;
+                        float v[32];
+                        tmem_ld_4x8cols(a, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = j + i;     // hi and lo of the wide blocks, then the others
+                            const bool wide = k < 2 * C::kWide;
+                            const int blk = wide ? k >> 1 : k - C::kWide;
+                            if (k >= kOBlocks || (wide && (k & 1)) || !owns(blk)) continue;
+                            float* dst = sums + h * kLatent + 128 * blk + 32 * wq + lane;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const float o = wide ? v[8 * i + c] + v[(8 * i + c + 8) & 31] : v[8 * i + c];
+                                if ((mask >> (8 * g + c)) & 1u) dst[c * kLatent] = o;
+                                else atomicAdd(dst + c * kLatent, o * alpha_s[h + c]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) m[e] = m_fin[hb + e];   // not kept in registers meanwhile
+            }
             if (ok) ok = mbar_wait(s_full, (uint32_t)(t & 1), kWaitNs);
             tc_fence_after();
             const uint32_t info = rinfo[bf * kTileRows + srow];
@@ -704,13 +772,12 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 for (int e = 0; e < 16; ++e) l_part[e] *= alpha_s[hb + e];
                 have_max = have_max || (raised_s[0] | raised_s[1]) != 0;
                 const uint32_t mask = raised_s[warp >> 2];
-                if (t > 0 && mask != 0) {            // their columns of O^T follow
+                if (t % kFlushTiles != 0 && mask != 0) {   // their columns of O^T follow
                     const int pb = (t - 1) & 1;
                     if (ok) ok = mbar_wait(&freed[pb * kLatentBlocks + kLatentBlocks - 1],
                                            (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
                     tc_fence_after();
                     // eight heads at a time, in each of O^T's blocks of 64 columns
-                    constexpr int kOBlocks = kLatentBlocks + C::kWide;
 #pragma unroll 1
                     for (int g = 0; g < 4; ++g) {
                         if (((mask >> (8 * g)) & 255u) == 0) continue;
@@ -798,6 +865,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             for (int r = 0; r < kTileRows; ++r) s4[r & 3] += lsc[r * (kHeads + 1) + h];
             const float l = (s4[0] + s4[1]) + (s4[2] + s4[3]);
             inv_fin[h] = l == 0.f ? 0.f : exp2i(e_base) / l;
+            m_moved[h] = exp2f(m_moved[h] - m_fin[h]);       // what the moved sums are worth
             m_fin[h] = l == 0.f ? kNoMax : m_fin[h] + log2f(l);
             l_fin[h] = l == 0.f ? 0.f : 1.f;
         }
@@ -809,10 +877,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         tc_fence_after();
         const int wq = warp & 3, hb = 16 * (warp >> 2);      // this warp's heads
         const uint32_t lane_addr = tmem_base + ((uint32_t)(32 * wq) << 16);
-        const bool final_out = n_split == 1;
-        const int64_t part = q * n_split + split;
-        float* dst = pair ? stage
-                          : (final_out ? out + q * kHeads * kLatent : part_o + part * kHeads * kLatent);
+        const bool final_out = n_split == 1, moved = n_tiles > kFlushTiles;
+        float* const sums = sums_at();
+        float* dst = pair ? stage : sums;
         float inv[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) inv[e] = inv_fin[hb + e];
@@ -829,6 +896,13 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 for (int e = 0; e < 16; ++e) v[e] += u[e];
             } else {
                 tmem_ld_16cols(lane_addr + C::o_col(i) + hb, v);
+            }
+            if (moved) {
+                float u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __ldcg(sums + (hb + e) * kLatent + c);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = fmaf(u[e], m_moved[hb + e], v[e]);
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) dst[(hb + e) * kLatent + c] = v[e] * inv[e];

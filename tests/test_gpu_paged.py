@@ -548,6 +548,25 @@ def test_attention_over_the_scales_range(spread, dtype):
     case.check(out, lse)
 
 
+@pytest.mark.parametrize("rope", [64, 0])
+@pytest.mark.parametrize("n_q", [160, 70])
+@pytest.mark.parametrize("spread", [1.0, 40.0])
+def test_attention_of_long_lists_whose_logits_climb(spread, n_q, rope):
+    """One or two CTAs of many tiles to a query; a head's rows from its lowest
+    logit to its highest (with the large spread by far more than 2^80), another
+    head's the other way round."""
+    c = AttnCase(19, [2100], [n_q], rope=rope, spread=spread, top_k=1990)
+    some = [0, n_q // 2, n_q - 1]
+    for k, i in enumerate(some):
+        rows, _ = c.rows_of(i)
+        n = c.n_sel[i]
+        z = c.q_abs[i, 7 * k].double().numpy() @ rows[c.idx[i, :n]].T
+        c.idx[i, :n] = c.idx[i, :n][np.argsort(z if k < 2 else -z)]
+    out, lse, code = c.call()
+    assert code == 0
+    c.check(out, lse, some)
+
+
 def test_attention_any_order_and_the_same_row_twice():
     case = AttnCase(15, [600, 300], top_k=256)
     rng = np.random.default_rng(1)
