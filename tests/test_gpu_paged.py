@@ -531,6 +531,15 @@ def test_attention_dense_over_a_long_sequence(fmt):
     case.check(out, lse)
 
 
+@pytest.mark.parametrize("dense", [True, False])
+def test_attention_of_uneven_lengths(dense):
+    """Splits planned for the rows of all sequences together."""
+    c = AttnCase(20, [9001, 3, 640, 65, 1, 2100], dense=dense, top_k=900)
+    out, lse, code = c.call()
+    assert code == 0
+    c.check(out, lse)
+
+
 def test_attention_with_the_kpool_tail():
     case = AttnCase(9, [2054, 2052, 40], top_k=2048, kpool=4, rope=0, fmt="s8")
     out, lse, code = case.call()
