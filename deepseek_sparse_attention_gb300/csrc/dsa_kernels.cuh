@@ -184,8 +184,10 @@ cudaError_t launch_stage_inputs(StageSeg a, StageSeg b, const uint32_t* w_src, u
 void plan_attention_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_split,
                            int32_t* n_split);
 size_t sparse_mla_scratch_bytes(const Shape& sh, const BatchDev& b);
+// nan_lse: a weight that is NaN gives a NaN lse (-inf otherwise).
 cudaError_t launch_merge_splits(int32_t n_q, int32_t n_split, const float* part_o,
-                                const float* part_ml, float* out, float* lse, cudaStream_t st);
+                                const float* part_ml, float* out, float* lse, cudaStream_t st,
+                                bool nan_lse = false);
 bool sparse_mla_tc_eligible(const Shape& sh, const BatchDev& b);
 // Splits of whole row tiles sized by main_rows; rows past them (up to
 // max_rows) go to further splits of the same size.

@@ -181,7 +181,8 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
         if (last) {
             if (lse != nullptr) lse[q * kHeads + h] = l == 0.f ? -INFINITY : m + logf(l);
         } else {
-            part_ml[(part * kHeads + h) * 2 + 0] = m;
+            // rows whose logits are all NaN: a split with weight
+            part_ml[(part * kHeads + h) * 2 + 0] = m == -INFINITY && l != 0.f ? 0.f : m;
             part_ml[(part * kHeads + h) * 2 + 1] = l;
         }
     }
@@ -226,7 +227,7 @@ cudaError_t launch_t(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
                    S::kTotal, st, b, pc, sh.scale, static_cast<const float*>(q_abs), idx, n_sel,
                    sh.index_row_width(), rps, n_split, out, lse, part_o, part_ml, err);
     if (e != cudaSuccess || n_split == 1) return e;
-    return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st);
+    return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st, /*nan_lse=*/true);
 }
 
 }  // namespace

@@ -139,16 +139,17 @@ __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
 
-// Maxima of x[0..15] over the 16 lanes that hold the same heads by a halving
+// Maxima of x[0..15] + lift over the 16 lanes that hold the same heads by a halving
 // exchange: at each step a lane keeps half of its values, swaps the other half
 // with its partner across one lane bit and takes the maximum; it ends with that
 // of x[8 b4 + 4 b3 + 2 b2 + b0], b the bits of its lane.
-__device__ __forceinline__ float halving_max(const float (&x)[16], int lane) {
+__device__ __forceinline__ float halving_max(const float (&x)[16], float lift, int lane) {
     float a[8], b[4], c[2];
     const bool h4 = (lane >> 4) & 1, h3 = (lane >> 3) & 1, h2 = (lane >> 2) & 1, h0 = lane & 1;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        a[i] = fmaxf(h4 ? x[i + 8] : x[i], __shfl_xor_sync(0xffffffffu, h4 ? x[i] : x[i + 8], 16));
+        a[i] = fmaxf((h4 ? x[i + 8] : x[i]) + lift,
+                     __shfl_xor_sync(0xffffffffu, (h4 ? x[i] : x[i + 8]) + lift, 16));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         b[i] = fmaxf(h3 ? a[i + 4] : a[i], __shfl_xor_sync(0xffffffffu, h3 ? a[i] : a[i + 4], 8));
@@ -337,7 +338,10 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         for (int i = 0; i < kQPer; ++i) {
             const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx = max(mx, max(u[k] & 0x7fffu, (u[k] >> 16) & 0x7fffu));
+            for (int k = 0; k < 4; ++k) {            // the largest finite one
+                const uint32_t a = u[k] & 0x7fffu, c = (u[k] >> 16) & 0x7fffu;
+                mx = max(mx, max(a < 0x7f80u ? a : 0u, c < 0x7f80u ? c : 0u));
+            }
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
         if (lane == 0) atomicMax(q_max, mx);
@@ -691,8 +695,10 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const uint32_t info = rinfo[bf * kTileRows + srow];
             const bool has = (info & kHasRow) != 0;
             const int e_row = (int)(info & 255u) - 127;
-            if (t == 0) {                            // the first tile's largest
-                const int mx = __reduce_max_sync(0xffffffffu, has ? e_row : -1000);
+            if (t == 0) {
+                // the first tile's largest, but for pages of zeros: their exponent
+                // is the least there is, and p counts relative to e_base
+                const int mx = __reduce_max_sync(0xffffffffu, has && e_row > kScaleExpMin ? e_row : -1000);
                 if (lane == 0 && warp < 4) e_first[wq] = mx;
                 softmax_sync();
                 const int em = max(max(e_first[0], e_first[1]), max(e_first[2], e_first[3]));
@@ -703,6 +709,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             float fa = has ? c2 * e8m0(info & 255u) : 0.f;
             if (fa > 3.4028234e38f) fa = 3.4028234e38f;
             const float ev = has ? (float)(e_row - e_base) : -INFINITY;
+            // a row of so small a scale counts for the maximum as if it were 2^-96,
+            // for p = 2^(x - m - ev) to stay within float32
+            const float lift = has ? fmaxf(-96.f - ev, 0.f) : 0.f;
             float x[16];                             // x[k]: head hb + k
             if constexpr (kParts == 2) {
                 float fb = has ? c2 * e8m0((info >> 8) & 255u) : 0.f;
@@ -729,7 +738,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     x[e] -= m[e];
                     top = fmaxf(top, x[e]);
                 }
-                const bool any = __any_sync(0xffffffffu, top > kSlack);
+                const bool any = __any_sync(0xffffffffu, top + lift > kSlack);
                 if (lane == 0) {
                     if (any) vote[t % 3] = 1;
                     mbar_arrive(votes);
@@ -747,7 +756,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 }
             }
             if (raise) {
-                const float mx = halving_max(x, lane);
+                const float mx = halving_max(x, lift, lane);
                 // in the block that W_hi takes below, free once the scores are formed
                 int* red = reinterpret_cast<int*>(smem + C::off_p(bf));
                 red[wq * kHeads + hb + ((lane >> 1) & 8) + ((lane >> 1) & 4) + ((lane >> 1) & 2) + (lane & 1)] =
@@ -913,8 +922,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             if (final_out) {
                 if (lse != nullptr) lse[q * kHeads + h] = m;
             } else {
-                part_ml[(part * kHeads + h) * 2] = m;
-                part_ml[(part * kHeads + h) * 2 + 1] = l;
+                // NaN as a sum: the merge takes its maximum over numbers
+                part_ml[(part * kHeads + h) * 2] = m == m ? m : 0.f;
+                part_ml[(part * kHeads + h) * 2 + 1] = m == m ? l : m;
             }
         }
     }
@@ -957,7 +967,7 @@ cudaError_t launch_w(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
     e = cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16*>(q_abs), pc, b, sh.scale, idx, n_sel, sh.index_row_width(), rps,
                            n_split, pair, out, lse, part_o, part_ml, err);
     if (e != cudaSuccess || n_split <= 2) return e;
-    return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st);
+    return launch_merge_splits(b.n_q, n_split, part_o, part_ml, out, lse, st, /*nan_lse=*/true);
 }
 
 }  // namespace

@@ -236,7 +236,7 @@ sparse_mla_simt(BatchDev b, float scale, const T* __restrict__ q_abs, const T* _
 // used.
 __global__ void __launch_bounds__(128)
 merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __restrict__ part_ml,
-             float* __restrict__ out, float* __restrict__ lse) {
+             float* __restrict__ out, float* __restrict__ lse, bool nan_lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials must be complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kB = 8;
@@ -309,7 +309,8 @@ merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __r
     const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
     reinterpret_cast<float4*>(out)[(q * kHeads + h) * (int64_t)(kLatent / 4) + c4] =
         make_float4(at.x * inv, at.y * inv, at.z * inv, at.w * inv);
-    if (lse != nullptr && c4 == 0) lse[q * kHeads + h] = Lt > 0.f ? Mt + logf(Lt) : -INFINITY;
+    if (lse != nullptr && c4 == 0)
+        lse[q * kHeads + h] = Lt > 0.f || (nan_lse && Lt != 0.f) ? Mt + logf(Lt) : -INFINITY;
 }
 
 // Rows per split: enough CTAs to fill the GPU about twice, at least one
@@ -349,9 +350,10 @@ cudaError_t launch_typed(const Shape& sh, const BatchDev& b, const void* q_abs, 
 }  // namespace
 
 cudaError_t launch_merge_splits(int32_t n_q, int32_t n_split, const float* part_o,
-                                const float* part_ml, float* out, float* lse, cudaStream_t st) {
+                                const float* part_ml, float* out, float* lse, cudaStream_t st,
+                                bool nan_lse) {
     return launch_pdl(merge_splits, dim3(kHeads * 4, (unsigned)n_q), dim3(128), 0, st,
-                      n_split, part_o, part_ml, out, lse);
+                      n_split, part_o, part_ml, out, lse, nan_lse);
 }
 
 void plan_attention_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_split,

@@ -204,6 +204,48 @@ def test_page_plan_over_many_steps_keeps_every_page_once():
         assert sorted(used + list(f)) == list(range(n_pages))
 
 
+@pytest.mark.parametrize("n", [7, 1500])
+def test_page_plan_captured_and_replayed_in_place(n):
+    """One captured plan: the stack, its height and the table carry over from
+    replay to replay, and a step that finds too few pages changes nothing."""
+    rng = np.random.default_rng(12)
+    page, ld = 16, 6
+    n_pages = 4 * n
+    pages = dsa.make_pages(page, n_pages, ld)
+    table = np.full((n, ld), -1, dtype=np.int32)
+    free, n_free = np.arange(n_pages, dtype=np.int32), n_pages
+    t_table, t_free = dev(table), dev(free)
+    t_n = torch.tensor([n_free], dtype=torch.int32, device=DEV)
+    held = np.zeros(n, dtype=np.int64)
+    lens = [torch.zeros(n, dtype=torch.int64, device=DEV) for _ in range(3)]
+    off = [torch.zeros(n + 1, dtype=torch.int64, device=DEV) for _ in range(2)]
+    slots = torch.zeros(100 * n, dtype=torch.int64, device=DEV)
+    ws = dsa.alloc_workspace(dsa.make_shape(), plan_batch(n), dsa.OP_PAGE_PLAN)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        dsa.dsa_page_plan(pages, *lens, t_free, t_n, t_table, off[0], off[1], slots, ws)
+    short = 0
+    for step in range(12):
+        kv = rng.integers(0, ld * page + 1, n)
+        if step % 4 == 3:
+            kv[:] = ld * page                           # more pages than there are
+        q = np.minimum(kv, rng.integers(0, 90, n))
+        for x, y in zip(lens, (held, kv, q)):
+            x.copy_(i64(y))
+        graph.replay()
+        code = dsa.dsa_check_device_error(ws)
+        want = ref.plan(page, held, kv, q, free, n_free, table, slots.numel())
+        table, free, n_free, enough = want[0], want[1], want[2], want[-1]
+        assert code == (0 if enough else 4)
+        assert np.array_equal(host(t_table), table) and np.array_equal(host(t_free), free)
+        assert t_n.item() == n_free and np.array_equal(host(slots), want[5])
+        assert np.array_equal(host(off[0]), want[3]) and np.array_equal(host(off[1]), want[4])
+        held = kv if enough else held
+        short += not enough
+    assert short >= 3
+
+
 # ------------------------------------------------------------------ append
 
 def random_rows(rng, n, width, dtype):
@@ -278,6 +320,15 @@ def test_append_matches_the_reference(page, width, dtype, fmt):
         case = AppendCase(rng, kv, q, page, width, fmt)
         rows, rows64 = random_rows(rng, int(sum(q)), width, dtype)
         assert case.check(rows, rows64, dtype) == 0
+
+
+def test_append_of_a_long_prompt_beside_single_tokens():
+    """More tokens than a grid dimension holds, in one call."""
+    kv, q = [70001, 129, 5000], [70001, 1, 4990]
+    rng = np.random.default_rng(31)
+    case = AppendCase(rng, kv, q, 64, 512, "e4m3")
+    rows, rows64 = random_rows(rng, sum(q), 512, "bf16")
+    assert case.check(rows, rows64, "bf16") == 0
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "s8"])
@@ -466,7 +517,7 @@ class AttnCase:
         rows, unit = self.rows_of(i)
         return ref.attention(self.q_abs[i].double().numpy(), rows, at, SCALE, unit), len(at)
 
-    def check(self, out, lse, queries=None, drop=()):
+    def check(self, out, lse, queries=None, drop=(), rms=1e-5):
         num = den = 0.0
         for i in range(self.n_q) if queries is None else queries:
             (o, l, weight, reach, floor), n = self.expect(i, drop)
@@ -478,7 +529,9 @@ class AttnCase:
             num += ((out[i] - o) ** 2).sum()
             den += (o ** 2).sum()
         # everything to about float32
-        assert num <= (1e-5) ** 2 * den
+        # (and, as element by element, 1e-37: float32 ends there -- a row that weighs
+        # e^-130 / 236 and holds 1e4 gives 1e-54, which is 0)
+        assert num <= rms ** 2 * den + out.size * 1e-37 ** 2
 
 
 GRID = [(dtype, fmt, rope) for dtype in ("bf16", "f32") for fmt in ("e4m3", "s8") for rope in (64, 0)]
@@ -637,6 +690,66 @@ def test_attention_is_not_touched_by_values_it_does_not_attend_over(dtype):
     t["codes"][p, r, 11] = 0x7F
     out, _, _ = case.call(t)
     assert np.isnan(out[0]).all() and np.array_equal(out[1], clean[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q,top_k", [(160, 100), (70, 300), (2, 300)])
+def test_attention_passes_nan_and_inf_on(n_q, top_k, dtype):
+    """One CTA to a query, a pair and a merge of several.  A query all of whose
+    rows are NaN; one head with an infinity and one with a NaN beside others."""
+    c = AttnCase(29, [700], [n_q], page=16, top_k=top_k, dtype=dtype)
+    c.q_abs[1, 5, 3] = float("inf")
+    c.q_abs[1, 9, 100] = float("nan")
+    c.idx[0, :c.n_sel[0]] = np.arange(c.n_sel[0]) % 16
+    for i in range(1, n_q):
+        c.idx[i] = np.where(c.idx[i] >= 0, np.maximum(c.idx[i], 16), -1)
+    t = c.tensors()
+    t["scales"][int(c.table[0, 0]), 0] = 255
+    out, lse, code = c.call(t)
+    assert code == 0 and np.isnan(out[0]).all() and np.isnan(lse[0]).all()
+    assert np.isnan(out[1, [5, 9]]).all() and np.isnan(lse[1, [5, 9]]).all()
+    fine = [h for h in range(64) if h not in (5, 9)]
+    finite = c.q_abs.clone()
+    finite[1, [5, 9]] = 0
+    c.q_abs = finite
+    (o, l, weight, reach, floor), n = c.expect(1)
+    tol, tol_lse = ref.attention_bounds(dtype, c.width, n, weight, reach, l, floor)
+    assert (np.abs(out[1] - o) <= tol)[fine].all() and (np.abs(lse[1] - l) <= tol_lse)[fine].all()
+    if n_q > 2:
+        c.check(out, lse, [2, n_q - 1])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "s8"])
+@pytest.mark.parametrize("kv", [400, 700])
+def test_attention_of_pages_of_zeros(kv, fmt):
+    """Pages of zeros have the least scale there is: first in the list, and all
+    of it, beside large values with small logits."""
+    c = AttnCase(30, [kv, 120, 300], top_k=600, fmt=fmt, spread=3000.0)
+    c.q_abs = c.q_abs / 1024
+    zero = np.concatenate([c.table[0, :2], c.table[1, :2], c.table[2, -1:]])
+    c.codes[zero], c.scales[zero] = 0, ref.E_MIN + 127
+    out, lse, code = c.call()
+    assert code == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("apart", [60.0, 75.0, 90.0, 130.0])
+def test_attention_of_zeros_that_outweigh_large_rows(apart, dtype):
+    """A page of large rows with logits far below those of pages of zeros."""
+    c = AttnCase(32, [300], top_k=300, spread=2e4, dtype=dtype)
+    c.codes[c.table[0, 0]] = c.codes[c.table[0, 0], :1]
+    c.codes[c.table[0, 1:]], c.scales[c.table[0, 1:]] = 0, ref.E_MIN + 127
+    row = c.rows_of(0)[0][0]
+    q = -apart / SCALE * row / (row @ row) * (1 + 0.002 * np.arange(64))[:, None]
+    c.q_abs = torch.tensor(q[None], dtype=torch.float32).to(TDT[dtype])
+    out, lse, code = c.call()
+    assert code == 0
+    # The whole output is one row times its weight e^(z - lse), z = -apart: a
+    # float32 sum of W products of mostly one sign, off by up to W 2^-23 |z|, which
+    # is the output's relative error (attention_bounds' first term).  With rounding
+    # errors of one size and any sign it would be sqrt(W) 2^-24 |z| = 8.6e-5 at 60.
+    c.check(out, lse, rms=c.width * 2.0 ** -23 * apart)
 
 
 def test_attention_far_into_a_large_pool():
