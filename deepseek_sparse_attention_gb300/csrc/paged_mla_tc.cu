@@ -333,17 +333,16 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         return k > 100 ? 100 : k;
     };
     auto store_query = [&](const uint4 (&v)[kQPer]) {
-        uint32_t mx = 0;
+        // the largest finite one, two at a time: with an exponent step added,
+        // infinities and NaNs are negative numbers
+        uint32_t two = 0x00800080u;
 #pragma unroll
         for (int i = 0; i < kQPer; ++i) {
             const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {            // the largest finite one
-                const uint32_t a = u[k] & 0x7fffu, c = (u[k] >> 16) & 0x7fffu;
-                mx = max(mx, max(a < 0x7f80u ? a : 0u, c < 0x7f80u ? c : 0u));
-            }
+            for (int k = 0; k < 4; ++k) two = __vmaxs2(two, (u[k] & 0x7fff7fffu) + 0x00800080u);
         }
-        mx = __reduce_max_sync(0xffffffffu, mx);
+        const uint32_t mx = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16) - 0x80u);
         if (lane == 0) atomicMax(q_max, mx);
         asm volatile("bar.sync 2, %0;" ::"n"(kQThreads) : "memory");
         const float f = exp2i(query_shift(*q_max));
