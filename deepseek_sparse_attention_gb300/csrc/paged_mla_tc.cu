@@ -432,9 +432,11 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         // row of a group of eight and quarter of its piece: eight lanes that store
         // together have four rows and two quarters of a line, eight places of it
         const int r8 = ((lane >> 1) & 3) | ((lane >> 2) & 4), k4 = (lane & 1) | ((lane >> 2) & 2);
+        // of the rope columns: two rows and every second place of their lines
+        const int rr = lane >> 2, kr = lane & 3;
         struct Tile {
             uint32_t raw[4][8];                      // 32 codes of rows rows0 + 8 i + r8
-            uint4 rope;                              // 16 rope codes of row rows0 + 8 piece + r8
+            uint4 rope;                              // 16 rope codes of row rows0 + 8 piece + rr
             uint32_t b0, b1;                         // scales of row rows0 + lane
             uint32_t has;                            // rows that exist, a bit each
         };
@@ -449,11 +451,14 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 ldg_32bytes(src + 128 * piece + 32 * k4, x.raw[i]);
             }
             if (kParts == 2) {
-                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * piece + r8) * W;
-                x.rope = __ldg(reinterpret_cast<const uint4*>(src + kLatent + 16 * k4));
+                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * piece + rr) * W;
+                x.rope = __ldg(reinterpret_cast<const uint4*>(src + kLatent + 16 * kr));
             }
-            x.b0 = __ldg(pc.scales + pg * kParts);
-            x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
+            // one warp of four has use for the scales: the others' lanes read the
+            // same place (32 pages' scales are 32 wavefronts of the cache)
+            const uint8_t* sc = pc.scales + (piece == 0 ? pg : 0) * kParts;
+            x.b0 = __ldg(sc);
+            x.b1 = kParts == 2 ? __ldg(sc + 1) : 0u;
         };
         Tile xa, xb;
         if (qi.seq != guess_row) {
@@ -484,7 +489,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x.raw[i][j] = 0;
                 }
-                if (!((x.has >> (8 * piece + r8)) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
+                if (!((x.has >> (8 * piece + rr)) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
             }
             // half of a 64-column block's line: four 16-byte pieces
             uint8_t* dst = rbuf + (2 * piece + (k4 >> 1)) * kBlock + (rows0 + r8) * 128;
@@ -506,9 +511,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 if (!ok) return;
                 const uint2 a0 = codes_f16<FMT>(x.rope.x), a1 = codes_f16<FMT>(x.rope.y);
                 const uint2 a2 = codes_f16<FMT>(x.rope.z), a3 = codes_f16<FMT>(x.rope.w);
-                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + 8 * piece + r8) * 128;
-                *reinterpret_cast<uint4*>(rope + (((2 * k4) ^ r8) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-                *reinterpret_cast<uint4*>(rope + (((2 * k4 + 1) ^ r8) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + 8 * piece + rr) * 128;
+                *reinterpret_cast<uint4*>(rope + (((2 * kr) ^ rr) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                *reinterpret_cast<uint4*>(rope + (((2 * kr + 1) ^ rr) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + kLatentBlocks]);
