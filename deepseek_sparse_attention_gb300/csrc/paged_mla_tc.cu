@@ -269,7 +269,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&p_full[i], kSoftmaxThreads);
             for (int g = 0; g < C::kPieces; ++g)      // arrivals of warps
-                mbar_init(&r_full[i * C::kPieces + g], g < kLatentBlocks ? 2 : kLoaders / 32);
+                mbar_init(&r_full[i * C::kPieces + g], kLoaders / 32);
             for (int g = 0; g < kLatentBlocks; ++g) mbar_init(&freed[i * kLatentBlocks + g], 1);
         }
         fence_mbarrier_init();
@@ -298,11 +298,11 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     const bool dense = idx == nullptr;
     const int64_t j0 = (int64_t)split * rows_per_split;
     const bool loader = warp >= kSoftmaxThreads / 32 && warp < kMmaWarp;
-    // loader warp lw brings piece lw % 4 of the rows 32 (lw / 4) .. + 31 of a tile,
-    // and the rope columns of eight of them; lane l knows where row rows0 + l is
-    const int lw = warp - kSoftmaxThreads / 32, piece = lw & 3, rows0 = 32 * (lw >> 2);
+    // loader warp lw brings the rows 8 lw .. + 7 of a tile; lane l knows where row
+    // rows0 + l % 8 is
+    const int rows0 = 8 * (warp - kSoftmaxThreads / 32);
     auto entry = [&](int t, int64_t end) -> int32_t {
-        const int64_t j = min(j0 + (int64_t)t * kTileRows + rows0 + lane, end - 1);
+        const int64_t j = min(j0 + (int64_t)t * kTileRows + rows0 + (lane & 7), end - 1);
         return dense ? (int32_t)j : idx[q * idx_width + j];
     };
     int32_t e0 = 0, e1 = 0, e2 = 0;
@@ -424,20 +424,21 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         // is worth is decided where it is used: a read within a branch is waited
         // for where the branch ends.
         const int32_t* table = pc.block_table + (int64_t)qi.seq * pc.pg.table_ld;
-        auto in_list = [&](int t) { return j0 + (int64_t)t * kTileRows + rows0 + lane < j1; };
+        auto in_list = [&](int t) { return j0 + (int64_t)t * kTileRows + rows0 + (lane & 7) < j1; };
         auto in_table = [&](int32_t r) {
             return r >= 0 && r < qi.L && (r >> pc.pg.shift) < pc.pg.table_ld;
         };
         auto page_of_row = [&](int32_t r) -> int32_t { return table[in_table(r) ? r >> pc.pg.shift : 0]; };
-        // row of a group of eight and quarter of its piece: eight lanes that store
-        // together have four rows and two quarters of a line, eight places of it
+        // this lane's row of the warp's eight and quarter of a piece: eight lanes
+        // that store together have four rows and two quarters of a line, eight
+        // places of it
         const int r8 = ((lane >> 1) & 3) | ((lane >> 2) & 4), k4 = (lane & 1) | ((lane >> 2) & 2);
         // of the rope columns: two rows and every second place of their lines
         const int rr = lane >> 2, kr = lane & 3;
         struct Tile {
-            uint32_t raw[4][8];                      // 32 codes of rows rows0 + 8 i + r8
-            uint4 rope;                              // 16 rope codes of row rows0 + 8 piece + rr
-            uint32_t b0, b1;                         // scales of row rows0 + lane
+            uint32_t raw[kLatentBlocks][8];          // 32 codes of each piece of row rows0 + r8
+            uint4 rope;                              // 16 rope codes of row rows0 + rr
+            uint32_t b0, b1;                         // scales of row rows0 + lane % 8
             uint32_t has;                            // rows that exist, a bit each
         };
         auto load = [&](Tile& x, int t, int32_t r, int32_t page) {
@@ -445,20 +446,15 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const int64_t pg = has ? page : 0;
             const int64_t at = has ? (pg << pc.pg.shift) + (r & (pc.pg.page_rows - 1)) : 0;
             x.has = __ballot_sync(0xffffffffu, has);
+            const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, r8) * W + 32 * k4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * i + r8) * W;
-                ldg_32bytes(src + 128 * piece + 32 * k4, x.raw[i]);
-            }
+            for (int i = 0; i < kLatentBlocks; ++i) ldg_32bytes(src + 128 * i, x.raw[i]);
             if (kParts == 2) {
-                const uint8_t* src = pc.codes + __shfl_sync(0xffffffffu, at, 8 * piece + rr) * W;
-                x.rope = __ldg(reinterpret_cast<const uint4*>(src + kLatent + 16 * kr));
+                const uint8_t* tail = pc.codes + __shfl_sync(0xffffffffu, at, rr) * W + kLatent + 16 * kr;
+                x.rope = __ldg(reinterpret_cast<const uint4*>(tail));
             }
-            // one warp of four has use for the scales: the others' lanes read the
-            // same place (32 pages' scales are 32 wavefronts of the cache)
-            const uint8_t* sc = pc.scales + (piece == 0 ? pg : 0) * kParts;
-            x.b0 = __ldg(sc);
-            x.b1 = kParts == 2 ? __ldg(sc + 1) : 0u;
+            x.b0 = __ldg(pc.scales + pg * kParts);
+            x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
         };
         Tile xa, xb;
         if (qi.seq != guess_row) {
@@ -476,42 +472,44 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const int buf = t & 1;
             uint8_t* rbuf = smem + C::kOffR + buf * C::kBufBytes;
             const uint32_t phase = (uint32_t)(((t >> 1) - 1) & 1);
-            // the piece's columns have been read by tile t - 2's value product
-            if (t >= 2) ok = mbar_wait(&freed[buf * kLatentBlocks + piece], phase, kWaitNs);
-            if (!ok) return;
-            const bool in = (x.has >> lane) & 1u;
-            if (piece == 0) rinfo[buf * kTileRows + rows0 + lane] = in ? kHasRow | (x.b1 << 8) | x.b0 : 0u;
-            if (piece == 0 && !in && in_list(t)) record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
-            if (x.has != 0xffffffffu) {              // zeros for rows that do not exist
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if ((x.has >> (8 * i + r8)) & 1u) continue;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x.raw[i][j] = 0;
-                }
-                if (!((x.has >> (8 * piece + rr)) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
+            if (lane < 8) {
+                const bool in = (x.has >> lane) & 1u;
+                if (!in && in_list(t)) record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
             }
-            // half of a 64-column block's line: four 16-byte pieces
-            uint8_t* dst = rbuf + (2 * piece + (k4 >> 1)) * kBlock + (rows0 + r8) * 128;
+            if ((x.has & 0xffu) != 0xffu) {          // zeros for rows that do not exist
+                if (!((x.has >> r8) & 1u)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kLatentBlocks; ++i)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x.raw[i][j] = 0;
+                }
+                if (!((x.has >> rr) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kLatentBlocks; ++i) {
+                // the piece's columns have been read by tile t - 2's value product
+                if (t >= 2 && ok) ok = mbar_wait(&freed[buf * kLatentBlocks + i], phase, kWaitNs);
+                if (!ok) return;
+                if (i == 0 && lane < 8)
+                    rinfo[buf * kTileRows + rows0 + lane] =
+                        (x.has >> lane) & 1u ? kHasRow | (x.b1 << 8) | x.b0 : 0u;
+                // half of a 64-column block's line: four 16-byte places
+                uint8_t* dst = rbuf + (2 * i + (k4 >> 1)) * kBlock + (rows0 + r8) * 128;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint2 lo = codes_f16<FMT>(x.raw[i][2 * j]), hi = codes_f16<FMT>(x.raw[i][2 * j + 1]);
-                    *reinterpret_cast<uint4*>(dst + 8 * i * 128 + (((4 * (k4 & 1) + j) ^ r8) << 4)) =
+                    *reinterpret_cast<uint4*>(dst + (((4 * (k4 & 1) + j) ^ r8) << 4)) =
                         make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + i]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + piece]);
             if constexpr (kParts == 2) {
-                // the rope block held tile t - 2's W_hi, which all of its products read
-                if (t >= 2) ok = mbar_wait(&freed[buf * kLatentBlocks + kLatentBlocks - 1], phase, kWaitNs);
-                if (!ok) return;
+                // the rope block held tile t - 2's W_hi, which its last product has read
                 const uint2 a0 = codes_f16<FMT>(x.rope.x), a1 = codes_f16<FMT>(x.rope.y);
                 const uint2 a2 = codes_f16<FMT>(x.rope.z), a3 = codes_f16<FMT>(x.rope.w);
-                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + 8 * piece + rr) * 128;
+                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + rr) * 128;
                 *reinterpret_cast<uint4*>(rope + (((2 * kr) ^ rr) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
                 *reinterpret_cast<uint4*>(rope + (((2 * kr + 1) ^ rr) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
                 fence_proxy_async_smem();
