@@ -394,7 +394,10 @@ typedef struct {
  * and counts as empty.  New tokens past max_new set it too and get no slot.
  * Nothing depends on the order in which the GPU runs: the same arguments give
  * the same tables.  n_seq <= 2^20, max_new < 2^31; pointers 8-byte aligned
- * (int32 ones 4-byte).  Workspace: DSA_OP_PAGE_PLAN. */
+ * (int32 ones 4-byte).  Workspace: DSA_OP_PAGE_PLAN, zeroed once
+ * (dsa_workspace_init, or allocated zero-filled): the CTAs count themselves in
+ * its header, and leave the count at zero, so two calls sharing one workspace
+ * must not run concurrently. */
 dsa_status dsa_page_plan(const dsa_pages *pages, int32_t n_seq, int64_t max_new,
                          const int64_t *held_len, const int64_t *kv_len, const int64_t *q_len,
                          int32_t *free_pages, const int32_t *n_free_in, int32_t *n_free_out,
@@ -434,10 +437,13 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  *   codes, scales, block_table as above
  * An index outside [0, L), or one whose block-table entry is no page of the
  * pool, sets the error word and its row is skipped.  A NaN code or scale of an
- * attended row gives NaN outputs.  float32 accumulation and softmax.  bf16
+ * attended row gives NaN outputs and a NaN lse, and so does an infinite or NaN
+ * query element for its head.  float32 accumulation and softmax.  bf16
  * queries run on the tensor cores: the query as f16 times a power of two (exact
  * for elements within 2^-32 of its largest), a row's weight in the output as two
- * f16 parts (2^-22 of it, or 2^-25 of the largest).  Pointers 16-byte aligned
+ * f16 parts (2^-22 of it, or 2^-25 of the largest); among the rows of a list no
+ * scale may be above 2^100 times those of its first 64 rows (pages of zeros do
+ * not count).  Pointers 16-byte aligned
  * (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
  * DSA_OP_PAGED_MLA. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,
