@@ -16,7 +16,7 @@
 // (the CTA is sized so that a page of up to 64 rows does; the rest of a larger
 // one is read again), and are requested before the slots are read: a CTA's time
 // is the latencies that it waits for in turn.  Bound by HBM for a prompt (2 or 4
-// bytes read and one written per element; 183,000 float32 rows: 91 us = 0.76 of
+// bytes read and one written per element; 183,000 float32 rows: 88 us = 0.79 of
 // the measured bandwidth, 108 us with the slots first, 160 us in CTAs of 512
 // threads whatever the page), by latency for a decode step (2.6 us for 64 rows).
 #include "dsa_kernels.cuh"
