@@ -644,57 +644,6 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         uint32_t vote_phase = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int bf = t & 1;
-            if (t > 0 && t % kFlushTiles == 0) {
-                // O^T moves to memory, as multiples of 2^m of the move that began a
-                // head's sum: added to it, or beginning it anew where m has grown so
-                // far that what is there no longer counts.
-                const int pb = (t - 1) & 1;
-                if (ok) ok = mbar_wait(&freed[pb * kLatentBlocks + kLatentBlocks - 1],
-                                       (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
-                tc_fence_after();
-                if (threadIdx.x < kHeads) {
-                    const int h = threadIdx.x;
-                    const float grown = m_fin[h] - m_moved[h];
-                    const bool anew = t == kFlushTiles || grown > 80.f;
-                    if (anew) m_moved[h] = m_fin[h];
-                    alpha_s[h] = anew ? 1.f : exp2f(grown);
-                    const uint32_t mask = __ballot_sync(0xffffffffu, anew);
-                    if (lane == 0) raised_s[warp] = mask;
-                }
-                softmax_sync();
-                const uint32_t mask = raised_s[warp >> 2];
-                float* const sums = sums_at();
-#pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
-                    const int h = 32 * (warp >> 2) + 8 * g;
-#pragma unroll
-                    for (int j = 0; j < kOBlocks; j += 4) {
-                        uint32_t a[4];               // the last one again past the end
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            a[i] = lane_addr + C::kOCol + 64 * min(j + i, kOBlocks - 1) + h;
-                        float v[32];
-                        tmem_ld_4x8cols(a, v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = j + i;     // hi and lo of the wide blocks, then the others
-                            const bool wide = k < 2 * C::kWide;
-                            const int blk = wide ? k >> 1 : k - C::kWide;
-                            if (k >= kOBlocks || (wide && (k & 1)) || !owns(blk)) continue;
-                            float* dst = sums + h * kLatent + 128 * blk + 32 * wq + lane;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float o = wide ? v[8 * i + c] + v[(8 * i + c + 8) & 31] : v[8 * i + c];
-                                if ((mask >> (8 * g + c)) & 1u) dst[c * kLatent] = o;
-                                else atomicAdd(dst + c * kLatent, o * alpha_s[h + c]);
-                            }
-                        }
-                    }
-                }
-                tc_fence_before();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) m[e] = m_fin[hb + e];   // not kept in registers meanwhile
-            }
             if (ok) ok = mbar_wait(s_full, (uint32_t)(t & 1), kWaitNs);
             tc_fence_after();
             const uint32_t info = rinfo[bf * kTileRows + srow];
@@ -786,7 +735,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
                 for (int e = 0; e < 16; ++e) l_part[e] *= alpha_s[hb + e];
                 have_max = have_max || (raised_s[0] | raised_s[1]) != 0;
-                if (t % kFlushTiles != 0) up = raised_s[warp >> 2];
+                if (t > 0) up = raised_s[warp >> 2];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     m[e] = m_fin[hb + e];
@@ -858,6 +807,55 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 *reinterpret_cast<uint4*>(plow + ((((hb >> 3) + c8) ^ (srow & 7)) << 4)) =
                     make_uint4(lo[4 * c8], lo[4 * c8 + 1], lo[4 * c8 + 2], lo[4 * c8 + 3]);
             fence_proxy_async_smem();
+            if (t > 0 && t % kFlushTiles == 0) {
+                // O^T moves to memory, as multiples of 2^m of the move that began a
+                // head's sum: added to it, or beginning it anew where m has grown so
+                // far that what is there no longer counts.
+                softmax_sync();                      // alpha_s is read
+                tc_fence_after();
+                if (threadIdx.x < kHeads) {
+                    const int h = threadIdx.x;
+                    const float grown = m_fin[h] - m_moved[h];
+                    const bool anew = t == kFlushTiles || grown > 80.f;
+                    if (anew) m_moved[h] = m_fin[h];
+                    alpha_s[h] = anew ? 1.f : exp2f(grown);
+                    const uint32_t mask = __ballot_sync(0xffffffffu, anew);
+                    if (lane == 0) raised_s[warp] = mask;
+                }
+                softmax_sync();
+                const uint32_t mask = raised_s[warp >> 2];
+                float* const sums = sums_at();
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    const int h = 32 * (warp >> 2) + 8 * g;
+#pragma unroll
+                    for (int j = 0; j < kOBlocks; j += 4) {
+                        uint32_t a[4];               // the last one again past the end
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a[i] = lane_addr + C::kOCol + 64 * min(j + i, kOBlocks - 1) + h;
+                        float v[32];
+                        tmem_ld_4x8cols(a, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = j + i;     // hi and lo of the wide blocks, then the others
+                            const bool wide = k < 2 * C::kWide;
+                            const int blk = wide ? k >> 1 : k - C::kWide;
+                            if (k >= kOBlocks || (wide && (k & 1)) || !owns(blk)) continue;
+                            float* dst = sums + h * kLatent + 128 * blk + 32 * wq + lane;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const float o = wide ? v[8 * i + c] + v[(8 * i + c + 8) & 31] : v[8 * i + c];
+                                if ((mask >> (8 * g + c)) & 1u) dst[c * kLatent] = o;
+                                else atomicAdd(dst + c * kLatent, o * alpha_s[h + c]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) m[e] = m_fin[hb + e];   // not kept in registers meanwhile
+            }
             tc_fence_before();
             mbar_arrive(&p_full[bf]);
         }
