@@ -72,9 +72,8 @@ constexpr float kSlack = 15.75f;
 // accumulation off instead of rounding it, so a sum's error grows with the tiles
 // in it: relative to the output, against 64 bits, 0.3e-6 for 2 tiles, 1.2e-6 for
 // 16, 1.6e-6 for 32, where float32 sums have 0.5e-6.  Moved every 11 tiles it is
-// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows took 600 us without,
-// 630 us with a move every 16 tiles and 660 us with one every 11 (a move and the
-// read at the end are 8,500 cycles).
+// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows take 573 us without and
+// 632 us so (every 16 tiles: half of that, and errors above 1e-6).
 constexpr int kFlushTiles = 11;
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any row
 constexpr int kSoftmaxThreads = 256;
