@@ -433,15 +433,14 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             return r >= 0 && r < qi.L && (r >> pc.pg.shift) < pc.pg.table_ld;
         };
         auto page_of_row = [&](int32_t r) -> int32_t { return table[in_table(r) ? r >> pc.pg.shift : 0]; };
-        // this lane's row of the warp's eight and quarter of a piece: eight lanes
-        // that store together have four rows and two quarters of a line, eight
-        // places of it
-        const int r8 = ((lane >> 1) & 3) | ((lane >> 2) & 4), k4 = (lane & 1) | ((lane >> 2) & 2);
-        // of the rope columns: two rows and every second place of their lines
-        const int rr = lane >> 2, kr = lane & 3;
+        // this lane's row of the warp's eight and quarter of a piece (of its 128
+        // columns, or of the 64 rope columns): four lanes read 128 bytes of a row.
+        // Eight lanes that store together have two rows' four quarters, of which
+        // the later two take their places in another order: eight places of a line.
+        const int r8 = lane >> 2, k4 = lane & 3;
         struct Tile {
             uint32_t raw[kLatentBlocks][8];          // 32 codes of each piece of row rows0 + r8
-            uint4 rope;                              // 16 rope codes of row rows0 + rr
+            uint4 rope;                              // 16 rope codes of the same row
             uint32_t b0, b1;                         // scales of row rows0 + lane % 8
             uint32_t has;                            // rows that exist, a bit each
         };
@@ -454,8 +453,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
             for (int i = 0; i < kLatentBlocks; ++i) ldg_32bytes(src + 128 * i, x.raw[i]);
             if (kParts == 2) {
-                const uint8_t* tail = pc.codes + __shfl_sync(0xffffffffu, at, rr) * W + kLatent + 16 * kr;
-                x.rope = __ldg(reinterpret_cast<const uint4*>(tail));
+                x.rope = __ldg(reinterpret_cast<const uint4*>(src + kLatent - 16 * k4));
             }
             x.b0 = __ldg(pc.scales + pg * kParts);
             x.b1 = kParts == 2 ? __ldg(pc.scales + pg * kParts + 1) : 0u;
@@ -487,8 +485,16 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
                         for (int j = 0; j < 8; ++j) x.raw[i][j] = 0;
                 }
-                if (!((x.has >> rr) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
+                if (!((x.has >> r8) & 1u)) x.rope = make_uint4(0, 0, 0, 0);
             }
+#pragma unroll
+            for (int i = 0; i < kLatentBlocks; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a = x.raw[i][j], b = x.raw[i][4 + j];
+                    x.raw[i][j] = k4 & 2 ? b : a;
+                    x.raw[i][4 + j] = k4 & 2 ? a : b;
+                }
 #pragma unroll
             for (int i = 0; i < kLatentBlocks; ++i) {
                 // the piece's columns have been read by tile t - 2's value product
@@ -502,7 +508,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint2 lo = codes_f16<FMT>(x.raw[i][2 * j]), hi = codes_f16<FMT>(x.raw[i][2 * j + 1]);
-                    *reinterpret_cast<uint4*>(dst + (((4 * (k4 & 1) + j) ^ r8) << 4)) =
+                    *reinterpret_cast<uint4*>(dst + (((4 * (k4 & 1) + (j ^ (k4 & 2))) ^ r8) << 4)) =
                         make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
                 fence_proxy_async_smem();
@@ -513,9 +519,9 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 // the rope block held tile t - 2's W_hi, which its last product has read
                 const uint2 a0 = codes_f16<FMT>(x.rope.x), a1 = codes_f16<FMT>(x.rope.y);
                 const uint2 a2 = codes_f16<FMT>(x.rope.z), a3 = codes_f16<FMT>(x.rope.w);
-                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + rr) * 128;
-                *reinterpret_cast<uint4*>(rope + (((2 * kr) ^ rr) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-                *reinterpret_cast<uint4*>(rope + (((2 * kr + 1) ^ rr) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+                uint8_t* rope = rbuf + 2 * kLatentBlocks * kBlock + (rows0 + r8) * 128;
+                *reinterpret_cast<uint4*>(rope + (((2 * k4) ^ r8) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                *reinterpret_cast<uint4*>(rope + (((2 * k4 + 1) ^ r8) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&r_full[buf * C::kPieces + kLatentBlocks]);
