@@ -9,13 +9,15 @@
 // KV Cache"; "GLM-5.x (glm-dsa, glm5next)", "The block").
 //
 // A CTA takes 16 heads and a range of one query's rows, 16 at a time: the rows
-// are widened to float in shared memory, and the 16 lanes of a half warp belong
-// to one head -- a lane forms one row's logit, the half warp folds the tile into
-// its running maximum and sum by shuffles, and each lane accumulates 32 of the
-// head's 512 outputs.  Bound by shared-memory reads (a float4 for four
-// multiply-adds); small float32 steps are bound by latency, which is why the
-// heads are spread over CTAs (one query of 256 rows: 27 us with all 64 heads in
-// a CTA and the softmax through shared memory, 14 us so).  Rows whose index or
+// are widened to float in shared memory, and each of four warps has four heads --
+// a lane forms the logits of two rows and four heads over a quarter of the
+// columns, the warp folds the tile into its running maxima and sums by shuffles,
+// and each lane accumulates 16 of the 512 outputs of its four heads.  Bound by
+// shared-memory reads, so a float4 read is used for 16 multiply-adds and more
+// (ten queries of 2,048 rows: 257 us with a half warp to a head and four
+// multiply-adds a read, 169 us so); small float32 steps are bound by latency,
+// which is why the heads are spread over CTAs (one query of 256 rows: 27 us with
+// all 64 heads in a CTA and the softmax through shared memory, 13.5 us so).  Rows whose index or
 // page is out of range are zero and take no weight.  Splits of a query are
 // combined by the log-sum-exp merge.
 #include <math.h>
@@ -25,9 +27,10 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeads = 64;
 constexpr int kGroup = 16;                       // heads of a CTA
+constexpr int kWarpHeads = 4;                    // of a warp
 constexpr int kTile = 16;                        // rows per tile
 constexpr int kLatent = kLatentCols;
 
@@ -41,8 +44,15 @@ struct Smem {
     static constexpr size_t kTotal = kRows + kQ + kR + kP;
 };
 
+__device__ __forceinline__ void fma4(float4& a, const float4& x, const float4& y) {
+    a.x = fmaf(x.x, y.x, a.x);
+    a.y = fmaf(x.y, y.y, a.y);
+    a.z = fmaf(x.z, y.z, a.z);
+    a.w = fmaf(x.w, y.w, a.w);
+}
+
 template <int FMT, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__ q_abs,
                const int32_t* __restrict__ idx, const int32_t* __restrict__ n_sel,
                int64_t idx_width, int32_t rows_per_split, int32_t n_split,
@@ -63,13 +73,15 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
     const int tid = threadIdx.x;
     const int64_t q = blockIdx.y;
     const int split = blockIdx.x, h0 = kGroup * blockIdx.z;
-    const int hl = tid >> 4, j = tid & 15, h = h0 + hl;  // this lane's head; its row, its columns
+    const int warp = tid >> 5, lane = tid & 31;
+    const int hw = kWarpHeads * warp;                  // this warp's first head of the group
+    const int rg = lane & 7, kq = lane >> 3;           // this lane's rows rg, rg + 8; its quarter of the columns
     const int64_t part = q * n_split + split;
     QueryInfo qi;
     if (!query_info(b, q, qi, err, /*where=*/33)) {
-        if (n_split > 1 && j == 0) {                   // no weight in the merge
-            part_ml[(part * kHeads + h) * 2 + 0] = -INFINITY;
-            part_ml[(part * kHeads + h) * 2 + 1] = 0.f;
+        if (n_split > 1 && tid < kGroup) {             // no weight in the merge
+            part_ml[(part * kHeads + h0 + tid) * 2 + 0] = -INFINITY;
+            part_ml[(part * kHeads + h0 + tid) * 2 + 1] = 0.f;
         }
         return;
     }
@@ -85,10 +97,15 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
             __ldg(reinterpret_cast<const float4*>(qsrc + (int64_t)r * W + c));
     }
 
-    float m = -INFINITY, l = 0.f;                      // the same in a head's 16 lanes
-    float o[kLatent / 16];                             // columns 4 j + 64 i + (0..3)
+    float m[kWarpHeads], l[kWarpHeads];                // the same in all lanes of the warp
+    float4 o[kWarpHeads][kLatent / 128];               // columns 4 lane + 128 i
 #pragma unroll
-    for (int i = 0; i < kLatent / 16; ++i) o[i] = 0.f;
+    for (int k = 0; k < kWarpHeads; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kLatent / 128; ++i) o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 
     for (int64_t t0 = j_begin; t0 < j_end; t0 += kTile) {
         const int nrows = (int)(j_end - t0 < kTile ? j_end - t0 : kTile);
@@ -126,64 +143,94 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
             }
         }
         __syncthreads();
-        // the logit of row j and head h
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int c = 0; c < W; c += 4) {
-            const float4 r4 = *reinterpret_cast<const float4*>(Rs + j * S::kStride + c);
-            const float4 q4 = *reinterpret_cast<const float4*>(Qs + hl * S::kStride + c);
-            acc[0] = fmaf(q4.x, r4.x, acc[0]);
-            acc[1] = fmaf(q4.y, r4.y, acc[1]);
-            acc[2] = fmaf(q4.z, r4.z, acc[2]);
-            acc[3] = fmaf(q4.w, r4.w, acc[3]);
+        // the logits of two rows and four heads over a quarter of the columns
+        float z[kWarpHeads][2];
+        {
+            float4 acc[kWarpHeads][2];
+#pragma unroll
+            for (int k = 0; k < kWarpHeads; ++k) acc[k][0] = acc[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int c = 4 * kq; c < W; c += 16) {
+                const float4 ra = *reinterpret_cast<const float4*>(Rs + rg * S::kStride + c);
+                const float4 rb = *reinterpret_cast<const float4*>(Rs + (rg + 8) * S::kStride + c);
+#pragma unroll
+                for (int k = 0; k < kWarpHeads; ++k) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(Qs + (hw + k) * S::kStride + c);
+                    fma4(acc[k][0], q4, ra);
+                    fma4(acc[k][1], q4, rb);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kWarpHeads; ++k) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = (acc[k][i].x + acc[k][i].y) + (acc[k][i].z + acc[k][i].w);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    z[k][i] = row_at[rg + 8 * i] >= 0 ? x * scale : -INFINITY;
+                }
+            }
         }
-        const float z = row_at[j] >= 0 ? ((acc[0] + acc[1]) + (acc[2] + acc[3])) * scale : -INFINITY;
-        float mx = z;
+        float alpha[kWarpHeads];
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float m_new = fmaxf(m, mx);
-        // no maximum yet: rows without weight, or a NaN logit to pass on
-        const float p = z == -INFINITY ? 0.f : expf(z - m_new);
-        const float alpha = m_new == -INFINITY ? 1.f : expf(m - m_new);
-        float sum = p;
+        for (int k = 0; k < kWarpHeads; ++k) {
+            float mx = fmaxf(z[k][0], z[k][1]);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l = l * alpha + sum;
-        m = m_new;
-        Ps[hl * kTile + j] = p;                        // read by this half warp alone
+            for (int d = 4; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float m_new = fmaxf(m[k], mx);
+            // no maximum yet: rows without weight, or a NaN logit to pass on
+            const float p0 = z[k][0] == -INFINITY ? 0.f : expf(z[k][0] - m_new);
+            const float p1 = z[k][1] == -INFINITY ? 0.f : expf(z[k][1] - m_new);
+            alpha[k] = m_new == -INFINITY ? 1.f : expf(m[k] - m_new);
+            float sum = p0 + p1;
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l[k] = l[k] * alpha[k] + sum;
+            m[k] = m_new;
+            if (kq == k) {                             // [row][head], read by this warp alone
+                Ps[(warp * kTile + rg) * kWarpHeads + k] = p0;
+                Ps[(warp * kTile + rg + 8) * kWarpHeads + k] = p1;
+            }
+#pragma unroll
+            for (int i = 0; i < kLatent / 128; ++i) {
+                o[k][i].x *= alpha[k]; o[k][i].y *= alpha[k]; o[k][i].z *= alpha[k]; o[k][i].w *= alpha[k];
+            }
+        }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kLatent / 16; ++i) o[i] *= alpha;
+#pragma unroll 2
         for (int r = 0; r < nrows; ++r) {
-            const float w = Ps[hl * kTile + r];
-            const float* rrow = Rs + r * S::kStride + 4 * j;
+            const float4 w = *reinterpret_cast<const float4*>(Ps + (warp * kTile + r) * kWarpHeads);
+            const float wk[kWarpHeads] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < kLatent / 64; ++i) {
-                const float4 r4 = *reinterpret_cast<const float4*>(rrow + 64 * i);
-                o[4 * i + 0] = fmaf(w, r4.x, o[4 * i + 0]);
-                o[4 * i + 1] = fmaf(w, r4.y, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(w, r4.z, o[4 * i + 2]);
-                o[4 * i + 3] = fmaf(w, r4.w, o[4 * i + 3]);
+            for (int i = 0; i < kLatent / 128; ++i) {
+                const float4 r4 = *reinterpret_cast<const float4*>(Rs + r * S::kStride + 4 * lane + 128 * i);
+#pragma unroll
+                for (int k = 0; k < kWarpHeads; ++k)
+                    fma4(o[k][i], make_float4(wk[k], wk[k], wk[k], wk[k]), r4);
             }
         }
         __syncthreads();
     }
 
     const bool last = n_split == 1;
-    const float inv = last ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-    float* dst = (last ? out + (q * kHeads + h) * (int64_t)kLatent
-                       : part_o + (part * kHeads + h) * (int64_t)kLatent) + 4 * j;
 #pragma unroll
-    for (int i = 0; i < kLatent / 64; ++i)
-        *reinterpret_cast<float4*>(dst + 64 * i) =
-            make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-    if (j == 0) {
-        if (last) {
-            if (lse != nullptr) lse[q * kHeads + h] = l == 0.f ? -INFINITY : m + logf(l);
-        } else {
-            // rows whose logits are all NaN: a split with weight
-            part_ml[(part * kHeads + h) * 2 + 0] = m == -INFINITY && l != 0.f ? 0.f : m;
-            part_ml[(part * kHeads + h) * 2 + 1] = l;
+    for (int k = 0; k < kWarpHeads; ++k) {
+        const int h = h0 + hw + k;
+        const float inv = last ? (l[k] == 0.f ? 0.f : 1.f / l[k]) : 1.f;
+        float* dst = (last ? out + (q * kHeads + h) * (int64_t)kLatent
+                           : part_o + (part * kHeads + h) * (int64_t)kLatent) + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < kLatent / 128; ++i)
+            *reinterpret_cast<float4*>(dst + 128 * i) =
+                make_float4(o[k][i].x * inv, o[k][i].y * inv, o[k][i].z * inv, o[k][i].w * inv);
+        if (lane == 0) {
+            if (last) {
+                if (lse != nullptr) lse[q * kHeads + h] = l[k] == 0.f ? -INFINITY : m[k] + logf(l[k]);
+            } else {
+                // rows whose logits are all NaN: a split with weight
+                part_ml[(part * kHeads + h) * 2 + 0] = m[k] == -INFINITY && l[k] != 0.f ? 0.f : m[k];
+                part_ml[(part * kHeads + h) * 2 + 1] = l[k];
+            }
         }
     }
 }
