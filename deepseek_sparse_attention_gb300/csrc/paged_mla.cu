@@ -15,7 +15,7 @@
 // and each lane accumulates 16 of the 512 outputs of its four heads.  Bound by
 // shared-memory reads, so a float4 read is used for 16 multiply-adds and more
 // (ten queries of 2,048 rows: 257 us with a half warp to a head and four
-// multiply-adds a read, 169 us so); small float32 steps are bound by latency,
+// multiply-adds a read, 169 us so, 131 us with the splits below); small float32 steps are bound by latency,
 // which is why the heads are spread over CTAs (one query of 256 rows: 27 us with
 // all 64 heads in a CTA and the softmax through shared memory, 13.5 us so).  Rows whose index or
 // page is out of range are zero and take no weight.  Splits of a query are
@@ -248,12 +248,14 @@ void paged_rows(const Shape& sh, const BatchDev& b, int64_t* main_rows, int64_t*
     if (*main_rows < 1 || *main_rows > *max_rows) *main_rows = *max_rows;
 }
 
-// CUDA-core splits: with the four head groups enough CTAs to fill the GPU four
-// times (three are resident per multiprocessor), at least one tile each.
+// CUDA-core splits: with the four head groups at most the CTAs that are resident
+// at once, three a multiprocessor, and at least one tile each.  (Four a
+// multiprocessor, rounded up: ten queries of 2,048 rows 169 us, one query 36.7 us;
+// so 131 and 25.7 us.)
 void plan_splits_simt(int32_t n_q, int64_t max_rows, int32_t* rows_per_split, int32_t* n_split) {
-    const int64_t target = 4 * (int64_t)sm_count() / (kHeads / kGroup);
+    const int64_t target = 3 * (int64_t)sm_count() / (kHeads / kGroup);
     const int64_t tiles = (max_rows + kTile - 1) / kTile;
-    int64_t splits = (target + n_q - 1) / n_q;
+    int64_t splits = target / n_q;
     if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
     const int64_t rps = (tiles + splits - 1) / splits * kTile;
