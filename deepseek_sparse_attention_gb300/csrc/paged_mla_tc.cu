@@ -12,7 +12,7 @@
 // output), and p relative to the same maximum with one fixed exponent taken off.
 // The query becomes f16 times one power of two per query (its elements span
 // 32 binades exactly; what is below that is below float32's reach too).  w is
-// carried as two f16 parts, hi + lo, to 2^-22 of it or 2^-25 of the largest.
+// carried as two f16 parts, hi + lo, to 2^-22 of it or 2^-37 of the largest.
 //
 // One CTA takes a range of one query's rows in tiles of 64, two f16 row buffers
 // deep:
@@ -62,11 +62,15 @@ constexpr uint32_t kSCol = 0, kSRopeCol = 64;        // S^T of the latent and th
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A running maximum is raised (and O^T rescaled) only when it is exceeded by more
-// than this, in log2: w stays below 55,109, within f16.  (With 14 a third of the
-// tiles of 2,048 normally distributed logits raised one: 1,024 queries 655 us, so
-// 638 us.)
-constexpr float kSlack = 15.75f;
+// A head's weights are w = 2^(x - m) with a reference m that is set kRoom below the
+// largest logit met and set again (and O^T rescaled) only when one exceeds it by more
+// than kSlack, all in log2: w is then at least 2^12 for the largest row and at most
+// 55,109, within f16, whose step of 2^-24 the weights share: a weight is off by 2^-37 of
+// the largest one at most.  (With m at the largest logit itself, every row 2^25 below
+// it had no weight: 2,048 equal rows 17 nats below one row of value zero gave zeros.
+// What the room costs in raises: 1,024 queries of 2,048 rows 614 -> 681 us, 64 queries
+// 63.3 -> 69.8 us; with a room of 10, 668 and 68.8 us.)
+constexpr float kRoom = 12.f, kSlack = 15.75f;
 // Tiles whose values are summed in TMEM before the sum moves to memory (to the
 // CTA's own part of the output or of the partials).  The tensor cores cut each
 // accumulation off instead of rounding it, so a sum's error grows with the tiles
@@ -731,8 +735,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     const bool up = tmax > m_fin[h] + kSlack;
                     float a = 1.f;
                     if (up) {
-                        a = exp2f(m_fin[h] - tmax);  // 0 from kNoMax
-                        m_fin[h] = tmax;
+                        a = exp2f(m_fin[h] - (tmax - kRoom));  // 0 from kNoMax
+                        m_fin[h] = tmax - kRoom;
                     }
                     alpha_s[h] = a;
                     const uint32_t mask = __ballot_sync(0xffffffffu, up);
