@@ -732,11 +732,15 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     const int h = threadIdx.x;
                     const float tmax = fval(max(max(red[h], red[kHeads + h]),
                                                 max(red[2 * kHeads + h], red[3 * kHeads + h])));
-                    const bool up = tmax > m_fin[h] + kSlack;
+                    // differences, as in the vote: of logits of millions m + kSlack
+                    // would round up, and a weight to f16's infinity
+                    const bool up = tmax - m_fin[h] > kSlack;
                     float a = 1.f;
                     if (up) {
-                        a = exp2f(m_fin[h] - (tmax - kRoom));  // 0 from kNoMax
-                        m_fin[h] = tmax - kRoom;
+                        const float lower = tmax - kRoom;      // rounded, by 4 where the spacing is 8
+                        const float m_new = tmax - lower > kSlack ? tmax : lower;
+                        a = exp2f(m_fin[h] - m_new);           // 0 from kNoMax
+                        m_fin[h] = m_new;
                     }
                     alpha_s[h] = a;
                     const uint32_t mask = __ballot_sync(0xffffffffu, up);

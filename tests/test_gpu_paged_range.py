@@ -3,7 +3,6 @@ import numpy as np
 import pytest
 import torch
 
-import paged_util as ref
 from test_gpu_paged import SCALE, TDT, AttnCase, _lib  # noqa: F401 (_lib: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +46,31 @@ def test_rows_far_below_a_sink_without_value_make_the_output(n_q, kv, dense, at_
         err = np.sqrt(((out[i] - o) ** 2).sum(1) / (o ** 2).sum(1))
         assert np.all(err <= tol), (i, (err / tol).max())
         assert np.allclose(lse[i], l, rtol=1e-6, atol=0)
+
+
+# ------------------------------------------------------------------ large logits
+
+@pytest.mark.parametrize("n_q", [160, 70, 2])
+@pytest.mark.parametrize("size", [22.2, 23.3, 24.4, 26.5, 27.5, 31.5, 60.5, 100.5])
+def test_finite_logits_of_any_size_give_finite_outputs(size, n_q):
+    """Rows whose logits, about 2^size in log2 units, differ by up to 32 of them:
+    float32 tells them apart to 2^(size - 24) only, but an output is a mean of rows,
+    and the sum of weights lies between one and the number of rows."""
+    c = AttnCase(43, [400], [n_q], page=16, fmt="s8", top_k=300)
+    rng = np.random.default_rng(1)
+    c.scales[:] = 127
+    c.codes[:, :, 512:] = 0
+    c.codes[:, :, 512] = 64
+    c.codes[:, :, 513] = rng.integers(0, 128, c.codes.shape[:2])
+    c.codes[c.table[0, :6], :, 513] //= 4                # the first rows are the lowest
+    q = torch.zeros(n_q, 64, 576)
+    sign = torch.tensor(np.where(rng.random((n_q, 64)) < 0.5, 1.0, -1.0))
+    q[:, :, 512] = (sign * 2.0 ** size / 64 / SCALE / 1.4427).float()
+    q[:, :, 513] = torch.tensor(rng.uniform(0.5, 1.0, (n_q, 64)) * 0.25 / SCALE / 1.4427).float()
+    c.q_abs = q.to(TDT["bf16"])
+    out, lse, code = c.call()
+    assert code == 0
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    assert np.abs(out).max() <= 128.0
+    z = c.q_abs[:, :, 512].double().numpy() * 64 * SCALE
+    assert np.all(np.abs(lse - z) <= 2.0 ** -20 * np.abs(z) + 40)
