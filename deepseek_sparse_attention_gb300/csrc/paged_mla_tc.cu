@@ -200,6 +200,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
     int* e_first = reinterpret_cast<int*>(tmem_slot + 4);            // [4]
     volatile uint32_t* vote = tmem_slot + 8;                         // [3] tiles
+    uint32_t* lacking = tmem_slot + 11;                              // [2] heads without a maximum
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t q = blockIdx.y;
@@ -744,12 +745,18 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     }
                     alpha_s[h] = a;
                     const uint32_t mask = __ballot_sync(0xffffffffu, up);
-                    if (lane == 0) raised_s[warp] = mask;
+                    const uint32_t none = __ballot_sync(0xffffffffu, m_fin[h] == kNoMax);
+                    if (lane == 0) {
+                        raised_s[warp] = mask;
+                        lacking[warp] = none;
+                    }
                 }
                 softmax_sync();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) l_part[e] *= alpha_s[hb + e];
-                have_max = have_max || (raised_s[0] | raised_s[1]) != 0;
+                // with a head that has none yet (logits of -inf so far) the next tile's
+                // logits come here as they are: x - m + m would lose them
+                have_max = (lacking[0] | lacking[1]) == 0;
                 if (t > 0) up = raised_s[warp >> 2];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {

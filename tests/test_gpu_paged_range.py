@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import paged_util as ref
 from test_gpu_paged import SCALE, TDT, AttnCase, _lib  # noqa: F401 (_lib: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +75,37 @@ def test_finite_logits_of_any_size_give_finite_outputs(size, n_q):
     assert np.abs(out).max() <= 128.0
     z = c.q_abs[:, :, 512].double().numpy() * 64 * SCALE
     assert np.all(np.abs(lse - z) <= 2.0 ** -20 * np.abs(z) + 40)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q", [160, 70, 2])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("every", [1, 2])
+def test_logits_beyond_float32_take_no_weight_beside_finite_ones(every, first, n_q, dtype):
+    """Half of the list, whole tiles and splits of it, at about -1e42 for every
+    head, or for every other one."""
+    if dtype == "f32" and n_q == 160:
+        n_q = 40
+    c = AttnCase(49, [640], [n_q], page=16, top_k=480, dtype=dtype, fmt="s8")
+    c.q_abs[:, ::every, 512] = 2.0 ** 20
+    c.q_abs[:, 1::2, 512] = 2.0 ** 20 if every == 1 else 0
+    c.scales[:, 1] = ref.E_MAX + 127
+    c.codes[:, :, 512:] = 0
+    low = np.arange(c.ld) < 20 if first else np.arange(c.ld) >= 20
+    c.codes[c.table[0, :c.ld][low], :, 512] = np.uint8(256 - 100)
+    out, lse, code = c.call()
+    assert code == 0
+    for i in (0, n_q - 1):
+        at = c.idx[i, :c.n_sel[i]]
+        drop = {int(j) for j in at if low[j // 16]}
+        (o, l, weight, reach, floor), n = c.expect(i, drop)
+        tol, tol_lse = ref.attention_bounds(dtype, c.width, n, weight, reach, l, floor)
+        heads = slice(None, None, every)                 # those that give the low rows no weight
+        assert (np.abs(out[i] - o) <= tol)[heads].all() and (np.abs(lse[i] - l) <= tol_lse)[heads].all()
+        if every == 2:
+            (o, l, weight, reach, floor), n = c.expect(i)
+            clean = c.q_abs[i].double().numpy()[1::2]
+            rows, unit = c.rows_of(i)
+            o, l, weight, reach, floor = ref.attention(clean, rows, at, SCALE, unit)
+            tol, tol_lse = ref.attention_bounds(dtype, c.width, n, weight, reach, l, floor)
+            assert (np.abs(out[i, 1::2] - o) <= tol).all() and (np.abs(lse[i, 1::2] - l) <= tol_lse).all()
