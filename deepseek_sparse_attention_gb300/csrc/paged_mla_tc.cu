@@ -9,7 +9,8 @@
 //     z = scale (2^e S_lat + 2^r S_rope),
 //     out = sum_j w_j codes_j / sum_j p_j,  w_j = p_j 2^e_j,
 // with w kept relative to a running maximum of z + e (a row's weight in the
-// output), and p relative to the same maximum with one fixed exponent taken off.
+// output), and p relative to the same maximum with one fixed exponent taken off
+// (kEBase: every exponent a scale may have then keeps p within float32).
 // The query becomes f16 times one power of two per query (its elements span
 // 32 binades exactly; what is below that is below float32's reach too).  w is
 // carried as two f16 parts, hi + lo, to 2^-22 of it or 2^-37 of the largest.
@@ -71,6 +72,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 // What the room costs in raises: 1,024 queries of 2,048 rows 614 -> 681 us, 64 queries
 // 63.3 -> 69.8 us; with a room of 10, 668 and 68.8 us.)
 constexpr float kRoom = 12.f, kSlack = 15.75f;
+// x = z + (e - kEBase): the reference m is kRoom or more below the largest x, so the
+// row there has p = 2^(x - m - (e - kEBase)) >= 2^-121 (e <= 119), 2^28 of float32's
+// smallest steps.  A row of so small a scale that x says little of its p counts
+// for m as if its x were z - kLift, which keeps p <= 2^95.75 and sums of 2^31 rows
+// within float32; its w, at 2^16 less than another's for the append's smallest
+// exponent, is still good to 2^-21.
+constexpr int kEBase = -14;
+constexpr float kLift = 80.f;
+// w stands in for p (times 2^(kEBase - e)) while neither is lost below 2^-126: rows of
+// x - z above kSmall, m set by rows of x - z up to kLarge (p >= 2^-36 there).
+constexpr float kSmall = -60.f, kLarge = 48.f;
 // Tiles whose values are summed in TMEM before the sum moves to memory (to the
 // CTA's own part of the output or of the partials).  The tensor cores cut each
 // accumulation off instead of rounding it, so a sum's error grows with the tiles
@@ -198,7 +210,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     uint32_t* q_max = tmem_slot + 1;
     uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
-    int* e_first = reinterpret_cast<int*>(tmem_slot + 4);            // [4]
+    uint32_t* far_s = tmem_slot + 4;                                 // a row past kLarge met at a raise
     volatile uint32_t* vote = tmem_slot + 8;                         // [3] tiles
     uint32_t* lacking = tmem_slot + 11;                              // [2] heads without a maximum
 
@@ -269,6 +281,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     }
     if (threadIdx.x == 0) {
         *q_max = 0;
+        *far_s = 0;
         mbar_init(q_full, kSoftmaxThreads + kLoaders);
         mbar_init(drain, 1);
         mbar_init(s_full, 1);
@@ -647,12 +660,12 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
         for (int e = 0; e < 16; ++e) l_part[e] = 0.f;
         constexpr int kOBlocks = kLatentBlocks + C::kWide;   // O^T's blocks of 64 columns
-        float* alpha_s = l_fin;                      // rescale factors
-        int e_base = 0;                              // an exponent of the query's rows, taken off theirs
+        float* alpha_s = l_fin;                      // rescale factors, of the sums of p in two parts
+        float* alpha2_s = inv_fin;
         float m[16];                                 // the heads' running maxima
 #pragma unroll
         for (int e = 0; e < 16; ++e) m[e] = kNoMax;
-        bool have_max = false, ok = true;
+        bool have_max = false, far = false, ok = true;
         uint32_t vote_phase = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int bf = t & 1;
@@ -661,23 +674,12 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const uint32_t info = rinfo[bf * kTileRows + srow];
             const bool has = (info & kHasRow) != 0;
             const int e_row = (int)(info & 255u) - 127;
-            if (t == 0) {
-                // the first tile's largest, but for pages of zeros: their exponent
-                // is the least there is, and p counts relative to e_base
-                const int mx = __reduce_max_sync(0xffffffffu, has && e_row > kScaleExpMin ? e_row : -1000);
-                if (lane == 0 && warp < 4) e_first[wq] = mx;
-                softmax_sync();
-                const int em = max(max(e_first[0], e_first[1]), max(e_first[2], e_first[3]));
-                e_base = em == -1000 ? 0 : min(max(em, -120), 120);
-            }
-            // x = z + (e - e_base), -inf without a row; a factor beyond float32
+            // x = z + (e - kEBase), -inf without a row; a factor beyond float32
             // (which multiplies zeros, or gives an infinite logit either way) is capped
             float fa = has ? c2 * e8m0(info & 255u) : 0.f;
             if (fa > 3.4028234e38f) fa = 3.4028234e38f;
-            const float ev = has ? (float)(e_row - e_base) : -INFINITY;
-            // a row of so small a scale counts for the maximum as if it were 2^-96,
-            // for p = 2^(x - m - ev) to stay within float32
-            const float lift = has ? fmaxf(-96.f - ev, 0.f) : 0.f;
+            const float ev = has ? (float)(e_row - kEBase) : -INFINITY;
+            const float lift = has ? fmaxf(-kLift - ev, 0.f) : 0.f;
             float x[16];                             // x[k]: head hb + k
             if constexpr (kParts == 2) {
                 float fb = has ? c2 * e8m0((info >> 8) & 255u) : 0.f;
@@ -724,6 +726,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             }
             if (raise) {
                 const float mx = halving_max(x, lift, lane);
+                if (__any_sync(0xffffffffu, has && ev > kLarge) && lane == 0) *far_s = 1;
                 // in the block that W_hi takes below, free once the scores are formed
                 int* red = reinterpret_cast<int*>(smem + C::off_p(bf));
                 red[wq * kHeads + hb + ((lane >> 1) & 8) + ((lane >> 1) & 4) + ((lane >> 1) & 2) + (lane & 1)] =
@@ -736,14 +739,17 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     // differences, as in the vote: of logits of millions m + kSlack
                     // would round up, and a weight to f16's infinity
                     const bool up = tmax - m_fin[h] > kSlack;
-                    float a = 1.f;
+                    float d = 0.f;
                     if (up) {
                         const float lower = tmax - kRoom;      // rounded, by 4 where the spacing is 8
                         const float m_new = tmax - lower > kSlack ? tmax : lower;
-                        a = exp2f(m_fin[h] - m_new);           // 0 from kNoMax
+                        d = m_fin[h] - m_new;
                         m_fin[h] = m_new;
                     }
-                    alpha_s[h] = a;
+                    // of O^T nothing counts below 2^-120; of the sums of p, which reach
+                    // from 2^127 to 2^-122, it may
+                    alpha_s[h] = exp2f(fmaxf(d, -120.f));
+                    alpha2_s[h] = exp2f(fminf(d + 120.f, 0.f));  // 0 from kNoMax
                     const uint32_t mask = __ballot_sync(0xffffffffu, up);
                     const uint32_t none = __ballot_sync(0xffffffffu, m_fin[h] == kNoMax);
                     if (lane == 0) {
@@ -753,7 +759,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 }
                 softmax_sync();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) l_part[e] *= alpha_s[hb + e];
+                for (int e = 0; e < 16; ++e) l_part[e] = l_part[e] * alpha_s[hb + e] * alpha2_s[hb + e];
+                far = *far_s != 0;
                 // with a head that has none yet (logits of -inf so far) the next tile's
                 // logits come here as they are: x - m + m would lose them
                 have_max = (lacking[0] | lacking[1]) == 0;
@@ -766,15 +773,16 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 }
             }
             // w = 2^(x - m) for the values, p = w 2^-ev for their sum -- by an
-            // exponential of its own where the page's scale is so small that w may
-            // be below float32 where p counts
-            if (__all_sync(0xffffffffu, !has || ev > -60.f)) {
-                const float f = has ? exp2i(e_base - e_row) : 0.f;
+            // exponential of its own (2^20 times it: the exponential ends at 2^-126)
+            // where w may be below float32 and p count
+            if (!far && __all_sync(0xffffffffu, !has || ev > kSmall)) {
+                const float f = has ? exp2i(kEBase - e_row) : 0.f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) l_part[e] = fmaf(w[e], f, l_part[e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) l_part[e] += has ? ex2(x[e] - ev) : 0.f;
+                for (int e = 0; e < 16; ++e)
+                    l_part[e] = fmaf(has ? ex2(x[e] - ev + 20.f) : 0.f, 0x1p-20f, l_part[e]);
             }
             uint8_t* prow = smem + C::off_p(bf) + srow * 128;
             uint8_t* plow = smem + C::kOffPlo + srow * 128;
@@ -900,20 +908,20 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         for (int e = 0; e < 16; ++e) lsc[srow * (kHeads + 1) + hb + e] = l_part[e];
         softmax_sync();
         if (threadIdx.x < kHeads) {
-            // the head's weight: out = O^T 2^e_base / l, log2 of it m + log2 l
+            // the head's weight: out = O^T 2^kEBase / l, log2 of it m + log2 l
             const int h = threadIdx.x;
             float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int r = 0; r < kTileRows; ++r) s4[r & 3] += lsc[r * (kHeads + 1) + h];
             const float l = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            inv_fin[h] = l == 0.f ? 0.f : exp2i(e_base) / l;
+            inv_fin[h] = l == 0.f ? 0.f : exp2i(kEBase) / l;
             m_moved[h] = exp2f(m_moved[h] - m_fin[h]);       // what the moved sums are worth
             m_fin[h] = l == 0.f ? kNoMax : m_fin[h] + log2f(l);
             l_fin[h] = l == 0.f ? 0.f : 1.f;
         }
     }
 
-    // ---- epilogue, warps 0-15: O^T read out of TMEM, times 2^e_base / l
+    // ---- epilogue, warps 0-15: O^T read out of TMEM, times 2^kEBase / l
     if (warp < kMmaWarp) {
         asm volatile("bar.sync 3, %0;" ::"n"(kMergers) : "memory");
         tc_fence_after();

@@ -441,9 +441,9 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  * query element for its head.  float32 accumulation and softmax.  bf16
  * queries run on the tensor cores: the query as f16 times a power of two (exact
  * for elements within 2^-32 of its largest), a row's weight in the output as two
- * f16 parts (2^-22 of it, or 2^-37 of the largest); among the rows of a list no
- * scale may be above 2^100 times those of its first 64 rows (pages of zeros do
- * not count).  Pointers 16-byte aligned
+ * f16 parts (2^-22 of it, or 2^-37 of the largest; 2^-21 of the largest where no
+ * row's scale is above 2^-94).  The scales of a list may be any distance apart.
+ * Pointers 16-byte aligned
  * (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
  * DSA_OP_PAGED_MLA. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,

@@ -109,3 +109,51 @@ def test_logits_beyond_float32_take_no_weight_beside_finite_ones(every, first, n
             o, l, weight, reach, floor = ref.attention(clean, rows, at, SCALE, unit)
             tol, tol_lse = ref.attention_bounds(dtype, c.width, n, weight, reach, l, floor)
             assert (np.abs(out[i, 1::2] - o) <= tol).all() and (np.abs(lse[i, 1::2] - l) <= tol_lse).all()
+
+
+# ------------------------------------------------------------------ scales far apart
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q", [160, 3])
+@pytest.mark.parametrize("order", ["rising", "falling", "any", "low first", "high first", "lowest", "highest"])
+def test_scales_of_any_distance(order, n_q, dtype):
+    """Every exponent the append writes, in one list; the logits come from the
+    rope columns, whose scales are ordinary."""
+    if dtype == "f32" and n_q == 160:
+        n_q = 40
+    c = AttnCase(45, [1800], [n_q], page=16, fmt="s8", dtype=dtype, top_k=1500, spread=4.0)
+    rng = np.random.default_rng(2)
+    pages = c.table[0, :ref.pages_for(1800, 16)]
+    n = len(pages)
+    top = ref.E_MAX if dtype == "bf16" else ref.E_MAX - 14      # the float32 path sums widened rows
+    e = np.rint(np.linspace(ref.E_MIN, top, n)).astype(int)
+    if order == "falling": e = e[::-1]
+    if order == "any": e = rng.permutation(e)
+    if order == "low first": e = np.where(np.arange(n) < n // 2, -105, top - 4)
+    if order == "high first": e = np.where(np.arange(n) < n // 2, top - 4, -105)
+    if order == "lowest": e = np.full(n, ref.E_MIN)
+    if order == "highest": e = np.full(n, top)
+    c.scales[pages, 0] = e + 127
+    c.codes[:, :, :512] = rng.integers(-127, 128, c.codes[:, :, :512].shape).astype(np.int8).view(np.uint8)
+    q = c.q_abs.float()
+    q[:, :, :512] = 0
+    # rows of small pages above those of large ones in the first half of the heads, 40 at most
+    q[:, :, 512] = 0
+    c.codes[:, :, 512] = 0
+    c.codes[pages, :, 512] = np.rint(np.linspace(-100, 100, n)).astype(np.int8).view(np.uint8)[:, None]
+    unit = np.exp2(c.scales[pages[0], 1].astype(float) - 127)
+    c.scales[pages, 1] = c.scales[pages[0], 1]
+    q[:, :, 512] = torch.linspace(-40, 40, 64) / SCALE / 100 / float(unit)
+    c.q_abs = q.to(TDT[dtype])
+    out, lse, code = c.call()
+    assert code == 0
+    some = [0, n_q // 2, n_q - 1]
+    c.check(out, lse, some)
+    # head by head and column by column as close as float32 sums of rows of one sign pattern are:
+    # attention_bounds' relative part, doubled, against the rows' weighted magnitudes
+    for i in some:
+        (o, l, weight, reach, floor), m = c.expect(i)
+        logit = c.width * 2.0 ** -23 * reach
+        rel = 4 * (logit + 2.0 ** -21 + 2.0 ** -23 * reach + 2.0 ** -22) + 2 * (m + 2) * 2.0 ** -23
+        largest = 2.0 ** -36 * floor if dtype == "bf16" else 0.0
+        assert np.all(np.abs(out[i] - o) <= rel * weight + largest + 1e-37)
