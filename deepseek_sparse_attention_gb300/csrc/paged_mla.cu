@@ -97,6 +97,7 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
             __ldg(reinterpret_cast<const float4*>(qsrc + (int64_t)r * W + c));
     }
 
+    bool rows = false;                                 // any that exists
     float m[kWarpHeads], l[kWarpHeads];                // the same in all lanes of the warp
     float4 o[kWarpHeads][kLatent / 128];               // columns 4 lane + 128 i
 #pragma unroll
@@ -143,6 +144,7 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
             }
         }
         __syncthreads();
+        rows |= row_at[rg] >= 0 || row_at[rg + 8] >= 0;
         // the logits of two rows and four heads over a quarter of the columns
         float z[kWarpHeads][2];
         {
@@ -213,10 +215,14 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
     }
 
     const bool last = n_split == 1;
+    rows = __any_sync(0xffffffffu, rows);
 #pragma unroll
     for (int k = 0; k < kWarpHeads; ++k) {
         const int h = h0 + hw + k;
-        const float inv = last ? (l[k] == 0.f ? 0.f : 1.f / l[k]) : 1.f;
+        // rows whose logits are all -inf: NaN, as of any softmax of those, unless
+        // another split has more (m = -inf, l = 1 for the merge)
+        const bool lost = rows && l[k] == 0.f;
+        const float inv = last ? (l[k] == 0.f ? (lost ? NAN : 0.f) : 1.f / l[k]) : 1.f;
         float* dst = (last ? out + (q * kHeads + h) * (int64_t)kLatent
                            : part_o + (part * kHeads + h) * (int64_t)kLatent) + 4 * lane;
 #pragma unroll
@@ -225,11 +231,11 @@ paged_mla_simt(BatchDev b, PagedCache pc, float scale, const float* __restrict__
                 make_float4(o[k][i].x * inv, o[k][i].y * inv, o[k][i].z * inv, o[k][i].w * inv);
         if (lane == 0) {
             if (last) {
-                if (lse != nullptr) lse[q * kHeads + h] = l[k] == 0.f ? -INFINITY : m[k] + logf(l[k]);
+                if (lse != nullptr) lse[q * kHeads + h] = l[k] != 0.f ? m[k] + logf(l[k]) : lost ? NAN : -INFINITY;
             } else {
                 // rows whose logits are all NaN: a split with weight
                 part_ml[(part * kHeads + h) * 2 + 0] = m[k] == -INFINITY && l[k] != 0.f ? 0.f : m[k];
-                part_ml[(part * kHeads + h) * 2 + 1] = l[k];
+                part_ml[(part * kHeads + h) * 2 + 1] = lost ? 1.f : l[k];
             }
         }
     }

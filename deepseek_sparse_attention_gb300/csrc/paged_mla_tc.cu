@@ -210,6 +210,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     uint32_t* q_max = tmem_slot + 1;
     uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
+    volatile uint32_t* rows_s = tmem_slot + 5;                       // any row of the list exists
     uint32_t* far_s = tmem_slot + 4;                                 // a row past kLarge met at a raise
     volatile uint32_t* vote = tmem_slot + 8;                         // [3] tiles
     uint32_t* lacking = tmem_slot + 11;                              // [2] heads without a maximum
@@ -224,7 +225,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     auto owns = [&](int blk) { return !halved || (blk >> 1) == half; };
     // Two splits of a query as a cluster: each stages its output as
     // [head][latent] in its shared memory, with the log2 of its weight in m_fin
-    // and whether it has any in l_fin; then each combines half of the heads from
+    // and whether it has rows in l_fin (all of them of logit -inf: m_fin = -inf);
+    // then each combines half of the heads from
     // both through distributed shared memory.  Every thread of both CTAs calls
     // this once (an empty split with l_fin = 0).
     float* stage = reinterpret_cast<float*>(smem);
@@ -255,7 +257,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             for (int k = 0; k < kEach; ++k) {
                 const int i = threadIdx.x + k * kMergers, h = (kHeads / 2) * rank + i / kC4, c4 = i % kC4;
                 const float l0 = l_fin[h], l1 = f1[k];
-                const float M = fmaxf(m_fin[h], f0[k]);  // kNoMax where there was no row
+                // rows whose logits are all -inf: NaN weights, as of any softmax of those
+                const float M = fmaxf(l0 != 0.f ? m_fin[h] : -INFINITY, l1 != 0.f ? f0[k] : -INFINITY);
                 const float g0 = l0 != 0.f ? exp2f(m_fin[h] - M) : 0.f;
                 const float g1 = l1 != 0.f ? exp2f(f0[k] - M) : 0.f;
                 const float L = g0 + g1;
@@ -282,6 +285,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     if (threadIdx.x == 0) {
         *q_max = 0;
         *far_s = 0;
+        *rows_s = 0;
         mbar_init(q_full, kSoftmaxThreads + kLoaders);
         mbar_init(drain, 1);
         mbar_init(s_full, 1);
@@ -496,6 +500,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 const bool in = (x.has >> lane) & 1u;
                 if (!in && in_list(t)) record_error(err, kDevBadIndex, (int32_t)q, /*where=*/34);
             }
+            if (lane == 0 && x.has != 0) *rows_s = 1;    // read behind the tile's scores
             if ((x.has & 0xffu) != 0xffu) {          // zeros for rows that do not exist
                 if (!((x.has >> r8) & 1u)) {
 #pragma unroll
@@ -674,7 +679,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             const uint32_t info = rinfo[bf * kTileRows + srow];
             const bool has = (info & kHasRow) != 0;
             const int e_row = (int)(info & 255u) - 127;
-            // x = z + (e - kEBase), -inf without a row; a factor beyond float32
+            // x = z + (e - kEBase), -inf without a row (or where z is); a factor beyond float32
             // (which multiplies zeros, or gives an infinite logit either way) is capped
             float fa = has ? c2 * e8m0(info & 255u) : 0.f;
             if (fa > 3.4028234e38f) fa = 3.4028234e38f;
@@ -914,10 +919,17 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
             for (int r = 0; r < kTileRows; ++r) s4[r & 3] += lsc[r * (kHeads + 1) + h];
             const float l = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            inv_fin[h] = l == 0.f ? 0.f : exp2i(kEBase) / l;
             m_moved[h] = exp2f(m_moved[h] - m_fin[h]);       // what the moved sums are worth
-            m_fin[h] = l == 0.f ? kNoMax : m_fin[h] + log2f(l);
-            l_fin[h] = l == 0.f ? 0.f : 1.f;
+            if (l != 0.f) {
+                inv_fin[h] = exp2i(kEBase) / l;
+                m_fin[h] += log2f(l);
+            } else {
+                // no rows, or rows of logit -inf only: NaN unless another split has more
+                const bool rows = *rows_s != 0, nan = rows && n_split == 1;
+                inv_fin[h] = nan ? NAN : 0.f;
+                m_fin[h] = nan ? NAN : rows ? -INFINITY : kNoMax;
+            }
+            l_fin[h] = l != 0.f || *rows_s != 0 ? 1.f : 0.f;
         }
     }
 

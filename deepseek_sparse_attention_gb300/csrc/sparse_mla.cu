@@ -233,7 +233,8 @@ sparse_mla_simt(BatchDev b, float scale, const T* __restrict__ q_abs, const T* _
 // four latent columns per thread; each group keeps a running maximum, and the
 // four groups' (maximum, sum, accumulator) are combined in shared memory.  An
 // empty split has m = -inf: weight 0, and its output (never written) is not
-// used.
+// used.  With `nan_lse` a split of m = -inf whose l is not 0 has rows, all of
+// logit -inf: NaN if no split has others.
 __global__ void __launch_bounds__(128)
 merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __restrict__ part_ml,
              float* __restrict__ out, float* __restrict__ lse, bool nan_lse) {
@@ -254,6 +255,7 @@ merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __r
                        (q * n_split * kHeads + h) * (int64_t)(kLatent / 4) + c4;
     const int64_t o_stride = (int64_t)kHeads * (kLatent / 4);   // float4s between splits
     float M = -INFINITY, L = 0.f;
+    bool rows = false;                                      // met while M is -inf
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = s_lo; s0 < s_hi; s0 += kB) {
         float2 v[kB];
@@ -267,7 +269,11 @@ merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __r
         float Mb = M;
 #pragma unroll
         for (int k = 0; k < kB; ++k) Mb = fmaxf(Mb, v[k].x);
-        if (Mb == -INFINITY) continue;                      // no weight yet
+        if (Mb == -INFINITY) {                              // no weight yet
+#pragma unroll
+            for (int k = 0; k < kB; ++k) rows |= v[k].y != 0.f;
+            continue;
+        }
         const float r = expf(M - Mb);                       // 0 while M is -inf
         L *= r;
         acc.x *= r; acc.y *= r; acc.z *= r; acc.w *= r;
@@ -285,7 +291,7 @@ merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __r
     }
     s_acc[grp][lane] = acc;
     s_m[grp][lane] = M;
-    s_l[grp][lane] = L;
+    s_l[grp][lane] = M == -INFINITY && rows ? 1.f : L;
     __syncthreads();
     if (grp != 0) return;
     float Mt = -INFINITY;
@@ -304,6 +310,14 @@ merge_splits(int32_t n_split, const float* __restrict__ part_o, const float* __r
             at.y = fmaf(a.y, f, at.y);
             at.z = fmaf(a.z, f, at.z);
             at.w = fmaf(a.w, f, at.w);
+        }
+    } else if (nan_lse) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            if (s_l[g][lane] != 0.f) {
+                Lt = NAN;
+                at = make_float4(NAN, NAN, NAN, NAN);
+            }
         }
     }
     const float inv = Lt > 0.f ? 1.f / Lt : 0.f;

@@ -157,3 +157,41 @@ def test_scales_of_any_distance(order, n_q, dtype):
         rel = 4 * (logit + 2.0 ** -21 + 2.0 ** -23 * reach + 2.0 ** -22) + 2 * (m + 2) * 2.0 ** -23
         largest = 2.0 ** -36 * floor if dtype == "bf16" else 0.0
         assert np.all(np.abs(out[i] - o) <= rel * weight + largest + 1e-37)
+
+
+# ------------------------------------------------------------------ infinite queries
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q,top_k,n_sel", [(160, 128, 1), (160, 128, 128), (70, 512, 512), (70, 512, 1),
+                                             (2, 512, 512), (2, 512, 1)])
+@pytest.mark.parametrize("inf", [float("inf"), float("-inf")])
+def test_an_infinite_query_element_gives_nan_whatever_the_signs(inf, n_q, top_k, n_sel, dtype):
+    """Columns 3 (latent) and 520 (rope) hold codes of one sign in every row:
+    the logits are all +inf or all -inf."""
+    c = AttnCase(47, [700], [n_q], page=16, top_k=top_k, dtype=dtype, n_sel=[n_sel] * n_q)
+    for col, sign in ((3, 0x00), (4, 0x80), (520, 0x00), (521, 0x80)):
+        c.codes[:, :, col] = 0x30 | sign
+    heads = {5: 3, 9: 4, 20: 520, 40: 521}
+    clean = c.q_abs.clone()
+    for h, col in heads.items():
+        c.q_abs[:, h, col] = inf
+        clean[:, h] = 0
+    out, lse, code = c.call()
+    assert code == 0
+    bad = sorted(heads)
+    assert np.isnan(out[:, bad]).all() and np.isnan(lse[:, bad]).all()
+    fine = [h for h in range(64) if h not in heads]
+    c.q_abs = clean
+    for i in (0, n_q - 1):
+        (o, l, weight, reach, floor), n = c.expect(i)
+        tol, tol_lse = ref.attention_bounds(dtype, c.width, n, weight, reach, l, floor)
+        assert (np.abs(out[i] - o) <= tol)[fine].all() and (np.abs(lse[i] - l) <= tol_lse)[fine].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinite_query_without_rows_is_an_empty_selection(dtype):
+    c = AttnCase(48, [700] * 3, top_k=512, dtype=dtype, n_sel=[0, 40, 512])
+    c.q_abs[0, 5, 3] = float("inf")
+    out, lse, code = c.call()
+    assert code == 0 and not out[0].any() and np.isneginf(lse[0]).all()
+    c.check(out, lse, [1, 2])
