@@ -11,7 +11,8 @@
 // F + R - 1 - (g_s + j) of the stack: below F that is free_pages, from F on the
 // (entry - F)-th page given back, found by a search in b.  So every column is
 // computed on its own and nothing is read that this launch writes.  If the
-// pages do not suffice no page moves and every slot is -1.
+// pages do not suffice, or F is no height the stack can have, no page moves and
+// every slot is -1.
 //
 // Bound by latency: a step's whole output is tens of bytes a sequence and 8
 // bytes a token.  Up to 1,024 sequences are one launch, in which every CTA scans
@@ -97,23 +98,24 @@ __device__ __forceinline__ void block_scan4(int64_t (&v)[4], int64_t (*warp_tot)
 // not fit: tokens beyond the slot map, a stack higher than its array, too few
 // pages.
 struct Verdict {
-    int64_t F;
-    bool enough;
+    int64_t F;                 // 0 for a height that the stack cannot have
+    bool enough;               // pages move
+    int32_t height;            // n_free_out
 };
 __device__ __forceinline__ Verdict judge(const PagePlanArgs& a, int64_t tokens, int64_t taken,
                                          int64_t back, bool report, int32_t* err) {
-    int64_t f = *a.n_free_in;
-    const bool bad_f = f < 0 || f > a.pg.n_pages;
-    if (bad_f) f = 0;
+    const int32_t given = *a.n_free_in;
+    const bool bad_f = given < 0 || given > a.pg.n_pages;
+    const int64_t f = bad_f ? 0 : given;
     const bool fits = f + back <= a.pg.n_pages;
-    const bool enough = fits && taken <= f + back;
+    const bool enough = !bad_f && fits && taken <= f + back;
     if (report) {
         if (bad_f) record_error(err, kDevBadBatch, -1, /*where=*/30);
         if (tokens > a.max_new) record_error(err, kDevBadBatch, -2, /*where=*/30);
         if (!fits) record_error(err, kDevBadBatch, -3, /*where=*/30);
-        else if (!enough) record_error(err, kDevNoPages, (int32_t)(taken - f - back), /*where=*/30);
+        else if (taken > f + back) record_error(err, kDevNoPages, (int32_t)(taken - f - back), /*where=*/30);
     }
-    return Verdict{f, enough};
+    return Verdict{f, enough, enough ? (int32_t)(f + back - taken) : given};
 }
 
 __global__ void __launch_bounds__(kScanThreads)
@@ -149,7 +151,7 @@ page_plan_scan(PagePlanArgs a, PlanScratch sc, int32_t* err) {
         sc.totals[1] = carry[2];
         sc.totals[2] = carry[3];
         sc.totals[3] = v.enough ? 1 : 0;
-        *a.n_free_out = (int32_t)(v.enough ? v.F + carry[3] - carry[2] : v.F);
+        *a.n_free_out = v.height;
     }
 }
 
@@ -280,7 +282,7 @@ page_plan_small(PagePlanArgs a, uint32_t* ticket, int32_t* err) {
         __threadfence();
         if (atomicAdd(ticket, 1u) == gridDim.x - 1) {
             *ticket = 0;
-            *a.n_free_out = (int32_t)(verdict.enough ? verdict.F + R - A : verdict.F);
+            *a.n_free_out = verdict.height;
         }
     }
     const Plan<uint32_t> p{a, q_off, taken_off, back_off, verdict.F, A, R, verdict.enough};

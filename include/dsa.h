@@ -389,7 +389,8 @@ typedef struct {
  * in the same order.  Entries given back, and free_pages entries from the new
  * height on, are left as they were.  If the free pages do not suffice the error
  * word is set (code 4), no page moves, n_free_out = n_free_in and every slot is
- * -1; row_off and q_off are written all the same.  A row with lengths out of
+ * -1; row_off and q_off are written all the same.  So with n_free_in negative or
+ * above n_pages (code 2).  A row with lengths out of
  * range (negative, q_len > kv_len, more than table_ld pages) sets the error word
  * and counts as empty.  New tokens past max_new set it too and get no slot.
  * Nothing depends on the order in which the GPU runs: the same arguments give
