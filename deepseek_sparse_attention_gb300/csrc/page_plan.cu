@@ -14,6 +14,10 @@
 // pages do not suffice, or F is no height the stack can have, no page moves and
 // every slot is -1.
 //
+// A page that two rows name would be pushed while one of them still reads it, or
+// twice.  Rows' held pages and free pages that are all different are n_pages at
+// most; more of them hold some page twice, and then nothing is given back.
+//
 // Bound by latency: a step's whole output is tens of bytes a sequence and 8
 // bytes a token.  Up to 1,024 sequences are one launch, in which every CTA scans
 // them all for itself (24 KB from L2) and keeps the sums in shared memory for its
@@ -58,26 +62,48 @@ __device__ __forceinline__ SeqPages seq_pages(const PagePlanArgs& a, int64_t s, 
     return p;
 }
 
-// Inclusive prefix sums over the CTA of four values per thread; the totals are
-// left in warp_tot[31].
-__device__ __forceinline__ void block_scan4(int64_t (&v)[4], int64_t (*warp_tot)[4]) {
+constexpr int kScans = 4;                 // rows, tokens, pages taken, pages given back
+constexpr int kSums = 5;                  // and pages held
+
+// What sequence s adds to each.
+__device__ __forceinline__ void seq_sums(const SeqPages& p, int64_t (&v)[kScans], uint32_t& held) {
+    v[0] += p.kv;
+    v[1] += p.q;
+    v[2] += p.need > p.held ? p.need - p.held : 0;
+    v[3] += p.held > p.need ? p.held - p.need : 0;
+    held += (uint32_t)p.held;
+}
+
+// Sum over the warp of numbers below 2^43.
+__device__ __forceinline__ int64_t warp_sum(uint64_t x) {
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)(x & 0xffffu));
+    return ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(x >> 16)) << 16) + lo;
+}
+
+// Inclusive prefix sums over the CTA of kScans values per thread; their totals, and
+// that of `held`, are left in warp_tot[31].
+__device__ __forceinline__ void block_scan(int64_t (&v)[kScans], uint32_t held,
+                                           int64_t (*warp_tot)[kSums]) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int64_t h = warp_sum(held);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kScans; ++k) {
             const int64_t o = __shfl_up_sync(0xffffffffu, v[k], d);
             if (lane >= d) v[k] += o;
         }
     }
     if (lane == 31) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) warp_tot[wid][k] = v[k];
+        for (int k = 0; k < kScans; ++k) warp_tot[wid][k] = v[k];
+        warp_tot[wid][kScans] = h;
     }
     __syncthreads();
     if (wid == 0) {
+        const int64_t all = warp_sum(lane < nw ? warp_tot[lane][kScans] : 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kScans; ++k) {
             int64_t t = lane < nw ? warp_tot[lane][k] : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -86,28 +112,30 @@ __device__ __forceinline__ void block_scan4(int64_t (&v)[4], int64_t (*warp_tot)
             }
             warp_tot[lane][k] = t;
         }
+        warp_tot[lane][kScans] = all;
     }
     __syncthreads();
     if (wid > 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] += warp_tot[wid - 1][k];
+        for (int k = 0; k < kScans; ++k) v[k] += warp_tot[wid - 1][k];
     }
 }
 
 // The stack's height, whether the pages suffice, and the reports of what does
-// not fit: tokens beyond the slot map, a stack higher than its array, too few
-// pages.
+// not fit: tokens beyond the slot map, pages that some rows or the stack name
+// twice, too few pages.
 struct Verdict {
     int64_t F;                 // 0 for a height that the stack cannot have
     bool enough;               // pages move
     int32_t height;            // n_free_out
 };
-__device__ __forceinline__ Verdict judge(const PagePlanArgs& a, int64_t tokens, int64_t taken,
-                                         int64_t back, bool report, int32_t* err) {
+__device__ __forceinline__ Verdict judge(const PagePlanArgs& a, const int64_t (&sum)[kSums],
+                                         bool report, int32_t* err) {
+    const int64_t tokens = sum[1], taken = sum[2], back = sum[3], held = sum[4];
     const int32_t given = *a.n_free_in;
     const bool bad_f = given < 0 || given > a.pg.n_pages;
     const int64_t f = bad_f ? 0 : given;
-    const bool fits = f + back <= a.pg.n_pages;
+    const bool fits = back == 0 || f + held <= a.pg.n_pages;
     const bool enough = !bad_f && fits && taken <= f + back;
     if (report) {
         if (bad_f) record_error(err, kDevBadBatch, -1, /*where=*/30);
@@ -120,8 +148,8 @@ __device__ __forceinline__ Verdict judge(const PagePlanArgs& a, int64_t tokens, 
 
 __global__ void __launch_bounds__(kScanThreads)
 page_plan_scan(PagePlanArgs a, PlanScratch sc, int32_t* err) {
-    __shared__ int64_t warp_tot[kScanThreads / 32][4];
-    int64_t carry[4] = {0, 0, 0, 0};
+    __shared__ int64_t warp_tot[kScanThreads / 32][kSums];
+    int64_t carry[kSums] = {0, 0, 0, 0, 0};
     if (threadIdx.x == 0) {
         a.row_off[0] = 0;
         a.q_off[0] = 0;
@@ -132,9 +160,10 @@ page_plan_scan(PagePlanArgs a, PlanScratch sc, int32_t* err) {
         const int64_t s = s0 + threadIdx.x;
         SeqPages p{0, 0, 0, 0};
         if (s < a.n_seq) p = seq_pages(a, s, err);
-        int64_t v[4] = {p.kv, p.q, p.need > p.held ? p.need - p.held : 0,
-                        p.held > p.need ? p.held - p.need : 0};
-        block_scan4(v, warp_tot);
+        int64_t v[kScans] = {0, 0, 0, 0};
+        uint32_t held = 0;
+        seq_sums(p, v, held);
+        block_scan(v, held, warp_tot);
         if (s < a.n_seq) {
             a.row_off[s + 1] = carry[0] + v[0];
             a.q_off[s + 1] = carry[1] + v[1];
@@ -142,11 +171,11 @@ page_plan_scan(PagePlanArgs a, PlanScratch sc, int32_t* err) {
             sc.back_off[s + 1] = carry[3] + v[3];
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) carry[k] += warp_tot[31][k];
+        for (int k = 0; k < kSums; ++k) carry[k] += warp_tot[31][k];
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        const Verdict v = judge(a, carry[1], carry[2], carry[3], true, err);
+        const Verdict v = judge(a, carry, true, err);
         sc.totals[0] = v.F;
         sc.totals[1] = carry[2];
         sc.totals[2] = carry[3];
@@ -240,24 +269,24 @@ page_plan_fill(PagePlanArgs a, PlanScratch sc, int32_t seq_ctas, int32_t* err) {
 // than 2^27 entries, less than 2^31 of them in all or the plan does not fit.
 __global__ void __launch_bounds__(kSmallThreads)
 page_plan_small(PagePlanArgs a, uint32_t* ticket, int32_t* err) {
-    __shared__ int64_t warp_tot[32][4];
+    __shared__ int64_t warp_tot[32][kSums];
     __shared__ int64_t q_off[kSmallSeqs + 1];
     __shared__ uint32_t taken_off[kSmallSeqs + 1], back_off[kSmallSeqs + 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n = (int)a.n_seq, first = threadIdx.x * kPer;
-    int64_t v[4] = {0, 0, 0, 0}, each[kPer][4];
+    int64_t v[kScans] = {0, 0, 0, 0}, each[kPer][kScans];
+    uint32_t held = 0;                                 // four rows of fewer than 2^27 pages
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         SeqPages p{0, 0, 0, 0};
         if (first + k < n) p = seq_pages(a, first + k, err);
-        each[k][0] = v[0] += p.kv;
-        each[k][1] = v[1] += p.q;
-        each[k][2] = v[2] += p.need > p.held ? p.need - p.held : 0;
-        each[k][3] = v[3] += p.held > p.need ? p.held - p.need : 0;
+        seq_sums(p, v, held);
+#pragma unroll
+        for (int i = 0; i < kScans; ++i) each[k][i] = v[i];
     }
-    int64_t own[4] = {v[0], v[1], v[2], v[3]};
-    block_scan4(v, warp_tot);
+    const int64_t own[kScans] = {v[0], v[1], v[2], v[3]};
+    block_scan(v, held, warp_tot);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int s = first + k;
@@ -276,7 +305,7 @@ page_plan_small(PagePlanArgs a, uint32_t* ticket, int32_t* err) {
         if (blockIdx.x == 0) a.row_off[0] = a.q_off[0] = 0;
     }
     const int64_t A = warp_tot[31][2], R = warp_tot[31][3];
-    const Verdict verdict = judge(a, warp_tot[31][1], A, R, blockIdx.x == 0 && threadIdx.x == 0, err);
+    const Verdict verdict = judge(a, warp_tot[31], blockIdx.x == 0 && threadIdx.x == 0, err);
     __syncthreads();                                   // the offsets are in, n_free_in is read
     if (threadIdx.x == 0) {
         __threadfence();

@@ -355,8 +355,9 @@ dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, c
  *          r % page_rows of page block_table[s][r / page_rows]; entries past a
  *          sequence's rows are not read
  * A code c of a page's part stands for c * 2^(b - 127), c an e4m3 number or a
- * signed integer.  A block table may name a page several times (shared
- * prefixes); a page that a call appends to belongs to one sequence. */
+ * signed integer.  The attention reads a block table that names a page several
+ * times (shared prefixes); a page that a call appends to belongs to one sequence,
+ * and dsa_page_plan gives no pages back while any is shared (see there). */
 typedef enum {
     DSA_CACHE_E4M3 = 0,        /* 8-bit float, 4 exponent and 3 mantissa bits, +-448 */
     DSA_CACHE_S8 = 1           /* 8-bit integer, -127..127                       */
@@ -389,10 +390,16 @@ typedef struct {
  * in the same order.  Entries given back, and free_pages entries from the new
  * height on, are left as they were.  If the free pages do not suffice the error
  * word is set (code 4), no page moves, n_free_out = n_free_in and every slot is
- * -1; row_off and q_off are written all the same.  So with n_free_in negative or
- * above n_pages (code 2).  A row with lengths out of
- * range (negative, q_len > kv_len, more than table_ld pages) sets the error word
- * and counts as empty.  New tokens past max_new set it too and get no slot.
+ * -1; row_off and q_off are written all the same.  So too, with code 2, for an
+ * n_free_in that is negative or above n_pages, and for pages to be given back
+ * when the pages that the rows hold and the free ones are more than n_pages (some
+ * page is named twice).  Pages are not told apart beyond that count: while rows
+ * share pages none may give any back here.  Rows that share may grow; a row that
+ * ends is passed with held_len = kv_len = 0, and the caller, who counts the
+ * sharers, pushes the pages that no row names any more on the stack.
+ * A row with lengths out of range (negative, q_len > kv_len, more than table_ld
+ * pages) sets the error word and counts as empty.  New tokens past max_new set it
+ * too and get no slot.
  * Nothing depends on the order in which the GPU runs: the same arguments give
  * the same tables.  n_seq <= 2^20, max_new < 2^31; pointers 8-byte aligned
  * (int32 ones 4-byte).  Workspace: DSA_OP_PAGE_PLAN, zeroed once
