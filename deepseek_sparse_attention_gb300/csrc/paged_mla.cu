@@ -287,19 +287,29 @@ cudaError_t launch_t(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
 
 }  // namespace
 
-// Rows that a tensor-core CTA takes at a time.
+// Rows that a tensor-core CTA takes at a time; the most rows that are planned by
+// whole tiles.
 constexpr int64_t kPlanTile = 64;
+constexpr int64_t kMostPlanned = 0x7fffffff / kPlanTile * kPlanTile;
 
 void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_split,
                        int32_t* n_split) {
     int64_t main_rows, max_rows;
     paged_rows(sh, b, &main_rows, &max_rows);
     const int32_t n_q = b.n_q > 0 ? b.n_q : 1;
-    if (sh.dtype != DSA_BF16) {
-        plan_splits_simt(n_q, max_rows, rows_per_split, n_split);
-        return;
+    // Whole tiles of the longest bounds would pass 32 bits: the plan is made for less,
+    // and its one split, or one more, takes the rest.
+    const int64_t planned = max_rows < kMostPlanned ? max_rows : kMostPlanned;
+    if (sh.dtype != DSA_BF16)
+        plan_splits_simt(n_q, planned, rows_per_split, n_split);
+    else
+        plan_attention_splits_tc(n_q, main_rows < planned ? main_rows : planned, planned,
+                                 rows_per_split, n_split);
+    if (planned < max_rows) {
+        if (*n_split == 1) *rows_per_split = (int32_t)max_rows;
+        *n_split = (int32_t)((max_rows + *rows_per_split - 1) / *rows_per_split);
     }
-    plan_attention_splits_tc(n_q, main_rows, max_rows, rows_per_split, n_split);
+    if (sh.dtype != DSA_BF16) return;
     // With one query to a sequence the batch's rows bound those of all queries
     // together: splits of r rows then give at most rows / r + n_q CTAs with work,
     // however the lengths differ (the others end at once), so r is chosen for one
