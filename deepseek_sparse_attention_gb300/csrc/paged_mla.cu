@@ -292,6 +292,12 @@ cudaError_t launch_t(const Shape& sh, const BatchDev& b, const PagedCache& pc, c
 constexpr int64_t kPlanTile = 64;
 constexpr int64_t kMostPlanned = 0x7fffffff / kPlanTile * kPlanTile;
 
+// Splits by the rows of all sequences together (below): one query to a sequence, and
+// at least half of the multiprocessors to spare.
+bool decode_batch_plan(const BatchDev& b) {
+    return b.n_q == b.n_seq && sm_count() - b.n_q >= sm_count() / 2;
+}
+
 void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_split,
                        int32_t* n_split) {
     int64_t main_rows, max_rows;
@@ -316,8 +322,8 @@ void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_spl
     // wave of those instead of one wave of the longest sequence's.  Eight dense
     // sequences of 20,000 to 100,003 rows: 227 us with the longest's, 185 us so.
     // The partials grow with the longest sequence's splits: up to four waves' of them.
+    if (!decode_batch_plan(b) || *n_split <= 2) return;
     const int64_t sms = sm_count(), spare = sms - n_q;
-    if (b.n_q != b.n_seq || spare < sms / 2 || *n_split <= 2) return;
     const int64_t tiles = (b.total_rows + kPlanTile - 1) / kPlanTile;
     int64_t rps = (tiles + spare - 1) / spare * kPlanTile;
     if (rps < 2 * kPlanTile) rps = 2 * kPlanTile;
@@ -328,11 +334,27 @@ void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_spl
     *n_split = (int32_t)((max_rows + rps - 1) / rps);
 }
 
+// Partials for the most splits that any batch of these queries with fewer rows could
+// be given, so that a workspace sized for a program's bounds serves all its batches.
 size_t paged_mla_scratch_bytes(const Shape& sh, const BatchDev& b) {
-    int32_t rps, n_split;
-    plan_paged_splits(sh, b, &rps, &n_split);
-    if (n_split == 1) return 0;
-    return (size_t)b.n_q * n_split * kHeads * (kLatent + 2) * sizeof(float);
+    int64_t main_rows, max_rows;
+    paged_rows(sh, b, &main_rows, &max_rows);
+    const int64_t n_q = b.n_q > 0 ? b.n_q : 1, sms = sm_count();
+    const bool tail = main_rows < max_rows;
+    int64_t splits, least;                           // and the fewest rows of one but the last
+    if (sh.dtype != DSA_BF16) {
+        splits = 3 * sms / (kHeads / kGroup) / n_q;
+        least = kTile;
+    } else {
+        splits = decode_batch_plan(b) ? (4 * sms + n_q - 1) / n_q : sms / n_q;
+        least = n_q == 1 ? kPlanTile : 2 * kPlanTile;
+    }
+    const int64_t whole = (max_rows + least - 1) / least;
+    if (splits > whole) splits = whole;
+    if (splits < 1) splits = 1;
+    if (max_rows > kMostPlanned || (sh.dtype == DSA_BF16 && tail)) ++splits;
+    if (splits == 1) return 0;
+    return (size_t)n_q * splits * kHeads * (kLatent + 2) * sizeof(float);
 }
 
 int32_t paged_mla_launches(const Shape& sh, const BatchDev& b) {

@@ -453,7 +453,8 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  * row's scale is above 2^-94).  The scales of a list may be any distance apart.
  * Pointers 16-byte aligned
  * (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
- * DSA_OP_PAGED_MLA. */
+ * DSA_OP_PAGED_MLA; it serves every batch of as many sequences and queries, and
+ * the same flags, whose rows are fewer. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,
                               const dsa_pages *pages, const void *q_abs, const void *codes,
                               const void *scales, const int32_t *block_table, const int32_t *idx,

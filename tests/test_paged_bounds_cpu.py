@@ -13,3 +13,32 @@ def test_splits_cover_every_row_of_the_longest_bound(lib, max_kv, n_q, dtype):
                         dsa.OP_PAGED_MLA)
     assert info["attn_rows_per_split"] > 0
     assert info["attn_splits"] * info["attn_rows_per_split"] >= max_kv
+
+
+def _rows_batch(n_seq, max_kv, total, flags):
+    b = _batch(n_seq, n_seq, 1, max_kv, flags)
+    b.total_rows = total
+    return b
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top_k,kpool", [(2048, 1), (2048, 4), (64, 4), (128, 4), (320, 1)])
+@pytest.mark.parametrize("flags", [0, dsa.FLAG_DENSE])
+@pytest.mark.parametrize("n_seq", [1, 2, 3, 8, 40, 76, 77, 152, 153, 400])
+def test_a_workspace_serves_every_batch_of_fewer_rows(lib, n_seq, flags, top_k, kpool, dtype):
+    """A program sizes its workspace once, for the longest sequences and the most
+    rows it will ever have."""
+    sh = dsa.make_shape(dtype=dtype, top_k=top_k, kpool=kpool)
+    lengths = [1, 63, 64, 65, 66, 67, 68, 127, 128, 130, 131, 132, 200, 320, 1000, 2048, 2050, 2051, 2052,
+               3000, 9000, 20011, 100003, 131072, 1 << 20, 1 << 30, (1 << 31) - 1]
+    largest = 0
+    for max_kv in lengths:
+        size = dsa.dsa_workspace_size(sh, _rows_batch(n_seq, max_kv, n_seq * max_kv, flags),
+                                      dsa.OP_PAGED_MLA)
+        for part in (1, 2, 3, 5, 9, 20, 100, 5000):
+            b = _rows_batch(n_seq, max_kv, max(n_seq * max_kv // part, 1), flags)
+            assert dsa.dsa_workspace_size(sh, b, dsa.OP_PAGED_MLA) == size
+            splits = dsa.dsa_plan(sh, b, dsa.OP_PAGED_MLA)["attn_splits"]
+            assert splits == 1 or n_seq * splits * 64 * 514 * 4 < size
+        assert size >= largest
+        largest = size
