@@ -333,11 +333,19 @@ def _at(t, dtype, device: int, least: int, what: str) -> int:
 
 def _bytes_at(t, device: int, count: int, what: str) -> int:
     """Address of a tensor of `count` one-byte elements of any type."""
+    if t is None:
+        raise ValueError(f"{what} is missing")
     if t.element_size() != 1 or t.numel() != count:
         raise ValueError(f"{what} holds {count} one-byte elements")
     if t.get_device() != device or not t.is_contiguous():
         _refuse(t, t.dtype, device, 0, what)
     return t.data_ptr()
+
+
+def _count(t, what: str) -> int:
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    return t.numel()
 
 
 def _stream_at(stream, device: int) -> int:
@@ -351,9 +359,10 @@ def dsa_page_plan(pages, held_len, kv_len, q_len, free_pages, n_free, block_tabl
     """Block tables, slot map (``slots``, one entry per new token) and batch
     offsets from request lengths (see dsa.h); ``n_free_out=None`` updates
     ``n_free`` in place."""
-    n, i64, i32, d = held_len.numel(), torch.int64, torch.int32, torch.cuda.current_device()
+    i64, i32, d = torch.int64, torch.int32, torch.cuda.current_device()
+    n, max_new = _count(held_len, "held_len"), _count(slots, "slots")
     free = _at(n_free, i32, d, 1, "n_free")
-    _call("dsa_page_plan", pages, n, slots.numel(), _at(held_len, i64, d, n, "held_len"),
+    _call("dsa_page_plan", pages, n, max_new, _at(held_len, i64, d, n, "held_len"),
           _at(kv_len, i64, d, n, "kv_len"), _at(q_len, i64, d, n, "q_len"),
           _at(free_pages, i32, d, pages.n_pages, "free_pages"), free,
           free if n_free_out is None else _at(n_free_out, i32, d, 1, "n_free_out"),

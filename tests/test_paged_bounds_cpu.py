@@ -1,8 +1,9 @@
 """Host side of the paged 8-bit cache at the ends of its bounds."""
 import pytest
+import torch
 
 import deepseek_sparse_attention_gb300 as dsa
-from test_paged_cpu import _batch, lib  # noqa: F401 (lib: the module's fixture)
+from test_paged_cpu import _batch, _pages, lib  # noqa: F401 (lib: the module's fixture)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -42,3 +43,32 @@ def test_a_workspace_serves_every_batch_of_fewer_rows(lib, n_seq, flags, top_k, 
             assert splits == 1 or n_seq * splits * 64 * 514 * 4 < size
         assert size >= largest
         largest = size
+
+
+def test_binding_names_a_missing_tensor(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    sh, b, pg = dsa.make_shape(), _batch(), _pages(64, 2, 4)
+    i64, i32 = torch.int64, torch.int32
+
+    class Fine:                                       # a tensor of the current device
+        is_cuda = True
+
+        def __init__(self, dtype):
+            self.dtype = dtype
+
+        def numel(self): return 1 << 20
+        def get_device(self): return 0
+        def is_contiguous(self): return True
+        def data_ptr(self): return 256
+
+    bf16 = Fine(torch.bfloat16)
+    with pytest.raises(ValueError, match="codes is missing"):
+        dsa.dsa_cache_append(sh, b, pg, bf16, Fine(i64), None, None, None)
+    with pytest.raises(ValueError, match="codes is missing"):
+        dsa.dsa_paged_mla_attn(sh, b, pg, bf16, None, None, None, None, None, None, None, None)
+    with pytest.raises(ValueError, match="held_len is missing"):
+        dsa.dsa_page_plan(pg, None, None, None, Fine(i32), Fine(i32), Fine(i32), Fine(i64), Fine(i64),
+                          Fine(i64), None)
+    with pytest.raises(ValueError, match="slots is missing"):
+        dsa.dsa_page_plan(pg, Fine(i64), Fine(i64), Fine(i64), Fine(i32), Fine(i32), Fine(i32), Fine(i64),
+                          Fine(i64), None, None)
