@@ -448,11 +448,11 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  * attended row gives NaN outputs and a NaN lse, and so does an infinite or NaN
  * query element for its head.  float32 accumulation and softmax.  bf16
  * queries run on the tensor cores: the query as f16 times a power of two (exact
- * for elements within 2^-32 of its largest), a row's weight in the output as two
- * f16 parts (2^-22 of it, or 2^-37 of the largest; 2^-21 of the largest where no
- * row's scale is above 2^-94).  The scales of a list may be any distance apart.
- * Pointers 16-byte aligned
- * (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
+ * for elements down to 2^-31 of the query's largest over all its heads, to 2^-39
+ * of that below), a row's weight in the output as two f16 parts (2^-22 of it, or
+ * 2^-37 of the largest; 2^-21 of the largest where no row's scale is above
+ * 2^-94).  The scales of a list may be any distance apart.  Pointers 16-byte
+ * aligned (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
  * DSA_OP_PAGED_MLA; it serves every batch of as many sequences and queries, and
  * the same flags, whose rows are fewer. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,

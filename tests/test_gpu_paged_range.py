@@ -195,3 +195,41 @@ def test_an_infinite_query_without_rows_is_an_empty_selection(dtype):
     out, lse, code = c.call()
     assert code == 0 and not out[0].any() and np.isneginf(lse[0]).all()
     c.check(out, lse, [1, 2])
+
+
+# ------------------------------------------------------------------ queries of any size
+
+@pytest.mark.parametrize("n_q", [160, 2])
+@pytest.mark.parametrize("size", [-133, -125, -110, -90, 0, 90])
+def test_queries_of_any_size_keep_their_logits(size, n_q):
+    """Elements around 2^size, rows as large as it takes for logits of order one
+    (2^110 at most)."""
+    c = AttnCase(51, [300], [n_q], page=16, top_k=256)
+    c.q_abs = (c.q_abs.double() * 2.0 ** size).to(TDT["bf16"])
+    c.scales = (c.scales.astype(int) + np.clip(-size, -90, 110)).astype(np.uint8)
+    out, lse, code = c.call()
+    assert code == 0
+    c.check(out, lse, [0, n_q - 1])
+
+
+@pytest.mark.parametrize("n_q", [160, 2])
+@pytest.mark.parametrize("largest", [1.0, 1.9921875])
+def test_elements_down_to_2_to_the_minus_31_of_the_largest_count(largest, n_q):
+    """One element decides each logit: a large one, which meets zeros, lies 2^31
+    above it."""
+    c = AttnCase(53, [300], [n_q], page=16, top_k=256, fmt="s8")
+    rng = np.random.default_rng(4)
+    c.codes[:, :, 512:] = 0
+    c.codes[:, :, 513] = rng.integers(0, 128, c.codes.shape[:2])
+    c.scales[:, 1] = 127
+    q = torch.zeros(n_q, 64, 576, dtype=torch.float64)
+    q[:, :, 513] = 1.9921875                             # 8 significant bits
+    q[:, :, 514] = 2.0 ** 31 * largest
+    c.q_abs = q.to(TDT["bf16"])
+    out, lse, code = c.call()
+    assert code == 0
+    c.check(out, lse, [0, n_q - 1])
+    # as good as if the element were alone
+    c.q_abs[:, :, 514] = 0
+    alone = c.call()
+    assert np.array_equal(out, alone[0]) and np.array_equal(lse, alone[1])
