@@ -444,7 +444,8 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  *   bound each sequence's keys as for the other entry points
  *   codes, scales, block_table as above
  * An index outside [0, L), or one whose block-table entry is no page of the
- * pool, sets the error word and its row is skipped.  A NaN code or scale of an
+ * pool, sets the error word and its row is skipped.  A query that the offsets do
+ * not cover sets it too; its out and lse are of no meaning.  A NaN code or scale of an
  * attended row gives NaN outputs and a NaN lse, and so does an infinite or NaN
  * query element for its head.  float32 accumulation and softmax.  bf16
  * queries run on the tensor cores: the query as f16 times a power of two (exact
