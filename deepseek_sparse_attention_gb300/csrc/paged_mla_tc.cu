@@ -157,6 +157,15 @@ __device__ __forceinline__ void ldg_32bytes(const uint8_t* p, uint32_t (&r)[8]) 
 // Packed scales of a tile's row: the bytes of its two parts and this flag.
 constexpr uint32_t kHasRow = 0x10000u;
 
+// A wait of all lanes of a warp, which go on or give up together: what follows
+// synchronises or is .aligned.  (A last test behind the time limit: the whole CTA may
+// have been off the multiprocessor meanwhile.  The votes cost 1,024 queries 698 ->
+// 708 us.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    const bool in = mbar_wait(bar, parity, kWaitNs) || mbar_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, in);
+}
+
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
 }
@@ -214,7 +223,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
     uint32_t* raised_s = tmem_slot + 2;                              // [2] heads, a bit each
     volatile uint32_t* rows_s = tmem_slot + 5;                       // any row of the list exists
     uint32_t* far_s = tmem_slot + 4;                                 // a row past kLarge met at a raise
-    volatile uint32_t* vote = tmem_slot + 8;                         // [3] tiles
+    // [3] tiles: the votes for a raise, and against any (16 bits each)
+    volatile uint16_t* vote = reinterpret_cast<volatile uint16_t*>(tmem_slot + 8);
     uint32_t* lacking = tmem_slot + 11;                              // [2] heads without a maximum
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -293,7 +303,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         mbar_init(s_full, 1);
         mbar_init(s_free, kSoftmaxThreads);
         mbar_init(votes, kSoftmaxThreads / 32);
-        vote[0] = vote[1] = vote[2] = 0;
+        for (int i = 0; i < 6; ++i) vote[i] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&p_full[i], kSoftmaxThreads);
             for (int g = 0; g < C::kPieces; ++g)      // arrivals of warps
@@ -521,7 +531,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
             for (int i = 0; i < kLatentBlocks; ++i) {
                 // the piece's columns have been read by tile t - 2's value product
-                if (t >= 2 && ok) ok = mbar_wait(&freed[buf * kLatentBlocks + i], phase, kWaitNs);
+                if (t >= 2 && ok) ok = warp_wait(&freed[buf * kLatentBlocks + i], phase);
                 if (!ok) return;
                 if (i == 0 && lane < 8)
                     rinfo[buf * kTileRows + rows0 + lane] =
@@ -674,7 +684,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         uint32_t vote_phase = 0;
         for (int t = 0; t < n_tiles; ++t) {
             const int bf = t & 1;
-            if (ok) ok = mbar_wait(s_full, (uint32_t)(t & 1), kWaitNs);
+            if (ok) ok = warp_wait(s_full, (uint32_t)(t & 1));
             tc_fence_after();
             const uint32_t info = rinfo[bf * kTileRows + srow];
             const bool has = (info & kHasRow) != 0;
@@ -713,17 +723,22 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                     top = fmaxf(top, x[e]);
                 }
                 const bool any = __any_sync(0xffffffffu, top + lift > kSlack);
+                // a warp of which a wait has failed votes against: all warps must meet at
+                // the same barriers to the end, whatever is in the scores by then
                 if (lane == 0) {
-                    if (any) vote[t % 3] = 1;
+                    if (any) vote[2 * (t % 3)] = 1;
+                    if (!ok) vote[2 * (t % 3) + 1] = 1;
                     mbar_arrive(votes);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = ex2(x[e]);
-                if (ok) ok = mbar_wait(votes, vote_phase, kWaitNs);
+                if (ok) ok = warp_wait(votes, vote_phase);
                 vote_phase ^= 1u;
-                raise = vote[t % 3] != 0;
+                const uint32_t cast = *reinterpret_cast<volatile uint32_t*>(vote + 2 * (t % 3));
+                raise = ok && cast == 1u;
                 // the last tile's vote, which every warp has read, for the one after next
-                if (threadIdx.x == 0) vote[(t + 2) % 3] = 0;
+                if (threadIdx.x == 0)
+                    *reinterpret_cast<volatile uint32_t*>(vote + 2 * ((t + 2) % 3)) = 0;
                 if (raise) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[e] += m[e];
@@ -809,8 +824,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             }
             // the previous tile's value products read W_lo
             if (t > 0 && ok)
-                ok = mbar_wait(&freed[((t - 1) & 1) * kLatentBlocks + kLatentBlocks - 1],
-                               (uint32_t)(((t - 1) >> 1) & 1), kWaitNs);
+                ok = warp_wait(&freed[((t - 1) & 1) * kLatentBlocks + kLatentBlocks - 1],
+                               (uint32_t)(((t - 1) >> 1) & 1));
             // O^T, whose products so far are in (before the exponentials this held
             // them up: 64 queries 67.8 us, so 65.7 us)
             if (up != 0) {
@@ -903,8 +918,8 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
         }
         {
             const int tl = n_tiles - 1;
-            if (ok) ok = mbar_wait(&freed[(tl & 1) * kLatentBlocks + kLatentBlocks - 1],
-                                   (uint32_t)((tl >> 1) & 1), kWaitNs);
+            if (ok) ok = warp_wait(&freed[(tl & 1) * kLatentBlocks + kLatentBlocks - 1],
+                                   (uint32_t)((tl >> 1) & 1));
         }
         if (!ok) record_error(err, kDevTimeout, (int32_t)q, /*where=*/37);
         // row sums to shared memory (the row buffers are free now)
