@@ -320,7 +320,7 @@ void plan_paged_splits(const Shape& sh, const BatchDev& b, int32_t* rows_per_spl
     // together: splits of r rows then give at most rows / r + n_q CTAs with work,
     // however the lengths differ (the others end at once), so r is chosen for one
     // wave of those instead of one wave of the longest sequence's.  Eight dense
-    // sequences of 20,000 to 100,003 rows: 227 us with the longest's, 185 us so.
+    // sequences of 20,000 to 100,003 rows: 230 us with the longest's, 174 us so.
     // The partials grow with the longest sequence's splits: up to four waves' of them.
     if (!decode_batch_plan(b) || *n_split <= 2) return;
     const int64_t sms = sm_count(), spare = sms - n_q;

@@ -24,8 +24,8 @@
 //               128-byte swizzle.  A buffer is handed over in pieces of 128
 //               columns, all warps on one piece after the other: a piece is
 //               refilled as soon as the value product has read it, and the next
-//               scores start as soon as their first is in (with two warps to each
-//               piece 64 queries of 2,048 rows took 71 us, so 68 us);
+//               scores start as soon as their first is in (5% less time for 64
+//               queries of 2,048 rows than with two warps to each piece);
 //   warp 16     issues S^T = R . Q^T (M = 64 rows, N = 64 heads, K = the row)
 //               and O^T += R^T . W^T (M = 128 latent columns, K = 64 rows), the
 //               scores of tile t + 1 before the values of tile t;
@@ -71,8 +71,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 55,109, within f16, whose step of 2^-24 the weights share: a weight is off by 2^-37 of
 // the largest one at most.  (With m at the largest logit itself, every row 2^25 below
 // it had no weight: 2,048 equal rows 17 nats below one row of value zero gave zeros.
-// What the room costs in raises: 1,024 queries of 2,048 rows 614 -> 681 us, 64 queries
-// 63.3 -> 69.8 us; with a room of 10, 668 and 68.8 us.)
+// What the room costs in raises: 1,024 queries of 2,048 rows 644 us without, 704 us so,
+// 64 queries 64.9 and 70.7 us; with a room of 10, 692 and 69.7 us.)
 constexpr float kRoom = 12.f, kSlack = 15.75f;
 // x = z + (e - kEBase): the reference m is kRoom or more below the largest x, so the
 // row there has p = 2^(x - m - (e - kEBase)) >= 2^-121 (e <= 119), 2^28 of float32's
@@ -90,8 +90,8 @@ constexpr float kSmall = -60.f, kLarge = 48.f;
 // accumulation off instead of rounding it, so a sum's error grows with the tiles
 // in it: relative to the output, against 64 bits, 0.3e-6 for 2 tiles, 1.2e-6 for
 // 16, 1.6e-6 for 32, where float32 sums have 0.5e-6.  Moved every 11 tiles it is
-// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows take 573 us without and
-// 632 us so (every 16 tiles: half of that, and errors above 1e-6).
+// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows take 644 us without and
+// 704 us so (every 16 tiles 666 us, and errors above 1e-6).
 constexpr int kFlushTiles = 11;
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any row
 constexpr int kSoftmaxThreads = 256;
@@ -827,7 +827,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 ok = warp_wait(&freed[((t - 1) & 1) * kLatentBlocks + kLatentBlocks - 1],
                                (uint32_t)(((t - 1) >> 1) & 1));
             // O^T, whose products so far are in (before the exponentials this held
-            // them up: 64 queries 67.8 us, so 65.7 us)
+            // them up: 3% of the time of 64 queries)
             if (up != 0) {
                 tc_fence_after();
                 // eight heads at a time, in each of O^T's blocks of 64 columns

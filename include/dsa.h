@@ -344,8 +344,11 @@ dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, c
 /* The paged 8-bit cache
  * ---------------------
  * The latent cache as a pool of pages instead of packed sequences, its values
- * held in 8 bits: half of a bf16 row's bytes, and sequences that grow without
- * moving.  The pages have no counterpart: the layout is this library's (one of
+ * held in 8 bits: half of a bf16 row's bytes, and latent rows that grow without
+ * moving.  The indexer's keys stay packed by sequence, as step 1 reads them, and
+ * the step as a whole (dsa_decode_step and the like) reads the packed cache only:
+ * over this one a step is dsa_page_plan, dsa_cache_append, dsa_index_select and
+ * dsa_paged_mla_attn.  The pages have no counterpart: the layout is this library's (one of
  * them names an 8-bit MLA cache, without its format).
  *   codes  [n_pages, page_rows, W] 8-bit, W = kv_lora + rope_dim
  *   scales [n_pages, parts] uint8: one E8M0 byte b per page and part of a row
