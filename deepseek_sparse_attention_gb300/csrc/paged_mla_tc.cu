@@ -727,7 +727,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 // the same barriers to the end, whatever is in the scores by then
                 if (lane == 0) {
                     if (any) vote[2 * (t % 3)] = 1;
-                    if (!ok) vote[2 * (t % 3) + 1] = 1;
+                    if (!ok) vote[1] = vote[3] = vote[5] = 1;    // for good
                     mbar_arrive(votes);
                 }
 #pragma unroll
@@ -737,8 +737,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 const uint32_t cast = *reinterpret_cast<volatile uint32_t*>(vote + 2 * (t % 3));
                 raise = ok && cast == 1u;
                 // the last tile's vote, which every warp has read, for the one after next
-                if (threadIdx.x == 0)
-                    *reinterpret_cast<volatile uint32_t*>(vote + 2 * ((t + 2) % 3)) = 0;
+                if (threadIdx.x == 0) vote[2 * ((t + 2) % 3)] = 0;
                 if (raise) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[e] += m[e];
