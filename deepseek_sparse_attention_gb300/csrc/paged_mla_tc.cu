@@ -858,16 +858,17 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             fence_proxy_async_smem();
             if (t > 0 && t % kFlushTiles == 0) {
                 // O^T moves to memory, as multiples of 2^m of the move that began a
-                // head's sum: added to it, or beginning it anew where m has grown so
-                // far that what is there no longer counts.
+                // head's sum, and is added to it.  Where m has grown by more than float32
+                // has room for, what is there is brought to the present 2^m first.
                 softmax_sync();                      // alpha_s is read
                 tc_fence_after();
                 if (threadIdx.x < kHeads) {
                     const int h = threadIdx.x;
-                    const float grown = m_fin[h] - m_moved[h];
-                    const bool anew = t == kFlushTiles || grown > 80.f;
-                    if (anew) m_moved[h] = m_fin[h];
+                    const float grown = t == kFlushTiles ? 0.f : m_fin[h] - m_moved[h];
+                    const bool anew = grown > 80.f;
+                    if (anew || t == kFlushTiles) m_moved[h] = m_fin[h];
                     alpha_s[h] = anew ? 1.f : exp2f(grown);
+                    alpha2_s[h] = anew ? exp2f(-grown) : 1.f;
                     const uint32_t mask = __ballot_sync(0xffffffffu, anew);
                     if (lane == 0) raised_s[warp] = mask;
                 }
@@ -895,15 +896,18 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
                                 if (wide) v[8 * i + c] += v[(8 * i + c + 8) & 31];
-                            if (((mask >> (8 * g)) & 255u) == 255u) {   // a first move
+                            if (t == kFlushTiles) {                  // a first move
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) dst[c * kLatent] = v[8 * i + c];
                                 continue;
                             }
+                            if (((mask >> (8 * g)) & 255u) != 0) {  // far grown heads among these
+#pragma unroll 1
+                                for (int c = 0; c < 8; ++c) dst[c * kLatent] = __ldcg(dst + c * kLatent) * alpha2_s[h + c];
+                            }
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
-                                if ((mask >> (8 * g + c)) & 1u) dst[c * kLatent] = v[8 * i + c];
-                                else atomicAdd(dst + c * kLatent, v[8 * i + c] * alpha_s[h + c]);
+                                atomicAdd(dst + c * kLatent, v[8 * i + c] * alpha_s[h + c]);
                             }
                         }
                     }

@@ -233,3 +233,43 @@ def test_elements_down_to_2_to_the_minus_31_of_the_largest_count(largest, n_q):
     c.q_abs[:, :, 514] = 0
     alone = c.call()
     assert np.array_equal(out, alone[0]) and np.array_equal(lse, alone[1])
+
+
+# ------------------------------------------------------------------ sums of long lists
+
+@pytest.mark.parametrize("rope_fmt", ["s8", "e4m3"])
+@pytest.mark.parametrize("n_q", [160, 70])
+@pytest.mark.parametrize("steps", [(0, 40, 44, 44, 44), (0, 36, 44, 44, 40), (0, 20, 36, 44, 44), (0, 0, 40, 44, 48),
+                                   (0, 44, 44, 44, 44), (0, 36, 44, 72, 80), (80, 44, 0, 40, 80), (0, 120, 112, 120, 120)])
+def test_logits_that_climb_by_hundreds_of_binades(steps, n_q, rope_fmt):
+    """Five stretches of some 700 rows whose logits are 2 steps[k] in log2 units,
+    each with values in columns of its own: every column is one stretch's output.
+    A stretch ends with the tile in which sums leave the accumulators."""
+    kv = 3500
+    c = AttnCase(55, [kv], [n_q], page=16, fmt="s8", dense=True)
+    pos = np.arange(c.ld * 16)
+    part = np.searchsorted([768, 1472, 2176, 2880], pos, side="right")
+    page, row = c.table[0][pos // 16], pos % 16
+    codes = np.zeros((len(pos), 576), dtype=np.int8)
+    rng = np.random.default_rng(5)
+    for k in range(5):
+        codes[part == k, 100 * k:100 * k + 100] = rng.integers(1, 128, ((part == k).sum(), 100))
+    codes[:, 512] = np.array(steps)[part]
+    c.codes[page, row] = codes.view(np.uint8)
+    c.scales[:] = 127
+    if rope_fmt == "e4m3":                               # the same in the other format
+        c.fmt = "e4m3"
+        c.codes[page, row] = ref.encode(codes.astype(float), "e4m3")
+    q = torch.zeros(n_q, 64, 576)
+    q[:, :, 512] = 22.125
+    c.q_abs = q.to(TDT["bf16"])
+    out, lse, code = c.call()
+    assert code == 0
+    for i in (0, n_q - 1):
+        (o, l, weight, reach, floor), n = c.expect(i)
+        # a logit is one product here, exact in float32 but for its rounding, twice: 2^-22 of it, as
+        # much of a weight; sums of 700 rows and more, cut off: (n + 2) 2^-23; a weight to 2^-21; and
+        # 2^-37 of the largest weight for each of a stretch's rows
+        rel = 2 * (2.0 ** -22 * reach + 2.0 ** -21) + (n + 2) * 2.0 ** -23
+        assert np.all(np.abs(out[i] - o) <= rel * np.abs(o) + 2.0 ** -37 * floor + 1e-37), i
+        assert np.all(np.abs(lse[i] - l) <= 2.0 ** -21 * np.abs(l) + n * 2.0 ** -23)
