@@ -75,13 +75,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 64 queries 64.9 and 70.7 us; with a room of 10, 692 and 69.7 us.)
 constexpr float kRoom = 12.f, kSlack = 15.75f;
 // x = z + (e - kEBase): the reference m is kRoom or more below the largest x, so the
-// row there has p = 2^(x - m - (e - kEBase)) >= 2^-121 (e <= 119), 2^28 of float32's
+// row there has p = 2^(x - m - (e - kEBase)) >= 2^-115 (e <= 119), 2^34 of float32's
 // smallest steps.  A row of so small a scale that x says little of its p counts
-// for m as if its x were z - kLift, which keeps p <= 2^95.75 and sums of 2^31 rows
-// within float32; its w, at 2^16 less than another's for the append's smallest
-// exponent, is still good to 2^-21.
-constexpr int kEBase = -14;
-constexpr float kLift = 80.f;
+// for m as if its x were z - kLift, which keeps p <= 2^101.75 and sums of 2^25 such
+// rows within float32; its w, at 2^16 less than another's for the append's smallest
+// exponent, is still good to 2^-21.  x is rounded with the exponent in it, to 2^-24 of
+// its size: kEBase is the exponent of pages of values up to 1.75 (e4m3), so that this
+// is z's own rounding for usual caches.
+constexpr int kEBase = -8;
+constexpr float kLift = 86.f;
 // w stands in for p (times 2^(kEBase - e)) while neither is lost below 2^-126: rows of
 // x - z above kSmall, m set by rows of x - z up to kLarge (p >= 2^-36 there).
 constexpr float kSmall = -60.f, kLarge = 48.f;
@@ -766,7 +768,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                         m_fin[h] = m_new;
                     }
                     // of O^T nothing counts below 2^-120; of the sums of p, which reach
-                    // from 2^127 to 2^-122, it may
+                    // from 2^127 to 2^-115, it may
                     alpha_s[h] = exp2f(fmaxf(d, -120.f));
                     alpha2_s[h] = exp2f(fminf(d + 120.f, 0.f));  // 0 from kNoMax
                     const uint32_t mask = __ballot_sync(0xffffffffu, up);
@@ -792,7 +794,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
                 }
             }
             // w = 2^(x - m) for the values, p = w 2^-ev for their sum -- by an
-            // exponential of its own (2^20 times it: the exponential ends at 2^-126)
+            // exponential of its own (2^16 times it: the exponential ends at 2^-126)
             // where w may be below float32 and p count
             if (!far && __all_sync(0xffffffffu, !has || ev > kSmall)) {
                 const float f = has ? exp2i(kEBase - e_row) : 0.f;
@@ -801,7 +803,7 @@ paged_mla_tc(const __nv_bfloat16* __restrict__ q_abs, PagedCache pc, BatchDev b,
             } else {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    l_part[e] = fmaf(has ? ex2(x[e] - ev + 20.f) : 0.f, 0x1p-20f, l_part[e]);
+                    l_part[e] = fmaf(has ? ex2(x[e] - ev + 16.f) : 0.f, 0x1p-16f, l_part[e]);
             }
             uint8_t* prow = smem + C::off_p(bf) + srow * 128;
             uint8_t* plow = smem + C::kOffPlo + srow * 128;

@@ -448,17 +448,18 @@ dsa_status dsa_cache_append(const dsa_shape *shape, const dsa_batch *batch, cons
  *   codes, scales, block_table as above
  * An index outside [0, L), or one whose block-table entry is no page of the
  * pool, sets the error word and its row is skipped.  A query that the offsets do
- * not cover sets it too; its out and lse are of no meaning.  A NaN code or scale of an
- * attended row gives NaN outputs and a NaN lse, and so does an infinite or NaN
- * query element for its head.  float32 accumulation and softmax.  bf16
+ * not cover sets it too; its out and lse are of no meaning.  A NaN code or scale
+ * of an attended row gives NaN outputs and a NaN lse, and so does an infinite or
+ * NaN query element for its head.  float32 accumulation and softmax.  bf16
  * queries run on the tensor cores: the query as f16 times a power of two (exact
  * for elements down to 2^-31 of the query's largest over all its heads, to 2^-39
  * of that below), a row's weight in the output as two f16 parts (2^-22 of it, or
  * 2^-37 of the largest; 2^-21 of the largest where no row's scale is above
- * 2^-94).  The scales of a list may be any distance apart.  Pointers 16-byte
- * aligned (codes 32-byte; lse, n_sel and block_table 4-byte; scales any).  Workspace:
- * DSA_OP_PAGED_MLA; it serves every batch of as many sequences and queries, and
- * the same flags, whose rows are fewer. */
+ * 2^-94), a logit (in log2 units) to 2^-24 of itself plus its latent scale's
+ * exponent's distance from -8.  The scales of a list may be any distance apart.
+ * Pointers 16-byte aligned (codes 32-byte; lse, n_sel and block_table 4-byte;
+ * scales any).  Workspace: DSA_OP_PAGED_MLA; it serves every batch of as many
+ * sequences and queries, and the same flags, whose rows are fewer. */
 dsa_status dsa_paged_mla_attn(const dsa_shape *shape, const dsa_batch *batch,
                               const dsa_pages *pages, const void *q_abs, const void *codes,
                               const void *scales, const int32_t *block_table, const int32_t *idx,
