@@ -71,8 +71,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 55,109, within f16, whose step of 2^-24 the weights share: a weight is off by 2^-37 of
 // the largest one at most.  (With m at the largest logit itself, every row 2^25 below
 // it had no weight: 2,048 equal rows 17 nats below one row of value zero gave zeros.
-// What the room costs in raises: 1,024 queries of 2,048 rows 644 us without, 704 us so,
-// 64 queries 64.9 and 70.7 us; with a room of 10, 692 and 69.7 us.)
+// What the room costs in raises: 1,024 queries of 2,048 rows 638 us without, 698 us so,
+// 64 queries 65.4 and 71.0 us; with a room of 10, 685 and 70.0 us.)
 constexpr float kRoom = 12.f, kSlack = 15.75f;
 // x = z + (e - kEBase): the reference m is kRoom or more below the largest x, so the
 // row there has p = 2^(x - m - (e - kEBase)) >= 2^-115 (e <= 119), 2^34 of float32's
@@ -92,8 +92,8 @@ constexpr float kSmall = -60.f, kLarge = 48.f;
 // accumulation off instead of rounding it, so a sum's error grows with the tiles
 // in it: relative to the output, against 64 bits, 0.3e-6 for 2 tiles, 1.2e-6 for
 // 16, 1.6e-6 for 32, where float32 sums have 0.5e-6.  Moved every 11 tiles it is
-// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows take 644 us without and
-// 704 us so (every 16 tiles 666 us, and errors above 1e-6).
+// 0.9e-6 for 32, at a cost: 1,024 queries of 2,048 rows take 650 us without and
+// 698 us so (every 16 tiles 673 us, and errors above 1e-6).
 constexpr int kFlushTiles = 11;
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any row
 constexpr int kSoftmaxThreads = 256;
