@@ -16,6 +16,10 @@ Tensor layouts (row-major, contiguous), with ``W = kv_lora + rope_dim``:
 * ``scores`` [n_q, ld] float32, ``idx`` [n_q, top_k + kpool - 1] int32,
   ``n_sel`` [n_q] int32, ``out`` [n_q, heads, kv_lora] float32,
   ``lse`` [n_q, heads] float32
+* ``q`` [n_q, heads, nope + rope], ``k_nope`` [rows, heads, nope], ``v`` and ``out`` of the
+  expanded attention [.., heads, v_dim]: the shape's dtype
+* ``dsa_rms_norm`` and ``dsa_rope`` also take tensors whose rows (and heads) are parts of
+  wider ones; their last dimension has stride 1
 * the paged 8-bit cache: ``codes`` [n_pages, page_rows, W] of one-byte elements,
   ``scales`` [n_pages, 2] uint8 ([n_pages, 1] without rope), ``block_table``
   [n_seq, table_ld] int32, ``slots`` [tokens] int64
@@ -41,6 +45,9 @@ __all__ = [
     "dsa_up_project", "OP_DECODE_STEP_HOST",
     "Pages", "make_pages", "CACHE_E4M3", "CACHE_S8", "OP_PAGE_PLAN", "OP_CACHE_APPEND",
     "OP_PAGED_MLA", "dsa_page_plan", "dsa_cache_append", "dsa_paged_mla_attn",
+    "RopePlan", "make_rope", "ROPE_PAIRS", "ROPE_HALVES", "NORM_SAME", "NORM_E4M3",
+    "OP_EXPANDED_MLA", "dsa_rms_norm", "dsa_rope_init", "dsa_rope", "dsa_expand_kv",
+    "dsa_expanded_mla_attn",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdsa.so")
@@ -51,7 +58,10 @@ OP_POOL_COMPRESS = 5
 OP_PROJECT = 6
 OP_DECODE_STEP_HOST = 7
 OP_PAGE_PLAN, OP_CACHE_APPEND, OP_PAGED_MLA = 16, 17, 18
+OP_EXPANDED_MLA = 24
 CACHE_E4M3, CACHE_S8 = 0, 1
+NORM_SAME, NORM_E4M3 = 0, 1
+ROPE_PAIRS, ROPE_HALVES, ROPE_MAX_PAIRS = 0, 1, 128
 FLAG_TWO_LAUNCH, FLAG_DESC_ORDER, FLAG_DENSE = 0x1, 0x2, 0x4
 _TORCH_DTYPE = {DSA_F32: torch.float32, DSA_BF16: torch.bfloat16}
 STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED",
@@ -89,6 +99,11 @@ class Pages(ctypes.Structure):
                 ("n_pages", ctypes.c_int64), ("table_ld", ctypes.c_int64)]
 
 
+class RopePlan(ctypes.Structure):
+    _fields_ = [("dims", ctypes.c_int32), ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
 
@@ -107,6 +122,7 @@ def load() -> ctypes.CDLL:
                               ctypes.c_int64, ctypes.c_size_t)
         B = ctypes.POINTER(Batch)
         G = ctypes.POINTER(Pages)
+        R = ctypes.POINTER(RopePlan)
         sigs = {
             "dsa_version": ([], ctypes.c_int),
             "dsa_status_string": ([i32], ctypes.c_char_p),
@@ -129,6 +145,12 @@ def load() -> ctypes.CDLL:
             "dsa_up_project": ([S, i32, i32, P, P, P, P, sz, P], ctypes.c_int),
             "dsa_page_plan": ([G, i32, i64, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
             "dsa_cache_append": ([S, B, G, P, P, P, P, P, sz, P], ctypes.c_int),
+            "dsa_rms_norm": ([i64, i32, i32, P, i64, P, i64, P, ctypes.c_float, P, i64, P, i64, i32, P,
+                              i32, P], ctypes.c_int),
+            "dsa_rope_init": ([R, i32, i32, i32] + [ctypes.c_double] * 6, ctypes.c_int),
+            "dsa_rope": ([R, i32, i64, i32, P, i64, i64, P, P, i64, i64, P], ctypes.c_int),
+            "dsa_expand_kv": ([S, i64, i32, i32, P, P, P, P, P, P, sz, P], ctypes.c_int),
+            "dsa_expanded_mla_attn": ([S, B, i32, i32, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
             "dsa_paged_mla_attn": ([S, B, G, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         }
         for name, (args, res) in sigs.items():
@@ -400,6 +422,145 @@ def dsa_paged_mla_attn(shape, batch, pages, q_abs, codes, scales, block_table, i
           None if dense else _at(n_sel, i32, d, n_q, "n_sel"),
           _at(out, f32, d, n_q * heads * shape.kv_lora, "out"),
           None if lse is None else _at(lse, f32, d, n_q * heads, "lse"),
+          _at(ws, torch.uint8, d, 0, "ws"), ws.numel(), _stream_at(stream, d))
+
+
+_DSA_DTYPE = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16}
+
+
+def _dtype(t, what: str) -> int:
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    d = _DSA_DTYPE.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{what} is float32 or bfloat16, not {t.dtype}")
+    return d
+
+
+def _rows_at(t, like, dtype, device: int, what: str):
+    """Address and row stride of a matrix of ``like``'s shape whose rows may be
+    parts of wider ones."""
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    shape, (ld, step) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
+    if shape != like or t.dtype is not dtype or t.get_device() != device:
+        if shape != like:
+            raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(shape)}")
+        _refuse(t, dtype, device, 0, what)
+    rows, width = like
+    if width > 1 and step != 1:
+        raise ValueError(f"{what}'s rows are contiguous: its last stride is 1")
+    return t.data_ptr(), ld if rows > 1 else width
+
+
+def dsa_rms_norm(x, weight, eps, out, add=None, total=None, scales=None, group=0,
+                 stream=None) -> None:
+    """Norm of the rows of ``x`` [rows, width], or of ``x + add`` (see dsa.h);
+    ``total`` gets the sum.  ``out`` has x's type, or one-byte elements (e4m3
+    codes) with ``scales`` [rows, ceil(width / group)] float32 (group 0: [rows, 1])."""
+    like, d, kind = getattr(x, "shape", None), torch.cuda.current_device(), _dtype(x, "x")
+    if len(like) != 2:
+        raise ValueError("x is a matrix of rows")
+    dt = x.dtype
+    rows, width = like
+    px, x_ld = _rows_at(x, like, dt, d, "x")
+    pa, a_ld = (None, 0) if add is None else _rows_at(add, like, dt, d, "add")
+    pt, t_ld = (None, 0) if total is None else _rows_at(total, like, dt, d, "total")
+    codes = out is not None and out.element_size() == 1
+    po, o_ld = _rows_at(out, like, out.dtype if codes else dt, d, "out")
+    ps = None
+    if codes:
+        ps = _at(scales, torch.float32, d, rows * (-(-width // group) if group else 1), "scales")
+    elif scales is not None:
+        raise ValueError("scales go with an out of one-byte elements")
+    _call("dsa_rms_norm", rows, width, kind, px, x_ld, pa, a_ld,
+          None if weight is None else _at(weight, torch.float32, d, width, "weight"), eps, pt, t_ld, po,
+          o_ld, NORM_E4M3 if codes else NORM_SAME, ps, group, _stream_at(stream, d))
+
+
+def dsa_rope_init(plan, dims, layout=ROPE_PAIRS, inverse=0, base=8e6, factor=1.0, original_len=0.0,
+                  beta_fast=32.0, beta_slow=1.0, magnitude=1.0) -> None:
+    """Fills a :class:`RopePlan` (see dsa.h)."""
+    _call("dsa_rope_init", ctypes.byref(plan), int(dims), int(layout), int(inverse), base, factor,
+          original_len, beta_fast, beta_slow, magnitude)
+
+
+def make_rope(dims, base, layout="pairs", factor=1.0, original_len=0.0, beta_fast=32.0,
+              beta_slow=1.0, magnitude=1.0, inverse=False) -> RopePlan:
+    """Plan of ``dsa_rope``: ``layout`` ROPE_PAIRS / ROPE_HALVES or "pairs" / "halves"."""
+    plan = RopePlan()
+    layout = {"pairs": ROPE_PAIRS, "halves": ROPE_HALVES}.get(layout, layout)
+    dsa_rope_init(plan, dims, layout, inverse, base, factor, original_len, beta_fast, beta_slow, magnitude)
+    return plan
+
+
+def _heads_at(t, like, dtype, device: int, what: str):
+    """Address and the strides of tokens and heads of [tokens, heads, dims] or
+    [tokens, dims], the last dimension contiguous."""
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    if t.shape != like:
+        raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, dtype, device, 0, what)
+    s = t.stride()
+    if s[-1] != 1:
+        raise ValueError(f"{what}'s heads are contiguous: its last stride is 1")
+    return t.data_ptr(), s[0], s[1] if len(s) == 3 else 0
+
+
+def dsa_rope(rope, x, pos, out, stream=None) -> None:
+    """``x`` [tokens, heads, dims] or [tokens, dims] (views of the rotated columns)
+    turned by ``pos`` [tokens] int64 into ``out``, which may be x (see dsa.h)."""
+    d, kind = torch.cuda.current_device(), _dtype(x, "x")
+    like = x.shape
+    if len(like) not in (2, 3) or like[-1] != rope.dims:
+        raise ValueError(f"x is [tokens, heads, {rope.dims}] or [tokens, {rope.dims}]")
+    px, x_tok, x_head = _heads_at(x, like, x.dtype, d, "x")
+    po, o_tok, o_head = _heads_at(out, like, x.dtype, d, "out")
+    _call("dsa_rope", rope, kind, like[0], like[1] if len(like) == 3 else 1, px, x_tok, x_head,
+          _at(pos, torch.int64, d, like[0], "pos"), po, o_tok, o_head, _stream_at(stream, d))
+
+
+def _weights_at(t, shape, device: int, what: str):
+    """Address and middle size of a weight [heads, features, kv_lora]."""
+    if t is None:
+        raise ValueError(f"{what} is missing")
+    n = t.shape[1] if t.dim() == 3 else 0
+    if t.dim() != 3 or t.shape[0] != shape.heads or t.shape[2] != shape.kv_lora:
+        raise ValueError(f"{what} is [{shape.heads}, features, {shape.kv_lora}]")
+    return _at(t, _TORCH_DTYPE[shape.dtype], device, 0, what), n
+
+
+def dsa_expand_kv(shape, cache, w_uk, w_uv, k_nope, v, ws, stream=None) -> None:
+    """``cache`` [rows, W] expanded into ``k_nope`` [rows, heads, nope] and ``v``
+    [rows, heads, v_dim] (see dsa.h)."""
+    d, dt = torch.cuda.current_device(), _TORCH_DTYPE[shape.dtype]
+    pk, nope = _weights_at(w_uk, shape, d, "w_uk")
+    pv, v_dim = _weights_at(w_uv, shape, d, "w_uv")
+    if cache is None or cache.dim() != 2 or cache.shape[1] != shape.kv_lora + shape.rope_dim:
+        raise ValueError(f"cache is [rows, {shape.kv_lora + shape.rope_dim}]")
+    rows = cache.shape[0]
+    _call("dsa_expand_kv", shape, rows, nope, v_dim, _at(cache, dt, d, 0, "cache"), pk, pv,
+          _at(k_nope, dt, d, rows * shape.heads * nope, "k_nope"),
+          _at(v, dt, d, rows * shape.heads * v_dim, "v"), _at(ws, torch.uint8, d, 0, "ws"), ws.numel(),
+          _stream_at(stream, d))
+
+
+def dsa_expanded_mla_attn(shape, batch, q, k_nope, cache, v, out, lse, ws, stream=None) -> None:
+    """Causal attention over expanded keys ``k_nope`` [rows, heads, nope] and values
+    ``v`` [rows, heads, v_dim], the rope part of the keys in ``cache`` (see dsa.h)."""
+    d, dt = torch.cuda.current_device(), _TORCH_DTYPE[shape.dtype]
+    heads, rope, n_q, rows = shape.heads, shape.rope_dim, batch.n_q, batch.total_rows
+    if k_nope is None or v is None or k_nope.dim() != 3 or v.dim() != 3:
+        raise ValueError("k_nope and v are [rows, heads, columns]")
+    nope, v_dim = k_nope.shape[2], v.shape[2]
+    _call("dsa_expanded_mla_attn", shape, batch, nope, v_dim,
+          _at(q, dt, d, n_q * heads * (nope + rope), "q"),
+          _at(k_nope, dt, d, rows * heads * nope, "k_nope"),
+          _at(cache, dt, d, rows * (shape.kv_lora + rope), "cache") if rope else None,
+          _at(v, dt, d, rows * heads * v_dim, "v"), _at(out, dt, d, n_q * heads * v_dim, "out"),
+          None if lse is None else _at(lse, torch.float32, d, n_q * heads, "lse"),
           _at(ws, torch.uint8, d, 0, "ws"), ws.numel(), _stream_at(stream, d))
 
 

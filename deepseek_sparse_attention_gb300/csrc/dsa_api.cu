@@ -170,6 +170,7 @@ size_t op_bytes(const Shape& sh, const BatchDev& b, int32_t op) {
         case DSA_OP_PAGE_PLAN: return align_up(scratch_off() + page_plan_scratch_bytes(b.n_seq));
         case DSA_OP_CACHE_APPEND: return kWsHeaderBytes;
         case DSA_OP_PAGED_MLA: return align_up(scratch_off() + paged_mla_scratch_bytes(sh, b));
+        case DSA_OP_EXPANDED_MLA: return align_up(scratch_off() + expanded_mla_scratch_bytes(sh, b));
         default: return 0;
     }
 }
@@ -220,11 +221,13 @@ cudaError_t enqueue_index_select(const Shape& sh, const BatchDev& b, const StepL
 // The operations of the paged 8-bit cache, numbered apart from the others.
 bool paged_op(int32_t op) { return op >= DSA_OP_PAGE_PLAN && op <= DSA_OP_PAGED_MLA; }
 bool known_op(int32_t op) {
-    return (op >= DSA_OP_INDEX_SCORES && op <= DSA_OP_DECODE_STEP_HOST) || paged_op(op);
+    return (op >= DSA_OP_INDEX_SCORES && op <= DSA_OP_DECODE_STEP_HOST) || paged_op(op) ||
+           op == DSA_OP_EXPANDED_MLA;
 }
 // Operations whose queries are new tokens, of which a batch may have millions.
 bool any_n_q(int32_t op) {
-    return op == DSA_OP_POOL_COMPRESS || op == DSA_OP_PAGE_PLAN || op == DSA_OP_CACHE_APPEND;
+    return op == DSA_OP_POOL_COMPRESS || op == DSA_OP_PAGE_PLAN || op == DSA_OP_CACHE_APPEND ||
+           op == DSA_OP_EXPANDED_MLA;
 }
 
 dsa_status check_pages(const dsa_pages* p, PagesDev* out) {
@@ -263,6 +266,7 @@ int32_t plan_launches(const Shape& sh, const BatchDev& bh, int32_t op, int32_t s
         case DSA_OP_PROJECT: return 1;
         case DSA_OP_CACHE_APPEND: return 1;
         case DSA_OP_PAGED_MLA: return paged_mla_launches(sh, bh);
+        case DSA_OP_EXPANDED_MLA: return splits > 1 ? 2 : 1;
         case DSA_OP_DECODE_STEP_HOST:                      // the input copy, then the step
             return 1 + ((bh.flags & DSA_FLAG_DENSE) ? attn : sel + attn);
         default: return (bh.flags & DSA_FLAG_DENSE) ? attn : sel + attn;
@@ -354,6 +358,7 @@ dsa_status dsa_plan(const dsa_shape* shape, const dsa_batch* batch, int32_t op,
     const BatchDev bh = host_batch(batch, sh);
     int32_t rps = 0, splits = 0;
     if (op == DSA_OP_PAGED_MLA) plan_paged_splits(sh, bh, &rps, &splits);
+    else if (op == DSA_OP_EXPANDED_MLA) splits = plan_expanded_splits(sh, bh);
     else plan_attention_splits(sh, bh, &rps, &splits);
     *info = dsa_plan_info{plan_launches(sh, bh, op, splits), splits, rps, 0};
     return DSA_OK;
@@ -583,6 +588,132 @@ dsa_status dsa_paged_mla_attn(const dsa_shape* shape, const dsa_batch* batch,
                                         bytes(ws) + scratch_off(), need - scratch_off(),
                                         static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)),
                        "paged_mla_attn");
+}
+
+dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void* x, int64_t x_ld,
+                        const void* add, int64_t add_ld, const float* weight, float eps, void* total,
+                        int64_t total_ld, void* out, int64_t out_ld, int32_t out_format, float* scales,
+                        int32_t group, void* stream) {
+    const bool e4m3 = out_format == DSA_NORM_E4M3;
+    if (n_rows < 0 || width < 1 || (dtype != DSA_F32 && dtype != DSA_BF16) ||
+        (out_format != DSA_NORM_SAME && !e4m3) || !isfinite(eps) || !(eps > 0.f))
+        return DSA_ERR_INVALID_ARG;
+    if (e4m3 ? group != 0 && group != 32 && group != 64 && group != 128 : group != 0)
+        return DSA_ERR_INVALID_ARG;
+    if (x_ld < width || (add != nullptr && add_ld < width) || (total != nullptr && total_ld < width) ||
+        out_ld < width)
+        return DSA_ERR_INVALID_ARG;
+    if (n_rows > 0 && (x == nullptr || out == nullptr || (e4m3 && scales == nullptr)))
+        return DSA_ERR_INVALID_ARG;
+    const uintptr_t e = dtype == DSA_BF16 ? 2 : 4;
+    if (!aligned(x, e) || !aligned(add, e) || !aligned(total, e) || (!e4m3 && !aligned(out, e)) ||
+        !aligned(weight, 4) || !aligned(scales, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (width > 16384 || n_rows >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    const NormArgs a{n_rows, x_ld, add_ld, total_ld, out_ld, x,     add, weight,
+                     total,  out,  scales, width,    group,  eps};
+    return cuda_status(launch_rms_norm(a, dtype, e4m3, static_cast<cudaStream_t>(stream)), "rms_norm");
+}
+
+dsa_status dsa_rope_init(dsa_rope_plan* plan, int32_t dims, int32_t layout, int32_t inverse,
+                         double base, double factor, double original_len, double beta_fast,
+                         double beta_slow, double magnitude) {
+    if (plan == nullptr || dims < 2 || (dims & 1) || (layout != DSA_ROPE_PAIRS && layout != DSA_ROPE_HALVES) ||
+        (inverse != 0 && inverse != 1) || !isfinite(base) || !(base > 1.0) || !isfinite(factor) ||
+        !(factor >= 1.0) || !isfinite(magnitude))
+        return DSA_ERR_INVALID_ARG;
+    if (factor != 1.0 && !(beta_fast == 0.0 && beta_slow == 0.0) &&
+        (!isfinite(original_len) || !(original_len > 0.0) || !isfinite(beta_fast) || !(beta_slow > 0.0) ||
+         !(beta_fast >= beta_slow)))
+        return DSA_ERR_INVALID_ARG;
+    if (dims > 2 * DSA_ROPE_MAX_PAIRS) return DSA_ERR_UNSUPPORTED;
+    memset(plan, 0, sizeof(*plan));
+    plan->dims = dims;
+    plan->layout = layout;
+    plan->inverse = inverse;
+    plan->magnitude = (float)magnitude;
+    init_rope_plan(dims, base, factor, original_len, beta_fast, beta_slow, plan->turns);
+    return DSA_OK;
+}
+
+dsa_status dsa_rope(const dsa_rope_plan* plan, int32_t dtype, int64_t n_tok, int32_t heads,
+                    const void* x, int64_t x_tok, int64_t x_head, const int64_t* pos, void* out,
+                    int64_t out_tok, int64_t out_head, void* stream) {
+    if (plan == nullptr || plan->dims < 2 || (plan->dims & 1) || plan->dims > 2 * DSA_ROPE_MAX_PAIRS ||
+        (plan->layout != DSA_ROPE_PAIRS && plan->layout != DSA_ROPE_HALVES) ||
+        (dtype != DSA_F32 && dtype != DSA_BF16) || n_tok < 0 || heads < 0)
+        return DSA_ERR_INVALID_ARG;
+    if (x_tok < 0 || x_head < 0 || out_tok < 0 || out_head < 0) return DSA_ERR_INVALID_ARG;
+    // no two of the output's heads, or tokens, share a column
+    if (n_tok > 0 && heads > 0) {
+        if (x == nullptr || out == nullptr || pos == nullptr) return DSA_ERR_INVALID_ARG;
+        const int64_t d = plan->dims;
+        const bool inner = heads == 1 || out_head >= d, outer = n_tok == 1 || out_tok >= d;
+        if (!inner || !outer) return DSA_ERR_INVALID_ARG;
+        if (heads > 1 && n_tok > 1) {
+            const bool tok_outer = out_tok >= (heads - 1) * out_head + d;
+            const bool head_outer = out_head / d >= n_tok || out_head >= (n_tok - 1) * out_tok + d;
+            if (!tok_outer && !head_outer) return DSA_ERR_INVALID_ARG;
+        }
+        if (x == out && ((n_tok > 1 && x_tok != out_tok) || (heads > 1 && x_head != out_head)))
+            return DSA_ERR_INVALID_ARG;
+    }
+    const uintptr_t e = dtype == DSA_BF16 ? 2 : 4;
+    if (!aligned(x, e) || !aligned(out, e) || !aligned(pos, 8)) return DSA_ERR_INVALID_ARG;
+    if (n_tok >= ((int64_t)1 << 31) || heads > 65536) return DSA_ERR_UNSUPPORTED;
+    return cuda_status(launch_rope(*plan, dtype, n_tok, heads, x, x_tok, x_head, pos, out, out_tok,
+                                   out_head, static_cast<cudaStream_t>(stream)),
+                       "rope");
+}
+
+// The head widths of the expanded form: nope_dim and v_dim.
+static dsa_status check_expanded(const Shape& sh, int32_t nope_dim, int32_t v_dim) {
+    if (nope_dim < 64 || nope_dim % 64 != 0 || v_dim < 128 || v_dim % 128 != 0) return DSA_ERR_INVALID_ARG;
+    if (nope_dim + sh.rope > 256 || v_dim > 256) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+dsa_status dsa_expand_kv(const dsa_shape* shape, int64_t n_rows, int32_t nope_dim, int32_t v_dim,
+                         const void* cache, const void* w_uk, const void* w_uv, void* k_nope, void* v,
+                         void* ws, size_t ws_bytes, void* stream) {
+    Shape sh;
+    dsa_status s = check_shape(shape, &sh);
+    if (s != DSA_OK) return s;
+    if (n_rows < 0) return DSA_ERR_INVALID_ARG;
+    if ((s = check_expanded(sh, nope_dim, v_dim)) != DSA_OK) return s;
+    if (n_rows > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+    if (n_rows > 0 && (cache == nullptr || w_uk == nullptr || w_uv == nullptr || k_nope == nullptr || v == nullptr))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(cache) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(k_nope) || !aligned16(v))
+        return DSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, kWsHeaderBytes)) != DSA_OK) return s;
+    return cuda_status(launch_expand_kv(sh, n_rows, nope_dim, v_dim, cache, w_uk, w_uv, k_nope, v,
+                                        static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)),
+                       "expand_kv");
+}
+
+dsa_status dsa_expanded_mla_attn(const dsa_shape* shape, const dsa_batch* batch, int32_t nope_dim,
+                                 int32_t v_dim, const void* q, const void* k_nope, const void* cache,
+                                 const void* v, void* out, float* lse, void* ws, size_t ws_bytes,
+                                 void* stream) {
+    Shape sh;
+    BatchDev b;
+    dsa_status s = check_shape(shape, &sh);
+    if (s != DSA_OK) return s;
+    if ((s = check_batch(batch, sh, &b, 1 << 24)) != DSA_OK) return s;
+    if ((s = check_expanded(sh, nope_dim, v_dim)) != DSA_OK) return s;
+    if (b.n_seq > (1 << 20) || b.total_rows >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    if (b.n_q > 0 && (q == nullptr || k_nope == nullptr || v == nullptr || out == nullptr ||
+                      (sh.rope > 0 && cache == nullptr)))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_nope) || !aligned16(cache) || !aligned16(v) || !aligned16(out) ||
+        !aligned(lse, 4))
+        return DSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, op_bytes(sh, b, DSA_OP_EXPANDED_MLA))) != DSA_OK) return s;
+    return cuda_status(launch_expanded_mla(sh, b, nope_dim, v_dim, q, k_nope, cache, v, out, lse,
+                                           bytes(ws) + scratch_off(), static_cast<int32_t*>(ws),
+                                           static_cast<cudaStream_t>(stream)),
+                       "expanded_mla_attn");
 }
 
 dsa_status dsa_decode_step(const dsa_shape* shape, const dsa_batch* batch, const void* q_idx,

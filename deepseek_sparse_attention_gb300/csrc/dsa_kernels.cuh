@@ -247,4 +247,37 @@ cudaError_t launch_paged_mla(const Shape& sh, const BatchDev& b, const PagedCach
                              float* out, float* lse, void* scratch, size_t scratch_bytes,
                              int32_t* err, cudaStream_t st);
 
+// Root-mean-square norm (rms_norm.cu): y = (x + add) / rms * weight, in x's type
+// or as e4m3 codes with a float32 scale per `group` columns (0: per row).
+struct NormArgs {
+    int64_t n_rows, x_ld, add_ld, total_ld, out_ld;      // row strides in elements
+    const void *x, *add;
+    const float* weight;
+    void *total, *out;
+    float* scales;
+    int32_t width, group;
+    float eps;
+};
+cudaError_t launch_rms_norm(const NormArgs& a, int32_t dtype, bool e4m3, cudaStream_t st);
+
+// Rotary embedding of part of each head (rope.cu).  init_rope_plan: the rates of
+// dims / 2 pairs as 64-bit fractions of a turn per position.
+void init_rope_plan(int32_t dims, double base, double factor, double original_len, double beta_fast,
+                    double beta_slow, uint64_t* turns);
+cudaError_t launch_rope(const dsa_rope_plan& r, int32_t dtype, int64_t n_tok, int32_t heads,
+                        const void* x, int64_t x_tok, int64_t x_head, const int64_t* pos, void* out,
+                        int64_t out_tok, int64_t out_head, cudaStream_t st);
+
+// Latent rows into every head's keys and values (expand_kv.cu).
+cudaError_t launch_expand_kv(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim,
+                             const void* rows, const void* w_uk, const void* w_uv, void* k_nope,
+                             void* v, int32_t* err, cudaStream_t st);
+
+// Causal attention over expanded keys and values (expanded_mla.cu).
+int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b);
+size_t expanded_mla_scratch_bytes(const Shape& sh, const BatchDev& b);
+cudaError_t launch_expanded_mla(const Shape& sh, const BatchDev& b, int32_t nope, int32_t v_dim,
+                                const void* q, const void* k_nope, const void* rows, const void* v,
+                                void* out, float* lse, void* scratch, int32_t* err, cudaStream_t st);
+
 }  // namespace dsa

@@ -1,0 +1,120 @@
+// expand_kv.cu -- the latent rows expanded into every head's keys and values.
+//
+//   k_nope[r, h, d] = sum_{i < kv_lora} w_uk[h, d, i] * latent[r, i]
+//   v[r, h, e]      = sum_{i < kv_lora} w_uv[h, e, i] * latent[r, i]
+//
+// "GLM 5.2 in one C file", "Attention: Multi head Latent Attention With a Tiny
+// KV Cache": the explicit form of what absorption folds into the query and the
+// output.  Two matrix products of the rows [n_rows, kv_lora] with the weights
+// [heads * d, kv_lora], both with the sum along contiguous memory, in one launch.
+//
+// On CUDA cores: tiles of 128 rows by 128 outputs, 8 x 8 of them to a thread,
+// 16 terms of the sum at a time through shared memory while the next are
+// loaded into registers.
+#include "dsa_kernels.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 128, kDepth = 16, kLd = kTile + 4;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
+                       __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                              *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+expand_simt(const T* __restrict__ rows, const T* __restrict__ w_uk, const T* __restrict__ w_uv,
+            T* __restrict__ k_nope, T* __restrict__ v, int64_t n_rows, int32_t width, int32_t kv_lora,
+            int32_t n_k, int32_t n_v) {
+    __shared__ float As[kDepth][kLd], Bs[kDepth][kLd];
+    const int tiles = (n_k + n_v) / kTile;
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kTile;
+    int n0 = (int)(blockIdx.x % tiles) * kTile;
+    const bool is_v = n0 >= n_k;                         // both widths are multiples of a tile
+    if (is_v) n0 -= n_k;
+    const T* w = is_v ? w_uv : w_uk;
+    T* out = is_v ? v : k_nope;
+    const int ld = is_v ? n_v : n_k;
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    // this thread's two pieces of four terms of each operand's tile
+    float4 a[2], b[2];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = t + i * 256, line = at >> 2, k = k0 + (at & 3) * 4;
+            a[i] = r0 + line < n_rows ? load4(rows + (r0 + line) * width + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            b[i] = load4(w + (int64_t)(n0 + line) * kv_lora + k);
+        }
+    };
+    float acc[8][8] = {};
+    load(0);
+    for (int k0 = 0; k0 < kv_lora; k0 += kDepth) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = t + i * 256, line = at >> 2, k = (at & 3) * 4;
+            As[k][line] = a[i].x; As[k + 1][line] = a[i].y; As[k + 2][line] = a[i].z; As[k + 3][line] = a[i].w;
+            Bs[k][line] = b[i].x; Bs[k + 1][line] = b[i].y; Bs[k + 2][line] = b[i].z; Bs[k + 3][line] = b[i].w;
+        }
+        __syncthreads();
+        if (k0 + kDepth < kv_lora) load(k0 + kDepth);
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) {
+            const float4 a0 = load4(&As[k][ty * 4]), a1 = load4(&As[k][64 + ty * 4]);
+            const float4 b0 = load4(&Bs[k][tx * 4]), b1 = load4(&Bs[k][64 + tx * 4]);
+            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) fma2(acc[i][j], acc[i][j + 1], av[i], av[i], bv[j], bv[j + 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + (i >> 2) * 64 + ty * 4 + (i & 3);
+        if (r >= n_rows) continue;
+        T* o = out + r * ld + n0 + tx * 4;
+        store4(o, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        store4(o + 64, acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+}
+
+template <typename T>
+cudaError_t launch_simt(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim, const void* rows,
+                        const void* w_uk, const void* w_uv, void* k_nope, void* v, cudaStream_t st) {
+    const int32_t n_k = sh.heads * nope, n_v = sh.heads * v_dim;
+    const int64_t grid = (n_rows + kTile - 1) / kTile * ((n_k + n_v) / kTile);
+    return launch_plain(expand_simt<T>, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const T*>(rows),
+                        static_cast<const T*>(w_uk), static_cast<const T*>(w_uv), static_cast<T*>(k_nope),
+                        static_cast<T*>(v), n_rows, sh.width(), sh.kv_lora, n_k, n_v);
+}
+
+}  // namespace
+
+cudaError_t launch_expand_kv(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim,
+                             const void* rows, const void* w_uk, const void* w_uv, void* k_nope,
+                             void* v, int32_t* err, cudaStream_t st) {
+    (void)err;
+    if (n_rows == 0) return cudaSuccess;
+    return sh.dtype == DSA_BF16
+               ? launch_simt<__nv_bfloat16>(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, st)
+               : launch_simt<float>(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, st);
+}
+
+}  // namespace dsa

@@ -1,0 +1,76 @@
+// expanded_mla.cuh -- what the kernels of the expanded latent attention share:
+// the units of work and where their results go.
+#pragma once
+
+#include "dsa_kernels.cuh"
+
+namespace dsa {
+
+// The operands, as the kernels take them.
+struct ExpandedArgs {
+    const void *q, *k_nope, *rows, *v;
+    void* out;
+    float* lse;
+    float *part_o, *part_ml;       // partial sums of splits, where there are several
+    int32_t heads, nope, rope, v_dim, kv_lora, width;
+    int32_t n_split;
+    float scale;
+    BatchDev b;
+    int32_t* err;
+};
+
+// A tile of up to BQ queries of one sequence and the key tiles of one split.
+struct ExpandedTile {
+    int64_t q0;                    // first query of the tile
+    int64_t row0;                  // first cache row of the sequence
+    int64_t first;                 // rows that the tile's first query sees
+    int32_t n_q;                   // its queries
+    int32_t kt0, kt1;              // key tiles of the split
+};
+
+// Tiles have slots: sequence s has the slots from q_off[s] / BQ + s on, which is
+// room for its ceil(q_len / BQ) tiles whatever the others' lengths are, so a slot
+// finds its sequence by a search over the offsets and nothing is planned ahead.
+// Slots left over have no tile.
+__host__ __device__ inline int64_t expanded_slots(int64_t n_q, int64_t n_seq, int bq) {
+    return n_q / bq + n_seq;
+}
+
+// False if the slot has no tile, or its sequence's offsets break the host's
+// bounds (recorded once for the sequence).
+__device__ __forceinline__ bool expanded_tile(const BatchDev& b, int64_t slot, int32_t split,
+                                              int32_t n_split, int bq, int bk, int32_t* err,
+                                              int32_t where, ExpandedTile& t) {
+    int32_t lo = 0, hi = b.n_seq - 1;
+    while (lo < hi) {                                    // last s whose slots start at or before this one
+        const int32_t mid = lo + (hi - lo + 1) / 2;
+        if (b.q_off[mid] / bq + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    const int64_t q0 = b.q_off[lo], q1 = b.q_off[lo + 1], r0 = b.row_off[lo], r1 = b.row_off[lo + 1];
+    const int64_t at = slot - (q0 / bq + lo);
+    if (slot == 0 && (b.q_off[0] != 0 || b.q_off[b.n_seq] != b.n_q))
+        record_error(err, kDevBadBatch, b.n_seq, where);
+    if (q0 < 0 || q1 < q0 || q1 > b.n_q || q1 - q0 > b.max_q_len || r0 < 0 || r1 > b.total_rows ||
+        r1 - r0 > b.max_kv_len || q1 - q0 > r1 - r0) {
+        if (at == 0) record_error(err, kDevBadBatch, lo, where);
+        return false;
+    }
+    const int64_t q_len = q1 - q0, kv_len = r1 - r0;
+    if (at < 0 || at * bq >= q_len) return false;
+    t.q0 = q0 + at * bq;
+    t.row0 = r0;
+    t.n_q = (int32_t)(q_len - at * bq < bq ? q_len - at * bq : bq);
+    t.first = kv_len - q_len + 1 + at * bq;
+    const int64_t tiles = (t.first + t.n_q - 1 + bk - 1) / bk;   // up to the last query's last row
+    t.kt0 = (int32_t)(tiles * split / n_split);
+    t.kt1 = (int32_t)(tiles * (split + 1) / n_split);
+    return true;
+}
+
+// Log2 of a sum of exponentials with maximum m (in log2 units) and sum l to the
+// natural logarithm; NaN where every attended logit was -inf (l == 0).
+__device__ __forceinline__ float expanded_lse(float m, float l) {
+    return l == 0.f ? __int_as_float(0x7fffffff) : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace dsa

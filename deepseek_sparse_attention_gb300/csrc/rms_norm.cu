@@ -1,0 +1,285 @@
+// rms_norm.cu -- root-mean-square norm of rows, with the residual's addition
+// before it and an output in the rows' type or in 8 bits with scales.
+//
+//   h = x + add,   y = h / sqrt(mean(h^2) + eps) * weight
+//   8 bits: scale_g = max(max_{j in g} |y_j| / 448, 2^-126), code_j = y_j / scale_g
+//
+// HBM-bound: a row is read once into registers, reduced and written.  It
+// belongs to TPR threads; each of their warps takes chunks of 256 columns, a
+// lane eight of them: neighbours, moved as 16 bytes, where pointers and strides
+// allow it (VEC), else every 32nd, so that a warp's accesses of single elements
+// are contiguous.  Either way the columns of a scale lie in one warp's chunk,
+// and their maximum is a shuffle.
+#include <cuda_fp8.h>
+
+#include "dsa_kernels.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kPer = 8;                      // columns a lane has of a chunk
+constexpr int kChunk = 32 * kPer;            // columns of a warp's chunk
+constexpr int kChunks = 4;                   // chunks a warp may have
+constexpr float kTop = 448.f;                // the largest e4m3 value
+constexpr float kLeast = 0x1p-126f;          // the least scale: its inverse is finite
+
+// Eight elements as they are in memory.
+template <typename T>
+struct Raw {
+    T v[kPer];
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_chunk(Raw<T>& r, const T* p, int col, int width) {
+    if (VEC) {
+        if (col >= width) return;
+        constexpr int n = sizeof(Raw<T>) / 16;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p + col)[i];
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            if (col + 32 * e < width) r.v[e] = p[col + 32 * e];
+    }
+}
+
+__device__ __forceinline__ void round_to(float* d, float v) { *d = v; }
+__device__ __forceinline__ void round_to(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_chunk(T* p, const float (&h)[kPer], int col, int width) {
+    alignas(16) Raw<T> r;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) round_to(&r.v[e], h[e]);
+    if (VEC) {
+        if (col >= width) return;
+        constexpr int n = sizeof(Raw<T>) / 16;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            reinterpret_cast<uint4*>(p + col)[i] = reinterpret_cast<const uint4*>(&r)[i];
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            if (col + 32 * e < width) p[col + 32 * e] = r.v[e];
+    }
+}
+
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum (or maximum) over the TPR threads of a row, the same in each of them.
+// Rows of more than a warp have a CTA to themselves, so all its threads come here.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = MAX ? max_nan(v, u) : v + u;
+    }
+    if (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = buf[0];
+#pragma unroll
+        for (int w = 1; w < TPR / 32; ++w) v = MAX ? max_nan(v, buf[w]) : v + buf[w];
+    }
+    return v;
+}
+
+__device__ __forceinline__ float scale_of(float amax) {
+    return isnan(amax) ? amax : fmaxf(amax / kTop, kLeast);
+}
+
+template <typename T, bool E4M3, bool VEC, int TPR>
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rms_norm_kernel(const NormArgs a) {
+    constexpr int kRows = TPR == 32 ? 8 : 1;             // rows of a CTA
+    constexpr int kWarps = TPR / 32;                     // warps of a row
+    __shared__ float buf[3][kWarps];
+    const int lane = threadIdx.x & 31;
+    const int warp = TPR == 32 ? 0 : threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
+    if (row >= a.n_rows) return;
+    pdl_wait();
+    pdl_trigger();
+
+    // this lane's first column of chunk c; its others follow (VEC) or are 32 apart
+    auto col = [&](int c) { return (c * kWarps + warp) * kChunk + lane * (VEC ? kPer : 1); };
+    const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
+    alignas(16) Raw<T> rx[kChunks], ra[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        rx[c] = ra[c] = Raw<T>{};
+        load_chunk<VEC>(rx[c], x, col(c), a.width);
+    }
+    if (a.add != nullptr) {
+        const T* add = static_cast<const T*>(a.add) + row * a.add_ld;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) load_chunk<VEC>(ra[c], add, col(c), a.width);
+    }
+    float h[kChunks][kPer];
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            h[c][e] = to_float(rx[c].v[e]) + to_float(ra[c].v[e]);   // zeros past the row
+            ss = fmaf(h[c][e], h[c][e], ss);
+        }
+    ss = row_reduce<TPR, false>(ss, buf[0]);
+    float rstd;
+    // Squares beyond float32, or so small that they lose bits which eps does
+    // not cover: once more, of h times a power of two (all threads of the row)
+    const bool high = isinf(ss);
+    const bool low = ss < 0x1p-60f * (float)a.width && a.eps < 0x1p-60f;
+    if (high || low) {
+        const float f = high ? 0x1p-70f : 0x1p60f;
+        ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) ss = fmaf(h[c][e] * f, h[c][e] * f, ss);
+        ss = row_reduce<TPR, false>(ss, buf[1]);
+        rstd = f / sqrtf(ss / (float)a.width + a.eps * f * f);
+    } else {
+        rstd = 1.f / sqrtf(ss / (float)a.width + a.eps);
+    }
+    if (a.total != nullptr) {
+        T* t = static_cast<T*>(a.total) + row * a.total_ld;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) store_chunk<VEC>(t, h[c], col(c), a.width);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {                  // y in the place of h
+        alignas(16) Raw<float> w;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) w.v[e] = 1.f;
+        if (a.weight != nullptr) load_chunk<VEC>(w, a.weight, col(c), a.width);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            h[c][e] = h[c][e] * rstd * w.v[e];
+            if (E4M3) amax = max_nan(amax, fabsf(h[c][e]));
+        }
+    }
+    if constexpr (!E4M3) {
+        T* y = static_cast<T*>(a.out) + row * a.out_ld;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) store_chunk<VEC>(y, h[c], col(c), a.width);
+    } else {
+        const int n_groups = a.group == 0 ? 1 : (a.width + a.group - 1) / a.group;
+        float* scales = a.scales + row * n_groups;
+        uint8_t* codes = static_cast<uint8_t*>(a.out) + row * a.out_ld;
+        float s = 0.f;
+        if (a.group == 0) {
+            s = scale_of(row_reduce<TPR, true>(amax, buf[2]));
+            if (warp == 0 && lane == 0) scales[0] = s;
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int at = (c * kWarps + warp) * kChunk;
+            if (at >= a.width) break;                    // the whole warp
+            float inv[kPer];
+            if (a.group == 0) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
+            } else if (VEC) {
+                // a group is 4, 8 or 16 lanes
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) m = max_nan(m, fabsf(h[c][e]));
+                const int lanes = a.group / kPer;
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const float m8 = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                const float m16 = max_nan(m8, __shfl_xor_sync(0xffffffffu, m8, 8));
+                s = scale_of(lanes == 4 ? m : lanes == 8 ? m8 : m16);
+                if (lane % lanes == 0 && col(c) < a.width) scales[col(c) / a.group] = s;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
+            } else {
+                // a group is 1, 2 or 4 neighbouring elements of all lanes
+                const int n = a.group / 32;
+                float m[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    m[e] = fabsf(h[c][e]);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
+                }
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const float m2 = max_nan(m[e & ~1], m[e | 1]);
+                    const float m4 = max_nan(max_nan(m[e & ~3], m[(e & ~3) + 1]),
+                                             max_nan(m[(e & ~3) + 2], m[e | 3]));
+                    s = scale_of(n == 1 ? m[e] : n == 2 ? m2 : m4);
+                    if (lane == 0 && e % n == 0 && at + 32 * e < a.width)
+                        scales[(at + 32 * e) / a.group] = s;
+                    inv[e] = 1.f / s;
+                }
+            }
+            // to nearest even; a NaN stays one.  The product with 1 / s may be
+            // the neighbouring code of the quotient's only where that lies within
+            // 2^-23 of the middle between two codes.
+            alignas(8) uint8_t q[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+                const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                    make_float2(h[c][e] * inv[e], h[c][e + 1] * inv[e + 1]), __NV_SATFINITE, __NV_E4M3);
+                q[e] = (uint8_t)(two & 0xff);
+                q[e + 1] = (uint8_t)(two >> 8);
+            }
+            if (VEC) {
+                if (col(c) < a.width)
+                    *reinterpret_cast<uint2*>(codes + col(c)) = *reinterpret_cast<const uint2*>(q);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (col(c) + 32 * e < a.width) codes[col(c) + 32 * e] = q[e];
+            }
+        }
+    }
+}
+
+template <typename T, bool E4M3, bool VEC>
+cudaError_t launch(const NormArgs& a, cudaStream_t st) {
+    // a warp to a row of up to 1,024 columns; else 128 or 512 threads
+    if (a.width <= kChunk * kChunks)
+        return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 32>, dim3((unsigned)((a.n_rows + 7) / 8)),
+                          dim3(256), 0, st, a);
+    if (a.width <= 4 * kChunk * kChunks)
+        return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 128>, dim3((unsigned)a.n_rows), dim3(128), 0,
+                          st, a);
+    return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 512>, dim3((unsigned)a.n_rows), dim3(512), 0, st, a);
+}
+
+template <typename T>
+cudaError_t launch(const NormArgs& a, bool e4m3, bool vec, cudaStream_t st) {
+    if (e4m3) return vec ? launch<T, true, true>(a, st) : launch<T, true, false>(a, st);
+    return vec ? launch<T, false, true>(a, st) : launch<T, false, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormArgs& a, int32_t dtype, bool e4m3, cudaStream_t st) {
+    if (a.n_rows == 0) return cudaSuccess;
+    // 16-byte moves (8 for codes) where every pointer, stride and the width allow them
+    const int64_t e = dtype == DSA_BF16 ? 2 : 4;
+    auto fits = [](const void* p, int64_t ld, int64_t size, int64_t unit) {
+        return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * size)) & (unit - 1)) == 0;
+    };
+    const bool vec = a.width % kPer == 0 && fits(a.x, a.x_ld, e, 16) && fits(a.add, a.add_ld, e, 16) &&
+                     fits(a.total, a.total_ld, e, 16) && fits(a.weight, 0, 4, 16) &&
+                     (e4m3 ? fits(a.out, a.out_ld, 1, 8) : fits(a.out, a.out_ld, e, 16));
+    return dtype == DSA_BF16 ? launch<__nv_bfloat16>(a, e4m3, vec, st) : launch<float>(a, e4m3, vec, st);
+}
+
+}  // namespace dsa

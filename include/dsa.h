@@ -17,6 +17,13 @@
  * lengths), dsa_cache_append (new rows rounded into their slots) and
  * dsa_paged_mla_attn (the attention).
  *
+ * Around them: dsa_rms_norm (norm of hidden or latent rows, with the residual's
+ * addition and an output in 8 bits) and dsa_rope (rotary positions of the
+ * queries' and the cache rows' tails), which make step 3's inputs, and the
+ * explicit form of the attention over every visible row, for prompts:
+ * dsa_expand_kv (each head's keys and values from the latent rows) and
+ * dsa_expanded_mla_attn.
+ *
  * Sources (page title -- section):
  *   "GLM-5.x (glm-dsa, glm5next)" (TensorSharp model notes) -- "The block"
  *     (64 query heads, one 576-wide cache row per token, indexer 32 x 128,
@@ -165,6 +172,7 @@ int64_t dsa_index_row_width(const dsa_shape *shape);
 #define DSA_OP_PAGE_PLAN 16            /* of the batch only n_seq is read        */
 #define DSA_OP_CACHE_APPEND 17
 #define DSA_OP_PAGED_MLA 18
+#define DSA_OP_EXPANDED_MLA 24         /* dsa_expand_kv takes DSA_OP_PROJECT's   */
 dsa_status dsa_workspace_size(const dsa_shape *shape, const dsa_batch *batch, int32_t op,
                               size_t *bytes);
 
@@ -340,6 +348,133 @@ dsa_status dsa_up_project(const dsa_shape *shape, int32_t n_q, int32_t v_dim, co
 dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, const void *q_abs,
                                const void *cache, const int32_t *idx, const int32_t *n_sel,
                                float *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Root-mean-square norm of rows, with the residual's addition before it.
+ *     h = x + add,  y = h / sqrt(mean(h^2) + eps) * weight
+ *   x      [n_rows, width] dtype, rows x_ld >= width elements apart (a part of
+ *          wider rows: the 512 latent columns of a 576-wide cache row, say)
+ *   add    the same type and shape with its own stride, or NULL: h = x
+ *   weight [width] float32, or NULL: ones
+ *   total  [n_rows, width] dtype out, or NULL: h rounded to dtype (the next
+ *          residual).  The norm is of h before that rounding.
+ *   out    DSA_NORM_SAME: y in dtype; DSA_NORM_E4M3: one-byte e4m3 codes
+ *   scales DSA_NORM_E4M3: [n_rows, ceil(width / group)] float32 out, dense, one
+ *          per `group` columns (32, 64 or 128; 0 = one per row): the larger of
+ *          2^-126 and the group's largest |y| / 448; a code is y / scale rounded
+ *          to nearest even, and stands for code * scale.  Not read otherwise,
+ *          and group = 0.
+ * out and total may be x or add themselves (same stride); no other overlap.
+ * Columns between a row's width and the next row are neither read nor written.
+ * float32 arithmetic; sums of squares beyond float32's range are formed again of
+ * scaled values, so that any finite h gives its norm.  A row with an infinity
+ * gives NaN there and zeros elsewhere, a row with a NaN gives NaN; a group with
+ * a NaN has a NaN scale and NaN codes.  eps > 0, finite.  width 1 .. 16384,
+ * n_rows < 2^31.  Pointers aligned to their elements: with all of them 16-byte
+ * aligned (codes 8), strides a multiple of 16 bytes and the width of 8 elements
+ * a row moves in 16-byte pieces.  No workspace. */
+typedef enum {
+    DSA_NORM_SAME = 0,         /* y in the type of x                             */
+    DSA_NORM_E4M3 = 1          /* codes of 8 bits and float32 scales             */
+} dsa_norm_format;
+dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void *x, int64_t x_ld,
+                        const void *add, int64_t add_ld, const float *weight, float eps, void *total,
+                        int64_t total_ld, void *out, int64_t out_ld, int32_t out_format, float *scales,
+                        int32_t group, void *stream);
+
+/* Rotary positions of part of each head: the tails of step 3's queries and of
+ * the cache rows ("GLM-5.x (glm-dsa, glm5next)", "The block", row "RoPE": NORM
+ * mode, base 8e6), or of any other head.
+ *     (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t),  t = pos * rate_i
+ * over dims / 2 pairs: columns (2i, 2i + 1) (DSA_ROPE_PAIRS, the pages' NORM mode)
+ * or (i, i + dims / 2) (DSA_ROPE_HALVES), with sin t negated if inverse.
+ *
+ * dsa_rope_init (host only) fills a plan, which the caller keeps and may copy:
+ *   rate_i = base^(-2i / dims), i < dims / 2, base > 1
+ *   factor > 1 stretches a trained context of original_len positions to factor
+ *   times as many ("YaRN: Efficient Context Window Extension of Large Language
+ *   Models", 2023, with the ramp over the pairs' places): a pair's rate becomes
+ *   rate * ((1 - g) + g / factor), g = clamp((i - low) / (high - low), 0, 1),
+ *   low = max(floor(place(beta_fast)), 0), high = min(ceil(place(beta_slow)),
+ *   dims - 1), place(n) = dims * ln(original_len / (2 pi n)) / (2 ln base): pairs
+ *   that make beta_fast (32) turns or more over the trained context stay as they
+ *   are, those with beta_slow (1) or fewer are divided by the factor (high - low
+ *   counts as 0.001 at least).  beta_fast = beta_slow = 0 divides every rate.
+ *   magnitude multiplies the result (1, or the scaling's own correction).
+ *   dims even, 2 .. 256.
+ * dsa_rope:
+ *   x   first rotated column of the first head; token t's head h starts
+ *       t * x_tok + h * x_head elements behind it, its columns one after another
+ *   pos [n_tok] int64, any values (negative ones turn back)
+ *   out laid out by out_tok and out_head; x itself with x's strides, or apart
+ *       from it.  Its heads must not overlap.  Only rotated columns are written.
+ * float32 arithmetic; the angle is exact modulo one turn up to the rate's 53
+ * bits.  n_tok < 2^31, heads <= 65536.  Pointers aligned to their elements; 16-byte
+ * aligned ones with strides of 16 bytes' multiples move in 16-byte pieces.  No
+ * workspace. */
+typedef enum {
+    DSA_ROPE_PAIRS = 0,
+    DSA_ROPE_HALVES = 1
+} dsa_rope_layout;
+#define DSA_ROPE_MAX_PAIRS 128
+typedef struct {
+    int32_t dims;                          /* rotated columns of a head          */
+    int32_t layout;                        /* a dsa_rope_layout                  */
+    int32_t inverse;                       /* 1: turn back                       */
+    float magnitude;
+    uint64_t turns[DSA_ROPE_MAX_PAIRS];    /* rate_i / 2 pi times 2^64           */
+} dsa_rope_plan;
+dsa_status dsa_rope_init(dsa_rope_plan *plan, int32_t dims, int32_t layout, int32_t inverse,
+                         double base, double factor, double original_len, double beta_fast,
+                         double beta_slow, double magnitude);
+dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int32_t heads,
+                    const void *x, int64_t x_tok, int64_t x_head, const int64_t *pos, void *out,
+                    int64_t out_tok, int64_t out_head, void *stream);
+
+/* The explicit form of the attention ("GLM 5.2 in one C file", "Attention: Multi
+ * head Latent Attention With a Tiny KV Cache": the decompressed keys and values
+ * that absorption avoids).  Where every visible row is attended over -- a prompt
+ * of up to top_k tokens, where the selection can remove nothing -- it gives what
+ * dsa_absorb_q, dsa_sparse_mla_attn with DSA_FLAG_DENSE and dsa_up_project give,
+ * for 2 (nope_dim + rope_dim + v_dim) operations a head, query and row instead of
+ * 2 (2 kv_lora + rope_dim).
+ *
+ * dsa_expand_kv: every head's keys and values of latent rows.
+ *   cache  [n_rows, kv_lora + rope_dim] dtype; only the latent columns are read
+ *   w_uk   [heads, nope_dim, kv_lora] dtype, as for dsa_absorb_q
+ *   w_uv   [heads, v_dim, kv_lora] dtype, as for dsa_up_project
+ *   k_nope [n_rows, heads, nope_dim] dtype out: w_uk[h] . latent
+ *   v      [n_rows, heads, v_dim] dtype out: w_uv[h] . latent
+ * float32 accumulation, rounded once.  nope_dim a multiple of 64 with nope_dim +
+ * rope_dim <= 256, v_dim 128 or 256, n_rows <= 2^24.  Pointers 16-byte aligned.
+ * Workspace: DSA_OP_PROJECT (the error word).
+ *
+ * dsa_expanded_mla_attn: causal attention over them, the batch as for the other
+ * entry points (row_off and q_off; key_off must be given but is not read, nor are
+ * the flags); query i of a sequence attends over its first L rows.
+ *   q      [n_q, heads, nope_dim + rope_dim] dtype, as for dsa_absorb_q
+ *   k_nope [total_rows, heads, nope_dim], v [total_rows, heads, v_dim] dtype
+ *   cache  [total_rows, kv_lora + rope_dim] dtype: its rope columns are the rope
+ *          part of every head's key; not read (may be NULL) if rope_dim == 0
+ *   out    [n_q, heads, v_dim] dtype
+ *   lse    [n_q, heads] float32 or NULL
+ *       z_j = scale * (q_nope . k_nope[j, h] + q_rope . rope[j]),  j < L
+ *       out = sum_j softmax(z)_j v[j, h],  lse = log sum_j exp(z_j)
+ * Rows that a query does not see have no part in its result, whatever they hold.
+ * A NaN or infinite logit, or attended logits of -inf alone, give NaN.
+ * float32 logits, maxima, sums and accumulation; bf16 operands give each
+ * weight exp(z_j - m) to the value product rounded to bf16 (2^-8 of itself at most), the
+ * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <
+ * 2^31.  A sequence whose offsets break the host bounds is skipped and sets the
+ * error word (code 2).  Pointers 16-byte aligned (lse 4).  Workspace:
+ * DSA_OP_EXPANDED_MLA; it serves every batch of no more queries whose max_kv_len
+ * is no larger. */
+dsa_status dsa_expand_kv(const dsa_shape *shape, int64_t n_rows, int32_t nope_dim, int32_t v_dim,
+                         const void *cache, const void *w_uk, const void *w_uv, void *k_nope, void *v,
+                         void *ws, size_t ws_bytes, void *stream);
+dsa_status dsa_expanded_mla_attn(const dsa_shape *shape, const dsa_batch *batch, int32_t nope_dim,
+                                 int32_t v_dim, const void *q, const void *k_nope, const void *cache,
+                                 const void *v, void *out, float *lse, void *ws, size_t ws_bytes,
+                                 void *stream);
 
 /* The paged 8-bit cache
  * ---------------------
