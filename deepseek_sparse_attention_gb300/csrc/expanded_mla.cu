@@ -20,7 +20,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kKeys = 32;
-constexpr int kMaxTileQ = 64;                            // queries of the largest tile
+constexpr int kMaxTileQ = 128;                           // queries of the largest tile
 constexpr int kMaxSplit = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int6
     float l = 0.f;
     for (int s = 0; s < a.n_split; ++s) {
         const float2 x = ml[s];
-        const float w = x.x == -INFINITY ? (x.y == 0.f ? 0.f : x.y) : exp2f(x.x - top);
+        if (x.x == -INFINITY && x.y == 0.f) continue;    // a split without a key that the query sees
+        const float w = x.x == -INFINITY ? x.y : exp2f(x.x - top);
         l += x.y * w;
 #pragma unroll
         for (int c = 0; c < VD / 128; ++c) {
@@ -230,14 +231,24 @@ cudaError_t launch_simt(const ExpandedArgs& a, cudaStream_t st) {
 
 template <typename T, int VD>
 cudaError_t launch_all(const ExpandedArgs& a, bool few, cudaStream_t st) {
-    cudaError_t e = few ? launch_simt<T, 1, VD>(a, st) : launch_simt<T, 4, VD>(a, st);
+    cudaError_t e;
+    if constexpr (sizeof(T) == 2) e = launch_expanded_tc(a, st);
+    else e = few ? launch_simt<T, 1, VD>(a, st) : launch_simt<T, 4, VD>(a, st);
     if (e != cudaSuccess || a.n_split == 1) return e;
     const int64_t n = (int64_t)a.b.n_q * a.heads;
     return launch_pdl(expanded_merge<T, VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
 }
 
-// Queries of a tile: 16 where no sequence has more, else 64.
+// Queries of a tile on CUDA cores: 16 where no sequence has more, else 64.
 bool few_queries(const BatchDev& b) { return b.max_q_len <= 16; }
+
+struct TileSize {
+    int queries, keys;
+};
+TileSize tile_size(const Shape& sh, const BatchDev& b) {
+    if (sh.dtype == DSA_BF16) return {kExpandedTcQ, kExpandedTcK};
+    return {few_queries(b) ? 16 : 64, kKeys};
+}
 
 }  // namespace
 
@@ -248,9 +259,9 @@ constexpr int64_t kSplitWaves = 4;
 // its longest split and a split's partial sums as one more tile.
 int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b) {
     if (b.n_q < 1) return 1;
-    const int bq = few_queries(b) ? 16 : 64;
-    const int64_t units = expanded_slots(b.n_q, b.n_seq, bq) * sh.heads, sms = sm_count();
-    const int64_t tiles = (b.max_kv_len + kKeys - 1) / kKeys;
+    const TileSize ts = tile_size(sh, b);
+    const int64_t units = expanded_slots(b.n_q, b.n_seq, ts.queries) * sh.heads, sms = sm_count();
+    const int64_t tiles = (b.max_kv_len + ts.keys - 1) / ts.keys;
     int32_t best = 1;
     int64_t least = INT64_MAX;
     for (int32_t s = 1; s <= kMaxSplit && s <= tiles && (s == 1 || units * s <= kSplitWaves * sms); ++s) {

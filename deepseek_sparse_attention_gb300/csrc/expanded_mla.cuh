@@ -73,4 +73,8 @@ __device__ __forceinline__ float expanded_lse(float m, float l) {
     return l == 0.f ? __int_as_float(0x7fffffff) : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// The tensor-core kernel (expanded_mla_tc.cu), bf16: its tiles.
+constexpr int kExpandedTcQ = 128, kExpandedTcK = 128;
+cudaError_t launch_expanded_tc(const ExpandedArgs& a, cudaStream_t st);
+
 }  // namespace dsa
