@@ -5,15 +5,17 @@
 //   the key tiles with a running maximum, O += P V (M = 128, N = v_dim, K = 128 keys)
 //
 // One CTA per (tile of 128 queries, head, split of the key tiles):
-//   warp 4     TMA: the queries once, then a ring of 16 KB blocks in the order of
+//   warp 8     TMA: the queries once, then a ring of 16 KB blocks in the order of
 //              their use -- a tile's keys as blocks of 64 columns (the rope block from
 //              the cache rows, for every head), its values as blocks of 8192 / v_dim keys;
-//   warp 5     issues the products, S of tile t + 1 before O of tile t;
-//   warps 0-3  softmax, a query row to a thread: S from TMEM, exp, P in bf16 back over S
-//              (O takes it from TMEM as its A operand), row maxima that are raised
-//              only when a logit exceeds them by more than kSlack (then O is rescaled
-//              in TMEM); at the end O to the output or the split's part;
-//   warps 6-7  values of tiles that some query sees only in part: NaN and infinities
+//   warp 9     issues the products, S of tile t + 1 before O of tile t;
+//   warps 0-7  softmax, a query row and half of its keys to a thread: S from TMEM,
+//              exp, P in bf16 back over S (O takes it from TMEM as its A operand).
+//              Row maxima are raised only when a logit exceeds them by more than
+//              kSlack, so the two halves of a row share a maximum without telling each
+//              other theirs: a barrier that also votes says whether any row is raised,
+//              and only then they are exchanged and O is rescaled in TMEM;
+//   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
 //              epilogue to the queries that see them.
 // P is rounded to bf16 because both operands of the value product have one
@@ -31,11 +33,13 @@ using namespace sm100;
 constexpr int kQ = kExpandedTcQ, kK = kExpandedTcK;      // queries and keys of a tile
 constexpr uint32_t kBlock = 16384;
 constexpr int kMaxRing = 13;
-constexpr int kThreads = 256;
+constexpr int kSoftmax = 256;                            // threads
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kThreads = 384;
 constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
-constexpr uint32_t kBarBytes = 1024;
+constexpr uint32_t kBarBytes = 2048;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                            // weights stay below 2^8
@@ -65,10 +69,52 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 struct Bars {
     uint64_t full[kMaxRing], empty[kMaxRing], turn[kMaxRing], clean[kMaxRing];
     uint64_t q_full, s_full[2], p_full[2], o_done, o_last, drain;
+    float half[kSoftmax];                                // maxima, then sums, of a row's halves
     uint32_t tmem;
     int32_t abort, poison;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+
+// Two at a time: x * a + b, and sums.
+__device__ __forceinline__ float2 fma_x2(float2 x, float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, a, b, d;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %5};\n\tmov.b64 b, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, x, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add_x2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The softmax warps meet here, and learn whether any thread's `p` holds.
+__device__ __forceinline__ bool softmax_vote(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)p)
+        : "memory");
+    return r != 0;
+}
+
+// A place in the ring and the parity of its use, one block after the other.
+struct Place {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void step(int ring) {
+        if (++at == ring) { at = 0; parity ^= 1; }
+    }
+};
 
 // A wait that a whole warp makes: all lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
@@ -106,7 +152,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         mbar_init(&s.q_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 128);
+            mbar_init(&s.p_full[i], kSoftmax / 32);
         }
         mbar_init(&s.o_done, 1);
         mbar_init(&s.o_last, 1);
@@ -115,11 +161,11 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         s.poison = 0;
         fence_mbarrier_init();
     }
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&s.tmem, kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == kTmaWarp && lane == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_r);
@@ -138,18 +184,22 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // key tiles from this one on are not seen in full by every query
     const int partial = live ? (int)(t.first / kK) : 0;
 
-    if (n > 0 && warp == 4) {
+    if (n > 0 && warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
             bool ok = true;
             int used = 0;                                          // blocks so far
-            auto next = [&](uint8_t*& dst, uint64_t*& bar) {
-                const int i = used % ring;
-                ok = *abort == 0 && mbar_wait(&s.empty[i], ((used / ring) & 1) ^ 1, kWaitNs);
+            Place p;
+            auto next = [&](uint8_t*& dst, uint64_t*& bar, bool partly = false) {
+                ok = *abort == 0 && mbar_wait(&s.empty[p.at], p.parity ^ 1, kWaitNs);
                 if (!ok) return false;
-                dst = Rs + i * kBlock;
-                bar = &s.full[i];
+                dst = Rs + p.at * kBlock;
+                bar = &s.full[p.at];
                 mbar_arrive_expect_tx(bar, kBlock);
+                // the cleaners' turn: they do not follow the ring, so its barrier's
+                // phase alone would not tell them this use from an earlier one
+                if (partly) mbar_arrive(&s.turn[p.at]);
                 ++used;
+                p.step(ring);
                 return true;
             };
             auto keys = [&](int kt) {
@@ -167,10 +217,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 for (int b = 0; b < kBlocksV; ++b) {
                     uint8_t* dst;
                     uint64_t* bar;
-                    if (!next(dst, bar)) return;
-                    // the cleaners' turn: they do not follow the ring, so its barrier's
-                    // phase alone would not tell them this use from an earlier one
-                    if (kt >= partial) mbar_arrive(&s.turn[(used - 1) % ring]);
+                    if (!next(dst, bar, kt >= partial)) return;
                     for (int c = 0; c < VD / 64; ++c)
                         tma_load_3d(dst + c * (kKeysV * 128), &tm_v, bar, c * 64, h, y + b * kKeysV);
                 }
@@ -191,17 +238,17 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     mbar_wait(&s.full[u % ring], (u / ring) & 1, 50000000ull);
             }
         }
-    } else if (n > 0 && warp == 5) {
+    } else if (n > 0 && warp == kMmaWarp) {
         if (elect_one()) {                                         // ---- products
             bool ok = mbar_wait(&s.q_full, 0, kWaitNs);
-            int used = 0;
+            Place p;
             uint32_t cleaned = 0;                                  // parities of the clean barriers
             const uint32_t q_addr = smem_u32(Qs), r_addr = smem_u32(Rs);
             const uint32_t id_s = idesc_bf16_f32(kQ, kK), id_o = idesc_bf16_f32_major(kQ, VD, 0, 1);
             auto scores = [&](int i) {
-                for (int b = 0; b < nk; ++b, ++used) {
-                    const int at = used % ring;
-                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], (used / ring) & 1, kWaitNs);
+                for (int b = 0; b < nk; ++b, p.step(ring)) {
+                    const int at = p.at;
+                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], p.parity, kWaitNs);
                     if (!ok) return;
                     tc_fence_after();
 #pragma unroll
@@ -214,9 +261,9 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             };
             auto values = [&](int i) {
                 ok = *abort == 0 && mbar_wait(&s.p_full[i & 1], (i >> 1) & 1, kWaitNs);
-                for (int b = 0; b < kBlocksV; ++b, ++used) {
-                    const int at = used % ring;
-                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], (used / ring) & 1, kWaitNs);
+                for (int b = 0; b < kBlocksV; ++b, p.step(ring)) {
+                    const int at = p.at;
+                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], p.parity, kWaitNs);
                     if (ok && t.kt0 + i >= partial) {
                         ok = mbar_wait(&s.clean[at], (cleaned >> at) & 1, kWaitNs);
                         cleaned ^= 1u << at;
@@ -247,8 +294,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (n > 0 && warp >= 6) {                               // ---- hidden values
-        const int c = threadIdx.x - 192;
+    } else if (n > 0 && warp >= kCleanWarp) {                               // ---- hidden values
+        const int c = threadIdx.x - kCleanWarp * 32;
         uint32_t turned = 0;                                       // parities of the turn barriers
         for (int i = partial > t.kt0 ? partial - t.kt0 : 0; i < n; ++i) {
             // blocks used before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
@@ -284,45 +331,44 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 break;
             }
         }
-    } else if (warp < 4 && live) {                                 // ---- softmax
-        const int row = threadIdx.x;
-        const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    } else if (warp < kSoftmax / 32 && live) {                     // ---- softmax
+        const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float scale = a.scale * kLog2e;
         const int64_t sees = t.first + row;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;                              // l: of this half's keys
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            ok = warp_wait(&s.s_full[i & 1], (i >> 1) & 1, abort);
-            if (!ok) break;
+            // a warp that gives up votes and meets the others all the same
+            ok = ok && warp_wait(&s.s_full[i & 1], (i >> 1) & 1, abort);
             tc_fence_after();
             const uint32_t at = lane_addr + (i & 1) * kK;
-            float v[4][32];
-            tmem_ld_32cols_x2(at, at + 32, v[0], v[1]);
-            tmem_ld_32cols_x2(at + 64, at + 96, v[2], v[3]);
+            float v[2][32];
+            tmem_ld_32cols_x2(at + half * 64, at + half * 64 + 32, v[0], v[1]);
             if (t.kt0 + i >= partial) {
-                const int64_t left = sees - (int64_t)(t.kt0 + i) * kK;   // keys of the tile that the row sees
+                // this half's keys of the tile that the row sees
+                const int64_t left = sees - (int64_t)(t.kt0 + i) * kK - half * 64;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= left) v[c][e] = -INFINITY;
+                for (int e = 0; e < 64; ++e)
+                    if (e >= left) v[e >> 5][e & 31] = -INFINITY;
             }
-            float top = v[0][0];
+            float tops[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, v[c][e]);
-            top *= scale;
-            const bool raise = top > m + kSlack;                   // of -inf: any logit above it
-            if (__any_sync(0xffffffffu, raise)) {
-                const float mn = raise ? top : m;
-                const float f = raise ? ex2(m - mn) : 1.f;
-                if (i > 0) {
+            for (int e = 4; e < 64; ++e) tops[e & 3] = fmaxf(tops[e & 3], v[e >> 5][e & 31]);
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+            // of -inf: any logit above it
+            if (softmax_vote(top > m + kSlack || !ok)) {
+                s.half[threadIdx.x] = top;
+                ok = !softmax_vote(!ok);                           // all go on, or none
+                if (!ok) break;
+                top = fmaxf(top, s.half[threadIdx.x ^ 128]);
+                const float mn = top > m + kSlack ? top : m;
+                const float f = mn == m ? 1.f : ex2(m - mn);
+                if (__any_sync(0xffffffffu, mn != m) && i > 0) {
                     ok = warp_wait(&s.o_done, (i - 1) & 1, abort);
-                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < VD; c += 32) {
+                    for (int c = half * (VD / 2); c < (half + 1) * (VD / 2) && ok; c += 32) {
                         float o[32];
                         tmem_ld_32cols(lane_addr + kOCol + c, o);
 #pragma unroll
@@ -332,43 +378,47 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 l *= f;
                 m = mn;
+                softmax_vote(false);                               // maxima read: free to be written
             }
-            const float base = m == -INFINITY ? 0.f : m;           // no logit above -inf yet
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float base = m == -INFINITY ? 0.f : -m;          // no logit above -inf yet
+            const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            float w[32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float w[32];
-#pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const float p0 = ex2(fmaf(v[2 * c + (e >> 5)][e & 31], scale, -base));
-                    const float p1 = ex2(fmaf(v[2 * c + (e >> 5)][(e & 31) + 1], scale, -base));
-                    sum[e & 2] += p0;
-                    sum[(e & 2) + 1] += p1;
-                    w[e >> 1] = __uint_as_float(pack(p0, p1));
-                }
-                tmem_st_32cols(at + c * 32, w);
+            for (int e = 0; e < 64; e += 2) {
+                float2 p = fma_x2(make_float2(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, base2);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                sum[(e >> 1) & 1] = add_x2(sum[(e >> 1) & 1], p);
+                w[e >> 1] = __uint_as_float(pack(p.x, p.y));
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_32cols(at + half * 32, w);
+            const float2 both = add_x2(sum[0], sum[1]);
+            l += both.x + both.y;
             tc_fence_before();
-            mbar_arrive(&s.p_full[i & 1]);
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&s.p_full[i & 1]);
         }
-        if (n > 0) ok = ok && warp_wait(&s.o_last, 0, abort);
+        s.half[threadIdx.x] = l;
+        ok = ok && (n == 0 || warp_wait(&s.o_last, 0, abort));
+        ok = !softmax_vote(!ok);
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 65);
             *abort = 1;
         } else {
             tc_fence_after();
+            l += s.half[threadIdx.x ^ 128];
             const int64_t qh = (t.q0 + row) * a.heads + h;
             const bool mine = row < t.n_q;
             const bool poison = n > 0 && *(volatile int32_t*)&s.poison != 0;
             const float inv = 1.f / l;
-            if (a.n_split > 1 && mine)
+            if (a.n_split > 1 && mine && half == 0)
                 *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + split) * 2) = make_float2(m, l);
-            if (a.n_split == 1 && mine && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
+            if (a.n_split == 1 && mine && half == 0 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
             const int64_t from = (int64_t)(partial > t.kt0 ? partial : t.kt0) * kK;
             const int64_t to = sees < (int64_t)t.kt1 * kK ? sees : (int64_t)t.kt1 * kK;
 #pragma unroll 1
-            for (int c = 0; c < VD && n > 0; c += 32) {
+            for (int c = half * (VD / 2); c < (half + 1) * (VD / 2) && n > 0; c += 32) {
                 float o[32];
                 tmem_ld_32cols(lane_addr + kOCol + c, o);
                 if (poison && mine) {
@@ -402,7 +452,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
