@@ -20,7 +20,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kKeys = 32;
-constexpr int kMaxTileQ = 128;                           // queries of the largest tile
+constexpr int kMaxTileQ = 256;                           // queries of the largest tile
 constexpr int kMaxSplit = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -260,7 +260,8 @@ constexpr int64_t kSplitWaves = 4;
 int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b) {
     if (b.n_q < 1) return 1;
     const TileSize ts = tile_size(sh, b);
-    const int64_t units = expanded_slots(b.n_q, b.n_seq, ts.queries) * sh.heads, sms = sm_count();
+    const int64_t units = expanded_slots(b.n_q, b.n_seq, ts.queries) * sh.heads;
+    const int64_t sms = sh.dtype == DSA_BF16 ? sm_count() / 2 : sm_count();   // CTAs, or pairs, at once
     const int64_t tiles = (b.max_kv_len + ts.keys - 1) / ts.keys;
     int32_t best = 1;
     int64_t least = INT64_MAX;

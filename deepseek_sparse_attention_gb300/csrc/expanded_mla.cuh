@@ -74,7 +74,7 @@ __device__ __forceinline__ float expanded_lse(float m, float l) {
 }
 
 // The tensor-core kernel (expanded_mla_tc.cu), bf16: its tiles.
-constexpr int kExpandedTcQ = 128, kExpandedTcK = 128;
+constexpr int kExpandedTcQ = 256, kExpandedTcK = 128;
 cudaError_t launch_expanded_tc(const ExpandedArgs& a, cudaStream_t st);
 
 }  // namespace dsa

@@ -1,14 +1,19 @@
 // expanded_mla_tc.cu -- causal attention over expanded keys and values on the
 // tcgen05 tensor cores (bf16).
 //
-//   S = Q K^T (M = 128 queries, N = 128 keys, K = the head's width), one pass over
-//   the key tiles with a running maximum, O += P V (M = 128, N = v_dim, K = 128 keys)
+//   S = Q K^T (M = 256 queries, N = 128 keys, K = the head's width), one pass over
+//   the key tiles with a running maximum, O += P V (M = 256, N = v_dim, K = 128 keys)
 //
-// One CTA per (tile of 128 queries, head, split of the key tiles):
-//   warp 8     TMA: the queries once, then a ring of 16 KB blocks in the order of
-//              their use -- a tile's keys as blocks of 64 columns (the rope block from
-//              the cache rows, for every head), its values as blocks of 8192 / v_dim keys;
-//   warp 9     issues the products, S of tile t + 1 before O of tile t;
+// A pair of CTAs (cta_group::2) per (tile of 256 queries, head, split of the key
+// tiles): each has 128 of the queries, their S, P and O, and loads half of the keys'
+// rows and half of the values' columns.  In each CTA
+//   warp 8     TMA: the queries once, then a ring of units in the order of their use:
+//              a tile's keys (columns in blocks of 64, the rope block from the cache rows,
+//              for every head), a tile's values.  (Handed over in eight blocks of 8 KB a
+//              tile, with or without a pair, a tile took 3,700 cycles: the threads that
+//              issue copies and products spend some 200 on each hand-over.)
+//   warp 9     in the first CTA issues the products for both, S of tile t + 1 before O
+//              of tile t;
 //   warps 0-7  softmax, a query row and half of its keys to a thread: S from TMEM,
 //              exp, P in bf16 back over S (O takes it from TMEM as its A operand).
 //              Row maxima are raised only when a logit exceeds them by more than
@@ -31,8 +36,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kQ = kExpandedTcQ, kK = kExpandedTcK;      // queries and keys of a tile
-constexpr uint32_t kBlock = 16384;
-constexpr int kMaxRing = 13;
+constexpr int kRows = kQ / 2;                            // queries of a CTA
+constexpr uint32_t kQBlock = kRows * 128;                // 64 columns of them
+constexpr uint32_t kKBlock = kK / 2 * 128;               // 64 columns of a CTA's half of a tile's keys
+constexpr int kMaxRing = 14;
 constexpr int kSoftmax = 256;                            // threads
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int kThreads = 384;
@@ -40,7 +47,7 @@ constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
 constexpr uint32_t kBarBytes = 2048;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kWaitCycles = 4000000000ll;          // about 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                            // weights stay below 2^8
 
@@ -50,24 +57,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], bf16.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-        "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 struct Bars {
-    uint64_t full[kMaxRing], empty[kMaxRing], turn[kMaxRing], clean[kMaxRing];
+    uint64_t full[kMaxRing], empty[kMaxRing], part[kMaxRing], clean[kMaxRing];
     uint64_t q_full, s_full[2], p_full[2], o_done, o_last, drain;
     float half[kSoftmax];                                // maxima, then sums, of a row's halves
     uint32_t tmem;
@@ -116,43 +112,59 @@ struct Place {
     }
 };
 
-// A wait that a whole warp makes: all lanes go on, or none.
+// A wait that ends early when another role gave up.  The clock is the SM's: reading
+// the global timer between two tries cost up to 2,000 cycles after the arrival.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (*abort != 0 || clock64() - t0 > kWaitCycles) return false;
+    return true;
+}
+// The same made by a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
-    const bool ok = *abort == 0 && mbar_wait(bar, parity, kWaitNs);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, wait(bar, parity, abort));
+}
+
+// Room for either kind of unit.
+__host__ __device__ constexpr uint32_t unit_size(int nk, int v_dim) {
+    const uint32_t k = nk * kKBlock, v = v_dim / 128 * (kK * 128);
+    return k > v ? k : v;
 }
 
 template <int VD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
             const ExpandedArgs a, const int32_t slots, const int32_t ring) {
-    constexpr int kKeysV = 8192 / VD;                    // keys of a block of values
-    constexpr int kBlocksV = kK / kKeysV;
+    constexpr uint32_t kVBlock = kK * 128;               // 64 columns of a tile's values
+    constexpr uint32_t kVBytes = VD / 128 * kVBlock;     // a CTA's half of them
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     Bars& s = *reinterpret_cast<Bars*>(smem);
     uint8_t* Qs = smem + kBarBytes;
     const int nk = (a.nope + a.rope) / 64, nope_blocks = a.nope / 64;   // blocks of a tile's keys
-    uint8_t* Rs = Qs + nk * kBlock;
+    const uint32_t unit_bytes = unit_size(nk, VD);       // of the ring
+    uint8_t* Rs = Qs + nk * kQBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a head's tiles one after the other (its keys and values stay in L2), the
     // longest first
-    const int split = (int)(blockIdx.x % a.n_split);
-    const int64_t slot = slots - 1 - (int64_t)(blockIdx.x / a.n_split) % slots;
-    const int h = (int)(blockIdx.x / a.n_split / slots);
+    const uint32_t unit = blockIdx.x / 2, rank = cluster_rank();
+    const int split = (int)(unit % a.n_split);
+    const int64_t slot = slots - 1 - (int64_t)(unit / a.n_split) % slots;
+    const int h = (int)(unit / a.n_split / slots);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
-            mbar_init(&s.turn[i], 1);
-            mbar_init(&s.clean[i], kCleaners);
+            mbar_init(&s.part[i], 1);
+            mbar_init(&s.clean[i], 2 * kCleaners / 32);
         }
         mbar_init(&s.q_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], kSoftmax / 32);
+            mbar_init(&s.p_full[i], 2 * kSoftmax / 32);
         }
         mbar_init(&s.o_done, 1);
         mbar_init(&s.o_last, 1);
@@ -162,8 +174,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(&s.tmem, kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(&s.tmem, kTmemCols);
+        tmem_relinquish_pair();
     }
     if (warp == kTmaWarp && lane == 0) {
         prefetch_tensormap(&tm_q);
@@ -172,7 +184,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         prefetch_tensormap(&tm_v);
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile int32_t* abort = &s.abort;
@@ -187,43 +199,44 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (n > 0 && warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
             bool ok = true;
-            int used = 0;                                          // blocks so far
             Place p;
-            auto next = [&](uint8_t*& dst, uint64_t*& bar, bool partly = false) {
-                ok = *abort == 0 && mbar_wait(&s.empty[p.at], p.parity ^ 1, kWaitNs);
-                if (!ok) return false;
-                dst = Rs + p.at * kBlock;
-                bar = &s.full[p.at];
-                mbar_arrive_expect_tx(bar, kBlock);
-                // the cleaners' turn: they do not follow the ring, so its barrier's
-                // phase alone would not tell them this use from an earlier one
-                if (partly) mbar_arrive(&s.turn[p.at]);
-                ++used;
+            // A unit of both CTAs counts on the first one's barrier -- or, of values that
+            // the cleaners see first, on each CTA's own, and the full barrier's phase passes.
+            auto next = [&](uint32_t bytes, uint32_t& bar, bool partly) -> uint8_t* {
+                ok = wait(&s.empty[p.at], p.parity ^ 1, abort);
+                if (!ok) return nullptr;
+                uint8_t* dst = Rs + p.at * unit_bytes;
+                if (partly) {
+                    bar = smem_u32(&s.part[p.at]);
+                    mbar_arrive_expect_tx(&s.part[p.at], bytes);
+                    if (rank == 0) mbar_arrive(&s.full[p.at]);
+                } else {
+                    bar = cluster_addr(&s.full[p.at], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[p.at], 2 * bytes);
+                }
                 p.step(ring);
-                return true;
+                return dst;
             };
-            auto keys = [&](int kt) {
-                const int32_t y = (int32_t)(t.row0 + (int64_t)kt * kK);
-                for (int b = 0; b < nk; ++b) {
-                    uint8_t* dst;
-                    uint64_t* bar;
-                    if (!next(dst, bar)) return;
-                    if (b < nope_blocks) tma_load_3d(dst, &tm_k, bar, b * 64, h, y);
-                    else tma_load_2d(dst, &tm_r, bar, a.kv_lora + (b - nope_blocks) * 64, y);
+            auto keys = [&](int kt) {                              // half of the tile's rows
+                const int32_t y = (int32_t)(t.row0 + (int64_t)kt * kK + rank * (kK / 2));
+                uint32_t bar;
+                uint8_t* dst = next(nk * kKBlock, bar, false);
+                for (int b = 0; b < nk && ok; ++b) {
+                    if (b < nope_blocks) tma_load_3d_pair(dst + b * kKBlock, &tm_k, bar, b * 64, h, y);
+                    else tma_load_2d_pair(dst + b * kKBlock, &tm_r, bar, a.kv_lora + (b - nope_blocks) * 64, y);
                 }
             };
-            auto values = [&](int kt) {
+            auto values = [&](int kt) {                            // half of the columns
                 const int32_t y = (int32_t)(t.row0 + (int64_t)kt * kK);
-                for (int b = 0; b < kBlocksV; ++b) {
-                    uint8_t* dst;
-                    uint64_t* bar;
-                    if (!next(dst, bar, kt >= partial)) return;
-                    for (int c = 0; c < VD / 64; ++c)
-                        tma_load_3d(dst + c * (kKeysV * 128), &tm_v, bar, c * 64, h, y + b * kKeysV);
-                }
+                uint32_t bar;
+                uint8_t* dst = next(kVBytes, bar, kt >= partial);
+                for (int c = 0; c < VD / 128 && ok; ++c)
+                    tma_load_3d_pair(dst + c * kVBlock, &tm_v, bar, rank * (VD / 2) + c * 64, h, y);
             };
-            mbar_arrive_expect_tx(&s.q_full, nk * kBlock);
-            for (int b = 0; b < nk; ++b) tma_load_3d(Qs + b * kBlock, &tm_q, &s.q_full, b * 64, h, (int32_t)t.q0);
+            if (rank == 0) mbar_arrive_expect_tx(&s.q_full, 2 * nk * kQBlock);
+            for (int b = 0; b < nk; ++b)
+                tma_load_3d_pair(Qs + b * kQBlock, &tm_q, cluster_addr(&s.q_full, 0), b * 64, h,
+                                 (int32_t)(t.q0 + rank * kRows));
             keys(t.kt0);
             for (int i = 0; i < n && ok; ++i) {
                 if (i + 1 < n) keys(t.kt0 + i + 1);
@@ -232,52 +245,50 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!ok) {
                 record_error(a.err, kDevTimeout, blockIdx.x, 62);
                 *abort = 1;
-                // copies in flight land first
-                mbar_wait(&s.q_full, 0, 50000000ull);
-                for (int u = used > ring ? used - ring : 0; u < used; ++u)
-                    mbar_wait(&s.full[u % ring], (u / ring) & 1, 50000000ull);
+                // copies in flight land first: their barriers are partly the other CTA's
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 50000000ull) {}
             }
         }
-    } else if (n > 0 && warp == kMmaWarp) {
+    } else if (n > 0 && warp == kMmaWarp && rank == 0) {
         if (elect_one()) {                                         // ---- products
-            bool ok = mbar_wait(&s.q_full, 0, kWaitNs);
+            bool ok = wait(&s.q_full, 0, abort);
             Place p;
             uint32_t cleaned = 0;                                  // parities of the clean barriers
             const uint32_t q_addr = smem_u32(Qs), r_addr = smem_u32(Rs);
             const uint32_t id_s = idesc_bf16_f32(kQ, kK), id_o = idesc_bf16_f32_major(kQ, VD, 0, 1);
             auto scores = [&](int i) {
-                for (int b = 0; b < nk; ++b, p.step(ring)) {
-                    const int at = p.at;
-                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], p.parity, kWaitNs);
-                    if (!ok) return;
-                    tc_fence_after();
+                ok = ok && wait(&s.full[p.at], p.parity, abort);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t k_addr = r_addr + p.at * unit_bytes, d = tmem + (i & 1) * kK;
+                for (int b = 0; b < nk; ++b) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss(tmem + (i & 1) * kK, sdesc_kmajor_sw128(q_addr + b * kBlock + kk * 32),
-                                    sdesc_kmajor_sw128(r_addr + at * kBlock + kk * 32), id_s, (b | kk) != 0);
-                    mma_commit(&s.empty[at]);
+                        mma_bf16_ss_pair(d, sdesc_kmajor_sw128(q_addr + b * kQBlock + kk * 32),
+                                         sdesc_kmajor_sw128(k_addr + b * kKBlock + kk * 32), id_s, (b | kk) != 0);
                 }
-                mma_commit(&s.s_full[i & 1]);
+                mma_commit_pair(&s.empty[p.at]);
+                mma_commit_pair(&s.s_full[i & 1]);
+                p.step(ring);
             };
             auto values = [&](int i) {
-                ok = *abort == 0 && mbar_wait(&s.p_full[i & 1], (i >> 1) & 1, kWaitNs);
-                for (int b = 0; b < kBlocksV; ++b, p.step(ring)) {
-                    const int at = p.at;
-                    ok = ok && *abort == 0 && mbar_wait(&s.full[at], p.parity, kWaitNs);
-                    if (ok && t.kt0 + i >= partial) {
-                        ok = mbar_wait(&s.clean[at], (cleaned >> at) & 1, kWaitNs);
-                        cleaned ^= 1u << at;
-                    }
-                    if (!ok) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kKeysV / 16; ++kk)
-                        mma_bf16_ts(tmem + kOCol, tmem + (i & 1) * kK + (b * kKeysV + kk * 16) / 2,
-                                    sdesc_sw128(r_addr + at * kBlock + kk * 2048, kKeysV * 128, 1024), id_o,
-                                    (i | b | kk) != 0);
-                    mma_commit(&s.empty[at]);
+                ok = wait(&s.full[p.at], p.parity, abort);
+                if (ok && t.kt0 + i >= partial) {
+                    ok = wait(&s.clean[p.at], (cleaned >> p.at) & 1, abort);
+                    cleaned ^= 1u << p.at;
                 }
-                mma_commit(&s.o_done);
+                ok = ok && wait(&s.p_full[i & 1], (i >> 1) & 1, abort);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t v_addr = r_addr + p.at * unit_bytes, w = tmem + (i & 1) * kK;
+#pragma unroll
+                for (int kk = 0; kk < kK / 16; ++kk)
+                    mma_bf16_ts_pair(tmem + kOCol, w + kk * 8, sdesc_sw128(v_addr + kk * 2048, kVBlock, 1024), id_o,
+                                     (i | kk) != 0);
+                mma_commit_pair(&s.empty[p.at]);
+                mma_commit_pair(&s.o_done);
+                p.step(ring);
             };
             scores(0);
             for (int i = 0; i < n && ok; ++i) {
@@ -285,54 +296,60 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (ok) values(i);
             }
             if (ok) {
-                mma_commit(&s.o_last);
+                mma_commit_pair(&s.o_last);
             } else {
                 record_error(a.err, kDevTimeout, blockIdx.x, 63);
                 *abort = 1;
-                mma_commit(&s.drain);                              // every issued product retired
+                mma_commit_pair(&s.drain);                         // every issued product retired
                 mbar_wait(&s.drain, 0, 50000000ull);
             }
         }
         __syncwarp();
-    } else if (n > 0 && warp >= kCleanWarp) {                               // ---- hidden values
+    } else if (n > 0 && warp >= kCleanWarp) {                      // ---- hidden values
         const int c = threadIdx.x - kCleanWarp * 32;
-        uint32_t turned = 0;                                       // parities of the turn barriers
+        uint32_t parted = 0;                                       // parities of the part barriers
         for (int i = partial > t.kt0 ? partial - t.kt0 : 0; i < n; ++i) {
-            // blocks used before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
-            const uint32_t first = (uint32_t)((i + 1 < n ? i + 2 : n) * nk + i * kBlocksV);
-            bool ok = true;
-            for (int b = 0; b < kBlocksV; ++b) {
-                const uint32_t u = first + b, at = u % ring;
-                ok = warp_wait(&s.turn[at], (turned >> at) & 1, abort) &&
-                     warp_wait(&s.full[at], (u / ring) & 1, abort);
-                turned ^= 1u << at;
-                if (!ok) break;
-                uint4* p = reinterpret_cast<uint4*>(Rs + at * kBlock);
-                bool bad = false;
-#pragma unroll 8
-                for (int k = 0; k < (int)kBlock / 16 / kCleaners; ++k) {
-                    uint4 x = p[c + k * kCleaners];
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-                    bool here = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; here = true; }
-                        if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; here = true; }
-                    }
-                    if (here) { p[c + k * kCleaners] = x; bad = true; }
-                }
-                if (bad) *(volatile int32_t*)&s.poison = 1;
-                fence_proxy_async_smem();
-                mbar_arrive(&s.clean[at]);
-            }
+            // units used before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
+            const uint32_t at = (uint32_t)((i + 1 < n ? i + 2 : n) + i) % ring;
+            const bool ok = warp_wait(&s.part[at], (parted >> at) & 1, abort);
+            parted ^= 1u << at;
             if (!ok) {
                 if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 64);
                 *abort = 1;
                 break;
             }
+            uint4* p = reinterpret_cast<uint4*>(Rs + at * unit_bytes) + c;
+            // an exponent of ones carries into its half's sign
+            auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+            bool bad = false;
+#pragma unroll 1
+            for (int k = 0; k < (int)(kVBytes / 16 / kCleaners); k += 8) {
+                uint4 x[8];
+                uint32_t any = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = p[(k + e) * kCleaners];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) any |= odd(x[e].x) | odd(x[e].y) | odd(x[e].z) | odd(x[e].w);
+                if (any == 0) continue;
+                bad = true;
+                // the halves that are odd become zeros
+                auto clean = [&](uint32_t w) { const uint32_t m = odd(w) >> 15; return w & ~(m * 0xffffu); };
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    p[(k + e) * kCleaners] = make_uint4(clean(x[e].x), clean(x[e].y), clean(x[e].z), clean(x[e].w));
+            }
+            if (bad) {                                             // both CTAs give them back
+                *(volatile int32_t*)&s.poison = 1;
+                st_cluster(cluster_addr(&s.poison, rank ^ 1), 1);
+                fence_cluster();
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.clean[at], 0));
         }
     } else if (warp < kSoftmax / 32 && live) {                     // ---- softmax
-        const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+        const int mine_row = threadIdx.x & 127, half = threadIdx.x >> 7;
+        const int row = (int)rank * kRows + mine_row;              // of the pair's queries
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float scale = a.scale * kLog2e;
         const int64_t sees = t.first + row;
@@ -397,7 +414,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             l += both.x + both.y;
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&s.p_full[i & 1]);
+            if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&s.p_full[i & 1], 0));
         }
         s.half[threadIdx.x] = l;
         ok = ok && (n == 0 || warp_wait(&s.o_last, 0, abort));
@@ -450,11 +467,13 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
     }
+    __syncwarp();
+    // neither CTA leaves while the other's products or signals still reach it
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
@@ -468,23 +487,24 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
         const uint32_t b[3] = {64, 1, box};
         return encode_bf16_map(m, base, 3, dims, strides, b);
     };
-    if (!heads_map(&tq, a.q, d, (uint64_t)a.b.n_q, kQ) || !heads_map(&tk, a.k_nope, (uint64_t)a.nope, rows, kK) ||
-        !heads_map(&tv, a.v, VD, rows, 8192 / VD))
+    if (!heads_map(&tq, a.q, d, (uint64_t)a.b.n_q, kRows) ||
+        !heads_map(&tk, a.k_nope, (uint64_t)a.nope, rows, kK / 2) || !heads_map(&tv, a.v, VD, rows, kK))
         return cudaErrorInvalidValue;
     tr = tk;
     if (a.rope > 0) {
         const uint64_t dims[2] = {(uint64_t)a.width, rows}, strides[1] = {(uint64_t)a.width * 2};
-        const uint32_t b[2] = {64, kK};
+        const uint32_t b[2] = {64, kK / 2};
         if (!encode_bf16_map(&tr, a.rows, 2, dims, strides, b)) return cudaErrorInvalidValue;
     }
     auto kern = expanded_tc<VD>;
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem);
     if (e != cudaSuccess) return e;
-    int ring = (int)((kSmem - 1024 - kBarBytes) / kBlock - d / 64);
+    const int nk = (int)(d / 64);
+    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
-    return launch_pdl(kern, dim3((unsigned)(slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr, tv,
-                      a, (int32_t)slots, (int32_t)ring);
+    return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr,
+                      tv, a, (int32_t)slots, (int32_t)ring);
 }
 
 }  // namespace
