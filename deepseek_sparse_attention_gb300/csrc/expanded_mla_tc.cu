@@ -4,14 +4,15 @@
 //   S = Q K^T (M = 256 queries, N = 128 keys, K = the head's width), one pass over
 //   the key tiles with a running maximum, O += P V (M = 256, N = v_dim, K = 128 keys)
 //
-// A pair of CTAs (cta_group::2) per (tile of 256 queries, head, split of the key
-// tiles): each has 128 of the queries, their S, P and O, and loads half of the keys'
-// rows and half of the values' columns.  In each CTA
-//   warp 8     TMA: the queries once, then a ring of units in the order of their use:
-//              a tile's keys (columns in blocks of 64, the rope block from the cache rows,
-//              for every head), a tile's values.  (Handed over in eight blocks of 8 KB a
-//              tile, with or without a pair, a tile took 3,700 cycles: the threads that
-//              issue copies and products spend some 200 on each hand-over.)
+// A unit of work is a tile of 256 queries of a sequence, a head and a split of the key
+// tiles; a pair of CTAs (cta_group::2) takes one after the other, each with 128 of the
+// queries, their S, P and O, and half of the keys' rows and of the values' columns to load.
+// The next unit is one whose launch the pair cancels (clusterlaunchcontrol), asked for a unit
+// ahead, so that its copies and first products run while the last one's output is written.
+// In each CTA
+//   warp 8     TMA: the queries, and a ring of a tile's keys (columns in blocks of 64, the
+//              rope block from the cache rows, for every head) or a tile's values in
+//              the order of their use; hands out the units of work;
 //   warp 9     in the first CTA issues the products for both, S of tile t + 1 before O
 //              of tile t;
 //   warps 0-7  softmax, a query row and half of its keys to a thread: S from TMEM,
@@ -19,10 +20,16 @@
 //              Row maxima are raised only when a logit exceeds them by more than
 //              kSlack, so the two halves of a row share a maximum without telling each
 //              other theirs: a barrier that also votes says whether any row is raised,
-//              and only then they are exchanged and O is rescaled in TMEM;
+//              and only then they are exchanged and O is rescaled in TMEM.  At the end
+//              O to the output or the split's part, through shared memory;
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
 //              epilogue to the queries that see them.
+// A key tile takes 2,050 cycles (head width and v_dim 256), which are the products' own: S
+// and O of 1,024 each.  What it took before: a unit's launch to itself, with its start, its
+// output and nothing beside them, 11,000 cycles; copies and products handed over in eight
+// blocks a tile, 3,700 cycles a tile, some 200 a hand-over; arrivals that release to the
+// cluster, 1,000 to 3,000 cycles each (sm100.cuh).
 // P is rounded to bf16 because both operands of the value product have one
 // type and V is bf16: 2^-8 of a weight at most, of random sign.
 #include <math.h>
@@ -39,7 +46,9 @@ constexpr int kQ = kExpandedTcQ, kK = kExpandedTcK;      // queries and keys of 
 constexpr int kRows = kQ / 2;                            // queries of a CTA
 constexpr uint32_t kQBlock = kRows * 128;                // 64 columns of them
 constexpr uint32_t kKBlock = kK / 2 * 128;               // 64 columns of a CTA's half of a tile's keys
-constexpr int kMaxRing = 14;
+constexpr int kMaxRing = 11;
+constexpr int kWorks = 4;                                // units of work handed out at a time
+constexpr uint32_t kStage = kRows / 4 * 128;             // a softmax warp's piece of the output: 32 rows of 128 bytes
 constexpr int kSoftmax = 256;                            // threads
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr int kThreads = 384;
@@ -62,14 +71,48 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-struct Bars {
+// A unit of work as the roles read it.
+struct Work {
+    int64_t q0, row0, first;                             // as ExpandedTile, of the pair
+    int32_t n_q, kt0, n;                                 // n: its key tiles, -1: no more work
+    int32_t partial;                                     // key tiles from this one on are not seen in full by every query
+    int32_t h, split;
+};
+
+struct Shared {
     uint64_t full[kMaxRing], empty[kMaxRing], part[kMaxRing], clean[kMaxRing];
-    uint64_t q_full, s_full[2], p_full[2], o_done, o_last, drain;
+    uint64_t q_full, q_free, s_full[2], p_full[2], o_done, o_free, o_last, drain;
+    uint64_t work_full[kWorks], work_free[kWorks], next_full[2], next_free[2];
+    alignas(16) uint4 next[2];                           // answers to the requests for work
+    Work work[kWorks];
     float half[kSoftmax];                                // maxima, then sums, of a row's halves
     uint32_t tmem;
-    int32_t abort, poison;
+    int32_t abort, poison[2];                            // poison: the last unit that met odd values
 };
-static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+static_assert(sizeof(Shared) <= kBarBytes, "barriers");
+
+// Asks for a cluster that has not been launched, in its place; the answer goes to
+// both CTAs of the pair.
+__device__ __forceinline__ void ask_work(uint4* answer, uint64_t* bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(answer)), "r"(smem_u32(bar))
+        : "memory");
+}
+// The first block of the cluster that the answer gives, or -1.
+__device__ __forceinline__ int64_t answer_block(const uint4* answer) {
+    uint32_t given, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+        : "=r"(given), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return given ? (int64_t)x : -1;
+}
 
 // Two at a time: x * a + b, and sums.
 __device__ __forceinline__ float2 fma_x2(float2 x, float2 a, float2 b) {
@@ -141,18 +184,13 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     constexpr uint32_t kVBytes = VD / 128 * kVBlock;     // a CTA's half of them
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    Bars& s = *reinterpret_cast<Bars*>(smem);
+    Shared& s = *reinterpret_cast<Shared*>(smem);
     uint8_t* Qs = smem + kBarBytes;
     const int nk = (a.nope + a.rope) / 64, nope_blocks = a.nope / 64;   // blocks of a tile's keys
     const uint32_t unit_bytes = unit_size(nk, VD);       // of the ring
     uint8_t* Rs = Qs + nk * kQBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a head's tiles one after the other (its keys and values stay in L2), the
-    // longest first
-    const uint32_t unit = blockIdx.x / 2, rank = cluster_rank();
-    const int split = (int)(unit % a.n_split);
-    const int64_t slot = slots - 1 - (int64_t)(unit / a.n_split) % slots;
-    const int h = (int)(unit / a.n_split / slots);
+    const uint32_t rank = cluster_rank();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxRing; ++i) {
@@ -162,15 +200,24 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_init(&s.clean[i], 2 * kCleaners / 32);
         }
         mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 2 * kSoftmax / 32);
+            mbar_init(&s.next_full[i], 1);
+            mbar_init(&s.next_free[i], 1);
+            s.poison[i] = 0;
+        }
+        for (int i = 0; i < kWorks; ++i) {
+            mbar_init(&s.work_full[i], 1);
+            // the softmax's and the cleaners' warps, and the products' thread
+            mbar_init(&s.work_free[i], (kSoftmax + kCleaners) / 32 + (rank == 0 ? 1 : 0));
         }
         mbar_init(&s.o_done, 1);
+        mbar_init(&s.o_free, 2 * kSoftmax / 32);
         mbar_init(&s.o_last, 1);
         mbar_init(&s.drain, 1);
         s.abort = 0;
-        s.poison = 0;
         fence_mbarrier_init();
     }
     if (warp == kMmaWarp) {
@@ -190,13 +237,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     volatile int32_t* abort = &s.abort;
     pdl_wait();
     pdl_trigger();
-    ExpandedTile t;
-    const bool live = expanded_tile(a.b, slot, split, a.n_split, kQ, kK, threadIdx.x == 0 ? a.err : nullptr, 61, t);
-    const int n = live ? t.kt1 - t.kt0 : 0;
-    // key tiles from this one on are not seen in full by every query
-    const int partial = live ? (int)(t.first / kK) : 0;
 
-    if (n > 0 && warp == kTmaWarp) {
+    if (warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
             bool ok = true;
             Place p;
@@ -217,51 +259,102 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 p.step(ring);
                 return dst;
             };
-            auto keys = [&](int kt) {                              // half of the tile's rows
-                const int32_t y = (int32_t)(t.row0 + (int64_t)kt * kK + rank * (kK / 2));
-                uint32_t bar;
-                uint8_t* dst = next(nk * kKBlock, bar, false);
-                for (int b = 0; b < nk && ok; ++b) {
-                    if (b < nope_blocks) tma_load_3d_pair(dst + b * kKBlock, &tm_k, bar, b * 64, h, y);
-                    else tma_load_2d_pair(dst + b * kKBlock, &tm_r, bar, a.kv_lora + (b - nope_blocks) * 64, y);
+            int64_t block = blockIdx.x - rank;                     // the pair's
+            int busy = 0;                                          // units of work with key tiles so far
+            bool asked = false;
+            for (uint32_t k = 0; ok; ++k) {
+                // ask for the unit after this one: the request needs both CTAs' leave
+                if (block >= 0) {
+                    mbar_arrive_expect_tx(&s.next_full[k & 1], 16);
+                    if (rank == 0) {
+                        ok = k < 2 || wait(&s.next_free[k & 1], ((k >> 1) - 1) & 1, abort);
+                        if (!ok) break;
+                        ask_work(&s.next[k & 1], &s.next_full[k & 1]);
+                    }
+                    asked = true;
                 }
-            };
-            auto values = [&](int kt) {                            // half of the columns
-                const int32_t y = (int32_t)(t.row0 + (int64_t)kt * kK);
-                uint32_t bar;
-                uint8_t* dst = next(kVBytes, bar, kt >= partial);
-                for (int c = 0; c < VD / 128 && ok; ++c)
-                    tma_load_3d_pair(dst + c * kVBlock, &tm_v, bar, rank * (VD / 2) + c * 64, h, y);
-            };
-            if (rank == 0) mbar_arrive_expect_tx(&s.q_full, 2 * nk * kQBlock);
-            for (int b = 0; b < nk; ++b)
-                tma_load_3d_pair(Qs + b * kQBlock, &tm_q, cluster_addr(&s.q_full, 0), b * 64, h,
-                                 (int32_t)(t.q0 + rank * kRows));
-            keys(t.kt0);
-            for (int i = 0; i < n && ok; ++i) {
-                if (i + 1 < n) keys(t.kt0 + i + 1);
-                if (ok) values(t.kt0 + i);
+                // this one: a head's tiles one after the other (its keys and values stay in
+                // L2), the longest first
+                ExpandedTile t;
+                Work w;
+                w.n = -1;
+                if (block >= 0) {
+                    const uint32_t unit = (uint32_t)(block / 2);
+                    w.split = (int)(unit % a.n_split);
+                    w.h = (int)(unit / a.n_split / slots);
+                    const int64_t slot = slots - 1 - (int64_t)(unit / a.n_split % slots);
+                    if (!expanded_tile(a.b, slot, w.split, a.n_split, kQ, kK, w.h == 0 ? a.err : nullptr, 61, t)) {
+                        t.n_q = 0;
+                        t.kt0 = t.kt1 = 0;
+                        t.q0 = t.row0 = t.first = 0;
+                    }
+                    w.q0 = t.q0; w.row0 = t.row0; w.first = t.first;
+                    w.n_q = t.n_q; w.kt0 = t.kt0; w.n = t.kt1 - t.kt0;
+                    w.partial = (int)(t.first / kK);
+                }
+                ok = k < kWorks || wait(&s.work_free[k % kWorks], (k / kWorks - 1) & 1, abort);
+                if (!ok) break;
+                s.work[k % kWorks] = w;
+                mbar_arrive(&s.work_full[k % kWorks]);
+                if (w.n < 0) break;
+                if (w.n > 0) {
+                    auto keys = [&](int kt) {                      // half of the tile's rows
+                        const int32_t y = (int32_t)(w.row0 + (int64_t)kt * kK + rank * (kK / 2));
+                        uint32_t bar;
+                        uint8_t* dst = next(nk * kKBlock, bar, false);
+                        for (int b = 0; b < nk && ok; ++b) {
+                            if (b < nope_blocks) tma_load_3d_pair(dst + b * kKBlock, &tm_k, bar, b * 64, w.h, y);
+                            else tma_load_2d_pair(dst + b * kKBlock, &tm_r, bar, a.kv_lora + (b - nope_blocks) * 64, y);
+                        }
+                    };
+                    auto values = [&](int kt) {                    // half of the columns
+                        const int32_t y = (int32_t)(w.row0 + (int64_t)kt * kK);
+                        uint32_t bar;
+                        uint8_t* dst = next(kVBytes, bar, kt >= w.partial);
+                        for (int c = 0; c < VD / 128 && ok; ++c)
+                            tma_load_3d_pair(dst + c * kVBlock, &tm_v, bar, rank * (VD / 2) + c * 64, w.h, y);
+                    };
+                    keys(w.kt0);
+                    ok = ok && (busy == 0 || wait(&s.q_free, (busy - 1) & 1, abort));
+                    if (!ok) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&s.q_full, 2 * nk * kQBlock);
+                    for (int b = 0; b < nk; ++b)
+                        tma_load_3d_pair(Qs + b * kQBlock, &tm_q, cluster_addr(&s.q_full, 0), b * 64, w.h,
+                                         (int32_t)(w.q0 + rank * kRows));
+                    for (int i = 0; i < w.n && ok; ++i) {
+                        if (i + 1 < w.n) keys(w.kt0 + i + 1);
+                        if (ok) values(w.kt0 + i);
+                    }
+                    ++busy;
+                }
+                ok = ok && wait(&s.next_full[k & 1], (k >> 1) & 1, abort);
+                if (!ok) break;
+                asked = false;
+                block = answer_block(&s.next[k & 1]);
+                fence_proxy_async_smem();                          // read before the next answer is written
+                if (rank != 0) mbar_arrive_cluster(cluster_addr(&s.next_free[k & 1], 0));
             }
             if (!ok) {
                 record_error(a.err, kDevTimeout, blockIdx.x, 62);
                 *abort = 1;
-                // copies in flight land first: their barriers are partly the other CTA's
+                // copies and answers in flight land first: their barriers are partly the other CTA's
                 const uint64_t t0 = globaltimer_ns();
-                while (globaltimer_ns() - t0 < 50000000ull) {}
+                while (globaltimer_ns() - t0 < (asked ? 100000000ull : 50000000ull)) {}
             }
         }
-    } else if (n > 0 && warp == kMmaWarp && rank == 0) {
-        if (elect_one()) {                                         // ---- products
-            bool ok = wait(&s.q_full, 0, abort);
+    } else if (warp == kMmaWarp) {
+        if (rank == 0 && elect_one()) {                            // ---- products
+            bool ok = true;
             Place p;
+            uint32_t g = 0, busy = 0;                              // key tiles and units of work so far
             uint32_t cleaned = 0;                                  // parities of the clean barriers
             const uint32_t q_addr = smem_u32(Qs), r_addr = smem_u32(Rs);
             const uint32_t id_s = idesc_bf16_f32(kQ, kK), id_o = idesc_bf16_f32_major(kQ, VD, 0, 1);
-            auto scores = [&](int i) {
+            auto scores = [&](uint32_t tile) {
                 ok = ok && wait(&s.full[p.at], p.parity, abort);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t k_addr = r_addr + p.at * unit_bytes, d = tmem + (i & 1) * kK;
+                const uint32_t k_addr = r_addr + p.at * unit_bytes, d = tmem + (tile & 1) * kK;
                 for (int b = 0; b < nk; ++b) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -269,35 +362,49 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                          sdesc_kmajor_sw128(k_addr + b * kKBlock + kk * 32), id_s, (b | kk) != 0);
                 }
                 mma_commit_pair(&s.empty[p.at]);
-                mma_commit_pair(&s.s_full[i & 1]);
+                mma_commit_pair(&s.s_full[tile & 1]);
                 p.step(ring);
             };
-            auto values = [&](int i) {
+            auto values = [&](uint32_t tile, bool more, bool partly) {
                 ok = wait(&s.full[p.at], p.parity, abort);
-                if (ok && t.kt0 + i >= partial) {
+                if (ok && partly) {
                     ok = wait(&s.clean[p.at], (cleaned >> p.at) & 1, abort);
                     cleaned ^= 1u << p.at;
                 }
-                ok = ok && wait(&s.p_full[i & 1], (i >> 1) & 1, abort);
+                ok = ok && wait(&s.p_full[tile & 1], (tile >> 1) & 1, abort);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t v_addr = r_addr + p.at * unit_bytes, w = tmem + (i & 1) * kK;
+                const uint32_t v_addr = r_addr + p.at * unit_bytes, w = tmem + (tile & 1) * kK;
 #pragma unroll
                 for (int kk = 0; kk < kK / 16; ++kk)
                     mma_bf16_ts_pair(tmem + kOCol, w + kk * 8, sdesc_sw128(v_addr + kk * 2048, kVBlock, 1024), id_o,
-                                     (i | kk) != 0);
+                                     more || kk != 0);
                 mma_commit_pair(&s.empty[p.at]);
                 mma_commit_pair(&s.o_done);
                 p.step(ring);
             };
-            scores(0);
-            for (int i = 0; i < n && ok; ++i) {
-                if (i + 1 < n) scores(i + 1);
-                if (ok) values(i);
+            for (uint32_t k = 0; ok; ++k) {
+                ok = wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
+                if (!ok) break;
+                const int n = s.work[k % kWorks].n;
+                const int partial = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
+                mbar_arrive(&s.work_free[k % kWorks]);
+                if (n < 0) break;
+                if (n == 0) continue;
+                ok = wait(&s.q_full, busy & 1, abort);
+                scores(g);
+                for (int i = 0; i < n && ok; ++i) {
+                    if (i + 1 < n) scores(g + i + 1);
+                    if (i == (n > 1 ? n - 2 : 0)) mma_commit_pair(&s.q_free);   // the last scores are issued
+                    // the last unit's O has been read
+                    if (i == 0 && busy > 0) ok = ok && wait(&s.o_free, (busy - 1) & 1, abort);
+                    if (ok) values(g + i, i > 0, i >= partial);
+                }
+                if (ok) mma_commit_pair(&s.o_last);
+                g += n;
+                ++busy;
             }
-            if (ok) {
-                mma_commit_pair(&s.o_last);
-            } else {
+            if (!ok) {
                 record_error(a.err, kDevTimeout, blockIdx.x, 63);
                 *abort = 1;
                 mma_commit_pair(&s.drain);                         // every issued product retired
@@ -305,170 +412,241 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (n > 0 && warp >= kCleanWarp) {                      // ---- hidden values
+    } else if (warp >= kCleanWarp) {                               // ---- hidden values
         const int c = threadIdx.x - kCleanWarp * 32;
         uint32_t parted = 0;                                       // parities of the part barriers
-        for (int i = partial > t.kt0 ? partial - t.kt0 : 0; i < n; ++i) {
-            // units used before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
-            const uint32_t at = (uint32_t)((i + 1 < n ? i + 2 : n) + i) % ring;
-            const bool ok = warp_wait(&s.part[at], (parted >> at) & 1, abort);
-            parted ^= 1u << at;
-            if (!ok) {
-                if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 64);
-                *abort = 1;
-                break;
-            }
-            uint4* p = reinterpret_cast<uint4*>(Rs + at * unit_bytes) + c;
-            // an exponent of ones carries into its half's sign
-            auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-            bool bad = false;
-#pragma unroll 1
-            for (int k = 0; k < (int)(kVBytes / 16 / kCleaners); k += 8) {
-                uint4 x[8];
-                uint32_t any = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = p[(k + e) * kCleaners];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) any |= odd(x[e].x) | odd(x[e].y) | odd(x[e].z) | odd(x[e].w);
-                if (any == 0) continue;
-                bad = true;
-                // the halves that are odd become zeros
-                auto clean = [&](uint32_t w) { const uint32_t m = odd(w) >> 15; return w & ~(m * 0xffffu); };
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    p[(k + e) * kCleaners] = make_uint4(clean(x[e].x), clean(x[e].y), clean(x[e].z), clean(x[e].w));
-            }
-            if (bad) {                                             // both CTAs give them back
-                *(volatile int32_t*)&s.poison = 1;
-                st_cluster(cluster_addr(&s.poison, rank ^ 1), 1);
-                fence_cluster();
-            }
-            fence_proxy_async_smem();
+        uint32_t before = 0;                                       // units of the ring before this work's
+        int32_t busy = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            ok = warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
+            if (!ok) break;
+            const int n = s.work[k % kWorks].n;
+            const int partial = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.clean[at], 0));
+            if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
+            if (n < 0) break;
+            if (n == 0) continue;
+            ++busy;
+            for (int i = partial > 0 ? partial : 0; i < n; ++i) {
+                // before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
+                const uint32_t at = (before + (uint32_t)((i + 1 < n ? i + 2 : n) + i)) % ring;
+                ok = warp_wait(&s.part[at], (parted >> at) & 1, abort);
+                parted ^= 1u << at;
+                if (!ok) break;
+                uint4* p = reinterpret_cast<uint4*>(Rs + at * unit_bytes) + c;
+                // an exponent of ones carries into its half's sign
+                auto odd = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                bool bad = false;
+#pragma unroll 1
+                for (int e0 = 0; e0 < (int)(kVBytes / 16 / kCleaners); e0 += 8) {
+                    uint4 x[8];
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = p[(e0 + e) * kCleaners];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) any |= odd(x[e].x) | odd(x[e].y) | odd(x[e].z) | odd(x[e].w);
+                    if (any == 0) continue;
+                    bad = true;
+                    // the halves that are odd become zeros
+                    auto clean = [&](uint32_t w) { return w & ~((odd(w) >> 15) * 0xffffu); };
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        p[(e0 + e) * kCleaners] = make_uint4(clean(x[e].x), clean(x[e].y), clean(x[e].z), clean(x[e].w));
+                }
+                if (bad) {                                         // both CTAs give them back
+                    *(volatile int32_t*)&s.poison[busy & 1] = busy;
+                    st_cluster(cluster_addr(&s.poison[busy & 1], rank ^ 1), busy);
+                    fence_cluster();
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.clean[at], 0));
+            }
+            before = (before + 2u * (uint32_t)n) % ring;
         }
-    } else if (warp < kSoftmax / 32 && live) {                     // ---- softmax
-        const int mine_row = threadIdx.x & 127, half = threadIdx.x >> 7;
-        const int row = (int)rank * kRows + mine_row;              // of the pair's queries
+        if (!ok) {
+            if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 64);
+            *abort = 1;
+        }
+    } else {                                                       // ---- softmax
+        const int row = (int)rank * kRows + (threadIdx.x & 127);   // of the pair's queries
+        const int half = threadIdx.x >> 7;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float scale = a.scale * kLog2e;
-        const int64_t sees = t.first + row;
-        float m = -INFINITY, l = 0.f;                              // l: of this half's keys
+        uint8_t* stage = Rs + ring * unit_bytes + warp * kStage;
+        uint32_t g = 0;
+        int32_t busy = 0;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            // a warp that gives up votes and meets the others all the same
-            ok = ok && warp_wait(&s.s_full[i & 1], (i >> 1) & 1, abort);
-            tc_fence_after();
-            const uint32_t at = lane_addr + (i & 1) * kK;
-            float v[2][32];
-            tmem_ld_32cols_x2(at + half * 64, at + half * 64 + 32, v[0], v[1]);
-            if (t.kt0 + i >= partial) {
-                // this half's keys of the tile that the row sees
-                const int64_t left = sees - (int64_t)(t.kt0 + i) * kK - half * 64;
+        for (uint32_t k = 0; ; ++k) {
+            ok = warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
+            if (softmax_vote(!ok)) { ok = false; break; }
+            const Work w = s.work[k % kWorks];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
+            const int n = w.n;
+            if (n < 0) break;
+            float m = -INFINITY, l = 0.f;                          // l: of this half's keys
+            const int64_t sees = w.first + row;
+            for (int i = 0; i < n; ++i, ++g) {
+                // a warp that gives up votes and meets the others all the same
+                ok = ok && warp_wait(&s.s_full[g & 1], (g >> 1) & 1, abort);
+                tc_fence_after();
+                const uint32_t at = lane_addr + (g & 1) * kK;
+                float v[2][32];
+                tmem_ld_32cols_x2(at + half * 64, at + half * 64 + 32, v[0], v[1]);
+                if (w.kt0 + i >= w.partial) {
+                    // this half's keys of the tile that the row sees
+                    const int64_t here = sees - (int64_t)(w.kt0 + i) * kK - half * 64;
+                    const int left = here < 0 ? 0 : here > 64 ? 64 : (int)here;
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e >= left) v[e >> 5][e & 31] = -INFINITY;
-            }
-            float tops[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
+                    for (int e = 0; e < 64; ++e)
+                        if (e >= left) v[e >> 5][e & 31] = -INFINITY;
+                }
+                float tops[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
 #pragma unroll
-            for (int e = 4; e < 64; ++e) tops[e & 3] = fmaxf(tops[e & 3], v[e >> 5][e & 31]);
-            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
-            // of -inf: any logit above it
-            if (softmax_vote(top > m + kSlack || !ok)) {
-                s.half[threadIdx.x] = top;
-                ok = !softmax_vote(!ok);                           // all go on, or none
-                if (!ok) break;
-                top = fmaxf(top, s.half[threadIdx.x ^ 128]);
-                const float mn = top > m + kSlack ? top : m;
-                const float f = mn == m ? 1.f : ex2(m - mn);
-                if (__any_sync(0xffffffffu, mn != m) && i > 0) {
-                    ok = warp_wait(&s.o_done, (i - 1) & 1, abort);
-                    tc_fence_after();
+                for (int e = 4; e < 64; ++e) tops[e & 3] = fmaxf(tops[e & 3], v[e >> 5][e & 31]);
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+                // of -inf: any logit above it
+                if (softmax_vote(top > m + kSlack || !ok)) {
+                    s.half[threadIdx.x] = top;
+                    ok = !softmax_vote(!ok);                       // all go on, or none
+                    if (!ok) break;
+                    top = fmaxf(top, s.half[threadIdx.x ^ 128]);
+                    const float mn = top > m + kSlack ? top : m;
+                    const float f = mn == m ? 1.f : ex2(m - mn);
+                    if (__any_sync(0xffffffffu, mn != m) && i > 0) {
+                        ok = warp_wait(&s.o_done, (g - 1) & 1, abort);
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c = half * (VD / 2); c < (half + 1) * (VD / 2) && ok; c += 32) {
-                        float o[32];
-                        tmem_ld_32cols(lane_addr + kOCol + c, o);
+                        for (int c = half * (VD / 2); c < (half + 1) * (VD / 2) && ok; c += 32) {
+                            float o[32];
+                            tmem_ld_32cols(lane_addr + kOCol + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st_32cols(lane_addr + kOCol + c, o);
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tmem_st_32cols(lane_addr + kOCol + c, o);
+                        }
+                    }
+                    l *= f;
+                    m = mn;
+                    softmax_vote(false);                           // maxima read: free to be written
+                }
+                const float base = m == -INFINITY ? 0.f : -m;      // no logit above -inf yet
+                const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    float2 p = fma_x2(make_float2(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, base2);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    sum[(e >> 1) & 1] = add_x2(sum[(e >> 1) & 1], p);
+                    x[e >> 1] = __uint_as_float(pack(p.x, p.y));
+                }
+                tmem_st_32cols(at + half * 32, x);
+                const float2 both = add_x2(sum[0], sum[1]);
+                l += both.x + both.y;
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&s.p_full[g & 1], 0));
+            }
+            s.half[threadIdx.x] = l;
+            if (n > 0) {
+                ok = ok && warp_wait(&s.o_last, busy & 1, abort);
+                ++busy;
+            }
+            if (softmax_vote(!ok)) { ok = false; break; }
+            tc_fence_after();
+            l += s.half[threadIdx.x ^ 128];
+            const int64_t qh = (w.q0 + row) * a.heads + w.h;
+            const bool mine = row < w.n_q;
+            const bool poison = n > 0 && *(volatile int32_t*)&s.poison[busy & 1] == busy;
+            if (mine && half == 0) {
+                if (a.n_split > 1)
+                    *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + w.split) * 2) = make_float2(m, l);
+                else if (a.lse != nullptr)
+                    a.lse[qh] = expanded_lse(m, l);
+            }
+            if (n == 0) continue;
+            // 32 columns of O, with what the cleaners took out of values that the row sees
+            auto columns = [&](int c, float (&o)[32]) {
+                tmem_ld_32cols(lane_addr + kOCol + c, o);
+                if (!poison || !mine) return;
+                const int64_t from = (int64_t)(w.partial > w.kt0 ? w.partial : w.kt0) * kK;
+                const int64_t end = (int64_t)(w.kt0 + n) * kK, to = sees < end ? sees : end;
+                for (int64_t j = from; j < to; ++j) {
+                    const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(a.v) +
+                                             ((w.row0 + j) * a.heads + w.h) * VD + c;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float z = __bfloat162float(y[e]);
+                        if (!isfinite(z)) o[e] += z;
                     }
                 }
-                l *= f;
-                m = mn;
-                softmax_vote(false);                               // maxima read: free to be written
-            }
-            const float base = m == -INFINITY ? 0.f : -m;          // no logit above -inf yet
-            const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            float w[32];
+            };
+            // 128 bytes of each of the warp's rows, from a row to a thread to whole lines
+            const int c0 = half * (VD / 2);
+            auto put = [&](const uint4 (&x)[8], uint8_t* base, int64_t row_bytes) {
+                __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                float2 p = fma_x2(make_float2(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, base2);
-                p.x = ex2(p.x);
-                p.y = ex2(p.y);
-                sum[(e >> 1) & 1] = add_x2(sum[(e >> 1) & 1], p);
-                w[e >> 1] = __uint_as_float(pack(p.x, p.y));
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = x[e];
+                __syncwarp();
+                const int r0 = (int)rank * kRows + (warp & 3) * 32;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = e * 4 + (lane >> 3);
+                    const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                    if (r0 + r < w.n_q)
+                        *reinterpret_cast<uint4*>(base + (w.q0 + r0 + r) * row_bytes + (lane & 7) * 16) = y;
+                }
+            };
+            if (a.n_split > 1) {
+                const int64_t row_bytes = (int64_t)a.heads * a.n_split * VD * 4;
+                uint8_t* base = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)w.h * a.n_split + w.split) * VD + c0);
+#pragma unroll 1
+                for (int c = 0; c < VD / 2; c += 32) {
+                    float o[32];
+                    columns(c0 + c, o);
+                    uint4 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                          __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+                    put(x, base + c * 4, row_bytes);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
+            } else {
+                const float inv = 1.f / l;
+                uint4 x[VD / 128][8];
+#pragma unroll
+                for (int c = 0; c < VD / 2; c += 32) {
+                    float o[32];
+                    columns(c0 + c, o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[c / 64][c % 64 / 8 + e] =
+                            make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv), pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                       pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
+                uint8_t* base = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)w.h * VD + c0);
+#pragma unroll
+                for (int c = 0; c < VD / 128; ++c) put(x[c], base + c * 128, (int64_t)a.heads * VD * 2);
             }
-            tmem_st_32cols(at + half * 32, w);
-            const float2 both = add_x2(sum[0], sum[1]);
-            l += both.x + both.y;
-            tc_fence_before();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&s.p_full[i & 1], 0));
         }
-        s.half[threadIdx.x] = l;
-        ok = ok && (n == 0 || warp_wait(&s.o_last, 0, abort));
-        ok = !softmax_vote(!ok);
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 65);
             *abort = 1;
-        } else {
-            tc_fence_after();
-            l += s.half[threadIdx.x ^ 128];
-            const int64_t qh = (t.q0 + row) * a.heads + h;
-            const bool mine = row < t.n_q;
-            const bool poison = n > 0 && *(volatile int32_t*)&s.poison != 0;
-            const float inv = 1.f / l;
-            if (a.n_split > 1 && mine && half == 0)
-                *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + split) * 2) = make_float2(m, l);
-            if (a.n_split == 1 && mine && half == 0 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
-            const int64_t from = (int64_t)(partial > t.kt0 ? partial : t.kt0) * kK;
-            const int64_t to = sees < (int64_t)t.kt1 * kK ? sees : (int64_t)t.kt1 * kK;
-#pragma unroll 1
-            for (int c = half * (VD / 2); c < (half + 1) * (VD / 2) && n > 0; c += 32) {
-                float o[32];
-                tmem_ld_32cols(lane_addr + kOCol + c, o);
-                if (poison && mine) {
-                    for (int64_t j = from; j < to; ++j) {
-                        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.v) +
-                                                 ((t.row0 + j) * a.heads + h) * VD + c;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float y = __bfloat162float(x[e]);
-                            if (!isfinite(y)) o[e] += y;
-                        }
-                    }
-                }
-                if (!mine) continue;
-                if (a.n_split > 1) {
-                    float4* p = reinterpret_cast<float4*>(a.part_o + (qh * a.n_split + split) * VD + c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
-                    uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * VD + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[e] = make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                          pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                          pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                          pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                }
-            }
         }
     }
-    __syncwarp();
     // neither CTA leaves while the other's products or signals still reach it
+    __syncwarp();
     tc_fence_before();
     cluster_sync();
     if (warp == kMmaWarp) {
@@ -500,7 +678,7 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int nk = (int)(d / 64);
-    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock) / unit_size(nk, VD));
+    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock - kSoftmax / 32 * kStage) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
     return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr,
