@@ -14,17 +14,18 @@
 //              rope block from the cache rows, for every head) or a tile's values in
 //              the order of their use; hands out the units of work;
 //   warp 9     in the first CTA issues the products for both, S of tile t + 1 before O
-//              of tile t;
+//              of tile t, from one unit of work into the next;
 //   warps 0-7  softmax, a query row and half of its keys to a thread: S from TMEM,
 //              exp, P in bf16 back over S (O takes it from TMEM as its A operand).
 //              Row maxima are raised only when a logit exceeds them by more than
 //              kSlack, so the two halves of a row share a maximum without telling each
 //              other theirs: a barrier that also votes says whether any row is raised,
-//              and only then they are exchanged and O is rescaled in TMEM.  At the end
-//              O to the output or the split's part, through shared memory;
+//              and only then they are exchanged and O is rescaled in TMEM;
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
-//              epilogue to the queries that see them.
+//              epilogue to the queries that see them;
+//   warps 12-15 epilogue: a unit's O to the output or the split's part, through shared
+//              memory, beside the next unit's first scores.
 // A key tile takes 2,050 cycles (head width and v_dim 256), which are the products' own: S
 // and O of 1,024 each.  What it took before: a unit's launch to itself, with its start, its
 // output and nothing beside them, 11,000 cycles; copies and products handed over in eight
@@ -48,14 +49,15 @@ constexpr uint32_t kQBlock = kRows * 128;                // 64 columns of them
 constexpr uint32_t kKBlock = kK / 2 * 128;               // 64 columns of a CTA's half of a tile's keys
 constexpr int kMaxRing = 11;
 constexpr int kWorks = 4;                                // units of work handed out at a time
-constexpr uint32_t kStage = kRows / 4 * 128;             // a softmax warp's piece of the output: 32 rows of 128 bytes
+constexpr uint32_t kStage = 32 * 128;                    // 128 bytes of an epilogue warp's rows
 constexpr int kSoftmax = 256;                            // threads
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
-constexpr int kThreads = 384;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kOutWarp = 12;
+constexpr int kThreads = 512;                            // 128 registers each at the launch, then
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;      // 256 threads of either kind
 constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
-constexpr uint32_t kBarBytes = 2048;
+constexpr uint32_t kBarBytes = 6144;
 constexpr long long kWaitCycles = 4000000000ll;          // about 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                            // weights stay below 2^8
@@ -82,10 +84,12 @@ struct Work {
 struct Shared {
     uint64_t full[kMaxRing], empty[kMaxRing], part[kMaxRing], clean[kMaxRing];
     uint64_t q_full, q_free, s_full[2], p_full[2], o_done, o_free, o_last, drain;
+    uint64_t l_full[2];
     uint64_t work_full[kWorks], work_free[kWorks], next_full[2], next_free[2];
     alignas(16) uint4 next[2];                           // answers to the requests for work
     Work work[kWorks];
-    float half[kSoftmax];                                // maxima, then sums, of a row's halves
+    float top[2][kSoftmax];                              // maxima of a row's halves, of every other tile
+    float l[2][kSoftmax], m[2][kRows];                   // a unit's sums of halves, and its maxima
     uint32_t tmem;
     int32_t abort, poison[2];                            // poison: the last unit that met odd values
 };
@@ -210,11 +214,12 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&s.work_full[i], 1);
-            // the softmax's and the cleaners' warps, and the products' thread
-            mbar_init(&s.work_free[i], (kSoftmax + kCleaners) / 32 + (rank == 0 ? 1 : 0));
+            // the softmax's, the cleaners' and the epilogue's warps, and the products' thread
+            mbar_init(&s.work_free[i], (kSoftmax + kCleaners + kRows) / 32 + (rank == 0 ? 1 : 0));
         }
         mbar_init(&s.o_done, 1);
-        mbar_init(&s.o_free, 2 * kSoftmax / 32);
+        mbar_init(&s.o_free, 2 * kRows / 32);
+        for (int i = 0; i < 2; ++i) mbar_init(&s.l_full[i], kSoftmax / 32);
         mbar_init(&s.o_last, 1);
         mbar_init(&s.drain, 1);
         s.abort = 0;
@@ -237,6 +242,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     volatile int32_t* abort = &s.abort;
     pdl_wait();
     pdl_trigger();
+    if (warp < kTmaWarp) regs_inc<kSoftmaxRegs>();
+    else regs_dec<kOtherRegs>();
 
     if (warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
@@ -346,27 +353,26 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (rank == 0 && elect_one()) {                            // ---- products
             bool ok = true;
             Place p;
-            uint32_t g = 0, busy = 0;                              // key tiles and units of work so far
+            uint32_t g = 0, busy = 0, k = 0;                       // key tiles, units with some, units so far
             uint32_t cleaned = 0;                                  // parities of the clean barriers
             const uint32_t q_addr = smem_u32(Qs), r_addr = smem_u32(Rs);
             const uint32_t id_s = idesc_bf16_f32(kQ, kK), id_o = idesc_bf16_f32_major(kQ, VD, 0, 1);
-            auto scores = [&](uint32_t tile) {
-                ok = ok && wait(&s.full[p.at], p.parity, abort);
+            auto scores = [&](uint32_t tile, const Place& at) {
+                ok = ok && wait(&s.full[at.at], at.parity, abort);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t k_addr = r_addr + p.at * unit_bytes, d = tmem + (tile & 1) * kK;
+                const uint32_t k_addr = r_addr + at.at * unit_bytes, d = tmem + (tile & 1) * kK;
                 for (int b = 0; b < nk; ++b) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_bf16_ss_pair(d, sdesc_kmajor_sw128(q_addr + b * kQBlock + kk * 32),
                                          sdesc_kmajor_sw128(k_addr + b * kKBlock + kk * 32), id_s, (b | kk) != 0);
                 }
-                mma_commit_pair(&s.empty[p.at]);
+                mma_commit_pair(&s.empty[at.at]);
                 mma_commit_pair(&s.s_full[tile & 1]);
-                p.step(ring);
             };
             auto values = [&](uint32_t tile, bool more, bool partly) {
-                ok = wait(&s.full[p.at], p.parity, abort);
+                ok = ok && wait(&s.full[p.at], p.parity, abort);
                 if (ok && partly) {
                     ok = wait(&s.clean[p.at], (cleaned >> p.at) & 1, abort);
                     cleaned ^= 1u << p.at;
@@ -381,28 +387,67 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                      more || kk != 0);
                 mma_commit_pair(&s.empty[p.at]);
                 mma_commit_pair(&s.o_done);
-                p.step(ring);
             };
-            for (uint32_t k = 0; ok; ++k) {
-                ok = wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
-                if (!ok) break;
-                const int n = s.work[k % kWorks].n;
-                const int partial = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
-                mbar_arrive(&s.work_free[k % kWorks]);
-                if (n < 0) break;
-                if (n == 0) continue;
-                ok = wait(&s.q_full, busy & 1, abort);
-                scores(g);
+            // the next unit with key tiles: known (1), not yet handed out (0), none (-1)
+            int known = 0, n_next = 0, partial_next = 0;
+            auto fetch = [&](bool blocking) {
+                while (known == 0) {
+                    uint64_t* bar = &s.work_full[k % kWorks];
+                    const uint32_t parity = (k / kWorks) & 1;
+                    if (!blocking && !mbar_test_wait(bar, parity)) return;
+                    ok = ok && wait(bar, parity, abort);
+                    if (!ok) return;
+                    n_next = s.work[k % kWorks].n;
+                    partial_next = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
+                    mbar_arrive(&s.work_free[k % kWorks]);
+                    ++k;
+                    known = n_next < 0 ? -1 : n_next > 0 ? 1 : 0;
+                }
+            };
+            bool early = false;                                    // the unit's first scores are issued
+            fetch(true);
+            while (ok && known == 1) {
+                const int n = n_next, partial = partial_next;
+                known = 0;
+                if (!early) {
+                    ok = wait(&s.q_full, busy & 1, abort);
+                    scores(g, p);
+                    p.step(ring);
+                }
+                early = false;
                 for (int i = 0; i < n && ok; ++i) {
-                    if (i + 1 < n) scores(g + i + 1);
+                    if (i + 1 < n) {
+                        scores(g + i + 1, p);
+                        p.step(ring);
+                    }
                     if (i == (n > 1 ? n - 2 : 0)) mma_commit_pair(&s.q_free);   // the last scores are issued
                     // the last unit's O has been read
                     if (i == 0 && busy > 0) ok = ok && wait(&s.o_free, (busy - 1) & 1, abort);
-                    if (ok) values(g + i, i > 0, i >= partial);
+                    if (i == n - 1) {
+                        // the next unit's first scores, if they can begin before these weights
+                        // are there; its keys lie behind this tile's values in the ring
+                        Place after = p;
+                        after.step(ring);
+                        const long long t0 = clock64();
+                        while (ok && !mbar_test_wait(&s.p_full[(g + i) & 1], ((g + i) >> 1) & 1)) {
+                            if (known == 0) fetch(false);
+                            if (known == 1 && mbar_test_wait(&s.q_full, (busy + 1) & 1) &&
+                                mbar_test_wait(&s.full[after.at], after.parity)) {
+                                scores(g + n, after);
+                                early = true;
+                                break;
+                            }
+                            if (*abort != 0 || clock64() - t0 > kWaitCycles) ok = false;
+                        }
+                    }
+                    values(g + i, i > 0, i >= partial);
+                    p.step(ring);
+                    if (early) p.step(ring);
                 }
                 if (ok) mma_commit_pair(&s.o_last);
                 g += n;
                 ++busy;
+                if (ok) fetch(true);
             }
             if (!ok) {
                 record_error(a.err, kDevTimeout, blockIdx.x, 63);
@@ -412,7 +457,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp >= kCleanWarp) {                               // ---- hidden values
+    } else if (warp >= kCleanWarp && warp < kOutWarp) {            // ---- hidden values
         const int c = threadIdx.x - kCleanWarp * 32;
         uint32_t parted = 0;                                       // parities of the part barriers
         uint32_t before = 0;                                       // units of the ring before this work's
@@ -469,25 +514,24 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 64);
             *abort = 1;
         }
-    } else {                                                       // ---- softmax
+    } else if (warp < kTmaWarp) {                                  // ---- softmax
         const int row = (int)rank * kRows + (threadIdx.x & 127);   // of the pair's queries
         const int half = threadIdx.x >> 7;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float scale = a.scale * kLog2e;
-        uint8_t* stage = Rs + ring * unit_bytes + warp * kStage;
-        uint32_t g = 0;
-        int32_t busy = 0;
+        uint32_t g = 0, busy = 0;
         bool ok = true;
         for (uint32_t k = 0; ; ++k) {
-            ok = warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
-            if (softmax_vote(!ok)) { ok = false; break; }
-            const Work w = s.work[k % kWorks];
+            ok = ok && warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
+            if (softmax_vote(!ok)) { ok = false; break; }          // all go on, or none
+            const Work& w = s.work[k % kWorks];
+            const int n = w.n, partial = w.partial - w.kt0;
+            const int64_t sees = w.first + row - (int64_t)w.kt0 * kK;   // keys of the split, and more
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
-            const int n = w.n;
             if (n < 0) break;
+            if (n == 0) continue;
             float m = -INFINITY, l = 0.f;                          // l: of this half's keys
-            const int64_t sees = w.first + row;
             for (int i = 0; i < n; ++i, ++g) {
                 // a warp that gives up votes and meets the others all the same
                 ok = ok && warp_wait(&s.s_full[g & 1], (g >> 1) & 1, abort);
@@ -495,13 +539,15 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const uint32_t at = lane_addr + (g & 1) * kK;
                 float v[2][32];
                 tmem_ld_32cols_x2(at + half * 64, at + half * 64 + 32, v[0], v[1]);
-                if (w.kt0 + i >= w.partial) {
+                if (i >= partial) {
                     // this half's keys of the tile that the row sees
-                    const int64_t here = sees - (int64_t)(w.kt0 + i) * kK - half * 64;
+                    const int64_t here = sees - (int64_t)i * kK - half * 64;
                     const int left = here < 0 ? 0 : here > 64 ? 64 : (int)here;
+                    if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (e >= left) v[e >> 5][e & 31] = -INFINITY;
+                        for (int e = 0; e < 64; ++e)
+                            if (e >= left) v[e >> 5][e & 31] = -INFINITY;
+                    }
                 }
                 float tops[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
 #pragma unroll
@@ -509,10 +555,10 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
                 // of -inf: any logit above it
                 if (softmax_vote(top > m + kSlack || !ok)) {
-                    s.half[threadIdx.x] = top;
-                    ok = !softmax_vote(!ok);                       // all go on, or none
+                    s.top[g & 1][threadIdx.x] = top;
+                    ok = !softmax_vote(!ok);
                     if (!ok) break;
-                    top = fmaxf(top, s.half[threadIdx.x ^ 128]);
+                    top = fmaxf(top, s.top[g & 1][threadIdx.x ^ 128]);
                     const float mn = top > m + kSlack ? top : m;
                     const float f = mn == m ? 1.f : ex2(m - mn);
                     if (__any_sync(0xffffffffu, mn != m) && i > 0) {
@@ -529,7 +575,6 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     }
                     l *= f;
                     m = mn;
-                    softmax_vote(false);                           // maxima read: free to be written
                 }
                 const float base = m == -INFINITY ? 0.f : -m;      // no logit above -inf yet
                 const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
@@ -550,98 +595,143 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&s.p_full[g & 1], 0));
             }
-            s.half[threadIdx.x] = l;
-            if (n > 0) {
-                ok = ok && warp_wait(&s.o_last, busy & 1, abort);
-                ++busy;
-            }
-            if (softmax_vote(!ok)) { ok = false; break; }
-            tc_fence_after();
-            l += s.half[threadIdx.x ^ 128];
-            const int64_t qh = (w.q0 + row) * a.heads + w.h;
-            const bool mine = row < w.n_q;
-            const bool poison = n > 0 && *(volatile int32_t*)&s.poison[busy & 1] == busy;
-            if (mine && half == 0) {
-                if (a.n_split > 1)
-                    *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + w.split) * 2) = make_float2(m, l);
-                else if (a.lse != nullptr)
-                    a.lse[qh] = expanded_lse(m, l);
-            }
-            if (n == 0) continue;
-            // 32 columns of O, with what the cleaners took out of values that the row sees
-            auto columns = [&](int c, float (&o)[32]) {
-                tmem_ld_32cols(lane_addr + kOCol + c, o);
-                if (!poison || !mine) return;
-                const int64_t from = (int64_t)(w.partial > w.kt0 ? w.partial : w.kt0) * kK;
-                const int64_t end = (int64_t)(w.kt0 + n) * kK, to = sees < end ? sees : end;
-                for (int64_t j = from; j < to; ++j) {
-                    const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(a.v) +
-                                             ((w.row0 + j) * a.heads + w.h) * VD + c;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float z = __bfloat162float(y[e]);
-                        if (!isfinite(z)) o[e] += z;
-                    }
-                }
-            };
-            // 128 bytes of each of the warp's rows, from a row to a thread to whole lines
-            const int c0 = half * (VD / 2);
-            auto put = [&](const uint4 (&x)[8], uint8_t* base, int64_t row_bytes) {
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = x[e];
-                __syncwarp();
-                const int r0 = (int)rank * kRows + (warp & 3) * 32;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = e * 4 + (lane >> 3);
-                    const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                    if (r0 + r < w.n_q)
-                        *reinterpret_cast<uint4*>(base + (w.q0 + r0 + r) * row_bytes + (lane & 7) * 16) = y;
-                }
-            };
-            if (a.n_split > 1) {
-                const int64_t row_bytes = (int64_t)a.heads * a.n_split * VD * 4;
-                uint8_t* base = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)w.h * a.n_split + w.split) * VD + c0);
-#pragma unroll 1
-                for (int c = 0; c < VD / 2; c += 32) {
-                    float o[32];
-                    columns(c0 + c, o);
-                    uint4 x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                                          __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-                    put(x, base + c * 4, row_bytes);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
-            } else {
-                const float inv = 1.f / l;
-                uint4 x[VD / 128][8];
-#pragma unroll
-                for (int c = 0; c < VD / 2; c += 32) {
-                    float o[32];
-                    columns(c0 + c, o);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[c / 64][c % 64 / 8 + e] =
-                            make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv), pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                       pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                       pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
-                uint8_t* base = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)w.h * VD + c0);
-#pragma unroll
-                for (int c = 0; c < VD / 128; ++c) put(x[c], base + c * 128, (int64_t)a.heads * VD * 2);
-            }
+            // for the epilogue, which has read those of the unit before the last: that O is free
+            s.l[busy & 1][threadIdx.x] = l;
+            if (half == 0) s.m[busy & 1][threadIdx.x] = m;
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&s.l_full[busy & 1]);
+            ++busy;
         }
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 65);
+            *abort = 1;
+        }
+    } else {                                                       // ---- epilogue
+        const int r = threadIdx.x & 127, row = (int)rank * kRows + r;
+        const int r0 = (int)rank * kRows + (warp & 3) * 32;        // the warp's first
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint8_t* stage = Rs + ring * unit_bytes + (warp & 3) * kStage;
+        int32_t busy = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            ok = warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
+            if (!ok) break;
+            const Work w = s.work[k % kWorks];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
+            if (w.n < 0) break;
+            const int64_t qh = (w.q0 + row) * a.heads + w.h;
+            const bool mine = row < w.n_q;
+            float2* ml = reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + w.split) * 2);
+            if (w.n == 0) {                                        // a split without keys
+                if (mine && a.n_split > 1) *ml = make_float2(-INFINITY, 0.f);
+                continue;
+            }
+            // the softmax may be two units ahead of this, hence its two barriers
+            ok = warp_wait(&s.l_full[busy & 1], (busy >> 1) & 1, abort) && warp_wait(&s.o_last, busy & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const float l = s.l[busy & 1][r] + s.l[busy & 1][r + 128], m = s.m[busy & 1][r];
+            ++busy;
+            const bool poison = *(volatile int32_t*)&s.poison[busy & 1] == busy;
+            if (mine && a.n_split > 1) *ml = make_float2(m, l);
+            if (mine && a.n_split == 1 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
+            if (poison) {                                          // what the cleaners took out and the row sees
+                const int64_t from = (int64_t)(w.partial > w.kt0 ? w.partial : w.kt0) * kK;
+                const int64_t sees = w.first + row, end = (int64_t)(w.kt0 + w.n) * kK;
+                const int64_t to = !mine ? from : sees < end ? sees : end;
+#pragma unroll 1
+                for (int c = 0; c < VD; c += 32) {
+                    float o[32];
+                    tmem_ld_32cols(lane_addr + kOCol + c, o);
+#pragma unroll 1
+                    for (int64_t j = from; j < to; ++j) {
+                        const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(a.v) +
+                                                 ((w.row0 + j) * a.heads + w.h) * VD + c;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float z = __bfloat162float(y[e]);
+                            if (!isfinite(z)) o[e] += z;
+                        }
+                    }
+                    __syncwarp();
+                    tmem_st_32cols(lane_addr + kOCol + c, o);
+                }
+            }
+            // 128 bytes of each of the warp's rows: a row of a thread's, then whole lines
+            auto put = [&](const uint4 (&x)[8]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = x[e];
+            };
+            auto write = [&](uint8_t* base, int64_t row_bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = e * 4 + (lane >> 3);
+                    const uint4 y = *reinterpret_cast<const uint4*>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+                    if (r0 + i < w.n_q)
+                        *reinterpret_cast<uint4*>(base + (w.q0 + r0 + i) * row_bytes + (lane & 7) * 16) = y;
+                }
+                __syncwarp();
+            };
+            auto read_all = [&] {                                  // O may be written again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
+            };
+            if (a.n_split > 1) {
+                const int64_t row_bytes = (int64_t)a.heads * a.n_split * VD * 4;
+                uint8_t* base = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)w.h * a.n_split + w.split) * VD);
+#pragma unroll 1
+                for (int c = 0; c < VD; c += 32) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        float o[16];
+                        tmem_ld_16cols(lane_addr + kOCol + c + d * 16, o);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[d * 4 + e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                                      __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+                    }
+                    if (c + 32 == VD) read_all();
+                    put(x);
+                    write(base + c * 4, row_bytes);
+                }
+            } else {
+                const float inv = 1.f / l;
+                const int64_t row_bytes = (int64_t)a.heads * VD * 2;
+                uint8_t* base = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)w.h * VD);
+                auto load = [&](int c, uint4 (&x)[8]) {            // 64 columns as bf16
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        float o[16];
+                        tmem_ld_16cols(lane_addr + kOCol + c + d * 16, o);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            x[d * 2 + e] = make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                      pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                      pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                      pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    }
+                };
+                // a piece in shared memory while the next is read
+                uint4 x[8];
+                load(0, x);
+                put(x);
+#pragma unroll 1
+                for (int c = 64; c < VD; c += 64) {
+                    load(c, x);
+                    if (c + 64 == VD) read_all();
+                    write(base + c * 2 - 128, row_bytes);
+                    put(x);
+                }
+                write(base + VD * 2 - 128, row_bytes);
+            }
+        }
+        if (!ok) {
+            if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 66);
             *abort = 1;
         }
     }
@@ -678,7 +768,7 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int nk = (int)(d / 64);
-    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock - kSoftmax / 32 * kStage) / unit_size(nk, VD));
+    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock - kRows / 32 * kStage) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
     return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr,
