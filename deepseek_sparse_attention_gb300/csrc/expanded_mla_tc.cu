@@ -53,7 +53,8 @@ constexpr uint32_t kStage = 32 * 128;                    // 128 bytes of an epil
 constexpr int kSoftmax = 256;                            // threads
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kOutWarp = 12;
 constexpr int kThreads = 512;                            // 128 registers each at the launch, then
-constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;      // 256 threads of either kind
+// of the softmax (256 threads), the epilogue and the others (128 each): 512 x 128 in all
+constexpr int kSoftmaxRegs = 136, kOutRegs = 128, kOtherRegs = 112;
 constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
@@ -243,7 +244,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     pdl_wait();
     pdl_trigger();
     if (warp < kTmaWarp) regs_inc<kSoftmaxRegs>();
-    else regs_dec<kOtherRegs>();
+    else if (warp < kOutWarp) regs_dec<kOtherRegs>();
+    static_assert(kOutRegs == 128, "as launched");
 
     if (warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
@@ -705,29 +707,39 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 uint8_t* base = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)w.h * VD);
                 auto load = [&](int c, uint4 (&x)[8]) {            // 64 columns as bf16
 #pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        float o[16];
-                        tmem_ld_16cols(lane_addr + kOCol + c + d * 16, o);
+                    for (int d = 0; d < 2; ++d) {
+                        float o[32];
+                        tmem_ld_32cols(lane_addr + kOCol + c + d * 32, o);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            x[d * 2 + e] = make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
+                        for (int e = 0; e < 4; ++e)
+                            x[d * 4 + e] = make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
                                                       pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                                                       pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                                                       pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
                     }
                 };
-                // a piece in shared memory while the next is read
-                uint4 x[8];
+                // O out of TMEM as soon as shared memory and registers take it
+                uint4 x[8], y[8];
                 load(0, x);
                 put(x);
-#pragma unroll 1
-                for (int c = 64; c < VD; c += 64) {
-                    load(c, x);
-                    if (c + 64 == VD) read_all();
-                    write(base + c * 2 - 128, row_bytes);
+                load(64, x);
+                if constexpr (VD == 256) {
+                    load(128, y);
+                    write(base, row_bytes);
                     put(x);
+                    load(192, x);
+                    read_all();
+                    write(base + 128, row_bytes);
+                    put(y);
+                    write(base + 256, row_bytes);
+                    put(x);
+                    write(base + 384, row_bytes);
+                } else {
+                    read_all();
+                    write(base, row_bytes);
+                    put(x);
+                    write(base + 128, row_bytes);
                 }
-                write(base + VD * 2 - 128, row_bytes);
             }
         }
         if (!ok) {
