@@ -684,7 +684,7 @@ dsa_status dsa_expand_kv(const dsa_shape* shape, int64_t n_rows, int32_t nope_di
     if (n_rows > (1 << 24)) return DSA_ERR_UNSUPPORTED;
     if (n_rows > 0 && (cache == nullptr || w_uk == nullptr || w_uv == nullptr || k_nope == nullptr || v == nullptr))
         return DSA_ERR_INVALID_ARG;
-    if (!aligned16(cache) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(k_nope) || !aligned16(v))
+    if (!aligned16(cache) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned(k_nope, 32) || !aligned(v, 32))
         return DSA_ERR_INVALID_ARG;
     if ((s = check_ws(ws, ws_bytes, kWsHeaderBytes)) != DSA_OK) return s;
     return cuda_status(launch_expand_kv(sh, n_rows, nope_dim, v_dim, cache, w_uk, w_uv, k_nope, v,
@@ -706,7 +706,7 @@ dsa_status dsa_expanded_mla_attn(const dsa_shape* shape, const dsa_batch* batch,
     if (b.n_q > 0 && (q == nullptr || k_nope == nullptr || v == nullptr || out == nullptr ||
                       (sh.rope > 0 && cache == nullptr)))
         return DSA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_nope) || !aligned16(cache) || !aligned16(v) || !aligned16(out) ||
+    if (!aligned16(q) || !aligned16(k_nope) || !aligned16(cache) || !aligned16(v) || !aligned(out, 32) ||
         !aligned(lse, 4))
         return DSA_ERR_INVALID_ARG;
     if ((s = check_ws(ws, ws_bytes, op_bytes(sh, b, DSA_OP_EXPANDED_MLA))) != DSA_OK) return s;

@@ -268,10 +268,14 @@ cudaError_t launch_rope(const dsa_rope_plan& r, int32_t dtype, int64_t n_tok, in
                         const void* x, int64_t x_tok, int64_t x_head, const int64_t* pos, void* out,
                         int64_t out_tok, int64_t out_head, cudaStream_t st);
 
-// Latent rows into every head's keys and values (expand_kv.cu).
+// Latent rows into every head's keys and values (expand_kv.cu: float32).
 cudaError_t launch_expand_kv(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim,
                              const void* rows, const void* w_uk, const void* w_uv, void* k_nope,
                              void* v, int32_t* err, cudaStream_t st);
+
+cudaError_t launch_expand_tc(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim,
+                             const void* rows, const void* w_uk, const void* w_uv, void* k_nope,
+                             void* v, int32_t* err, cudaStream_t st);     // bf16 (expand_kv_tc.cu)
 
 // Causal attention over expanded keys and values (expanded_mla.cu).
 int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b);

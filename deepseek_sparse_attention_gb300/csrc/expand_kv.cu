@@ -8,7 +8,7 @@
 // output.  Two matrix products of the rows [n_rows, kv_lora] with the weights
 // [heads * d, kv_lora], both with the sum along contiguous memory, in one launch.
 //
-// On CUDA cores: tiles of 128 rows by 128 outputs, 8 x 8 of them to a thread,
+// bf16 runs on the tensor cores (expand_kv_tc.cu).  Float32, on CUDA cores: tiles of 128 rows by 128 outputs, 8 x 8 of them to a thread,
 // 16 terms of the sum at a time through shared memory while the next are
 // loaded into registers.
 #include "dsa_kernels.cuh"
@@ -22,24 +22,12 @@ using namespace sm100;
 constexpr int kTile = 128, kDepth = 16, kLd = kTile + 4;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
-                       __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                              *reinterpret_cast<const uint32_t*>(&hi));
-}
-
-template <typename T>
 __global__ void __launch_bounds__(256)
-expand_simt(const T* __restrict__ rows, const T* __restrict__ w_uk, const T* __restrict__ w_uv,
-            T* __restrict__ k_nope, T* __restrict__ v, int64_t n_rows, int32_t width, int32_t kv_lora,
+expand_simt(const float* __restrict__ rows, const float* __restrict__ w_uk, const float* __restrict__ w_uv,
+            float* __restrict__ k_nope, float* __restrict__ v, int64_t n_rows, int32_t width, int32_t kv_lora,
             int32_t n_k, int32_t n_v) {
     __shared__ float As[kDepth][kLd], Bs[kDepth][kLd];
     const int tiles = (n_k + n_v) / kTile;
@@ -47,8 +35,8 @@ expand_simt(const T* __restrict__ rows, const T* __restrict__ w_uk, const T* __r
     int n0 = (int)(blockIdx.x % tiles) * kTile;
     const bool is_v = n0 >= n_k;                         // both widths are multiples of a tile
     if (is_v) n0 -= n_k;
-    const T* w = is_v ? w_uv : w_uk;
-    T* out = is_v ? v : k_nope;
+    const float* w = is_v ? w_uv : w_uk;
+    float* out = is_v ? v : k_nope;
     const int ld = is_v ? n_v : n_k;
     const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
     // this thread's two pieces of four terms of each operand's tile
@@ -89,20 +77,19 @@ expand_simt(const T* __restrict__ rows, const T* __restrict__ w_uk, const T* __r
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + (i >> 2) * 64 + ty * 4 + (i & 3);
         if (r >= n_rows) continue;
-        T* o = out + r * ld + n0 + tx * 4;
+        float* o = out + r * ld + n0 + tx * 4;
         store4(o, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         store4(o + 64, acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
     }
 }
 
-template <typename T>
 cudaError_t launch_simt(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim, const void* rows,
                         const void* w_uk, const void* w_uv, void* k_nope, void* v, cudaStream_t st) {
     const int32_t n_k = sh.heads * nope, n_v = sh.heads * v_dim;
     const int64_t grid = (n_rows + kTile - 1) / kTile * ((n_k + n_v) / kTile);
-    return launch_plain(expand_simt<T>, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const T*>(rows),
-                        static_cast<const T*>(w_uk), static_cast<const T*>(w_uv), static_cast<T*>(k_nope),
-                        static_cast<T*>(v), n_rows, sh.width(), sh.kv_lora, n_k, n_v);
+    return launch_plain(expand_simt, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const float*>(rows),
+                        static_cast<const float*>(w_uk), static_cast<const float*>(w_uv),
+                        static_cast<float*>(k_nope), static_cast<float*>(v), n_rows, sh.width(), sh.kv_lora, n_k, n_v);
 }
 
 }  // namespace
@@ -110,11 +97,10 @@ cudaError_t launch_simt(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v
 cudaError_t launch_expand_kv(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim,
                              const void* rows, const void* w_uk, const void* w_uv, void* k_nope,
                              void* v, int32_t* err, cudaStream_t st) {
-    (void)err;
     if (n_rows == 0) return cudaSuccess;
     return sh.dtype == DSA_BF16
-               ? launch_simt<__nv_bfloat16>(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, st)
-               : launch_simt<float>(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, st);
+               ? launch_expand_tc(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, err, st)
+               : launch_simt(sh, n_rows, nope, v_dim, rows, w_uk, w_uv, k_nope, v, st);
 }
 
 }  // namespace dsa

@@ -24,8 +24,10 @@
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
 //              epilogue to the queries that see them;
-//   warps 12-15 epilogue: a unit's O to the output or the split's part, through shared
-//              memory, beside the next unit's first scores.
+//   warps 12-15 epilogue: a unit's O to the output or the split's part, a row to a
+//              thread in whole sectors, beside the next unit's first scores.  (Through shared
+//              memory to whole lines it took 10 to 20% longer over short units: the
+//              products leave its bandwidth to no one.)
 // A key tile takes 2,050 cycles (head width and v_dim 256), which are the products' own: S
 // and O of 1,024 each.  What it took before: a unit's launch to itself, with its start, its
 // output and nothing beside them, 11,000 cycles; copies and products handed over in eight
@@ -36,7 +38,7 @@
 #include <math.h>
 
 #include "expanded_mla.cuh"
-#include "sm100.cuh"
+#include "pair.cuh"
 
 namespace dsa {
 namespace {
@@ -49,17 +51,15 @@ constexpr uint32_t kQBlock = kRows * 128;                // 64 columns of them
 constexpr uint32_t kKBlock = kK / 2 * 128;               // 64 columns of a CTA's half of a tile's keys
 constexpr int kMaxRing = 11;
 constexpr int kWorks = 4;                                // units of work handed out at a time
-constexpr uint32_t kStage = 32 * 128;                    // 128 bytes of an epilogue warp's rows
 constexpr int kSoftmax = 256;                            // threads
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kOutWarp = 12;
 constexpr int kThreads = 512;                            // 128 registers each at the launch, then
-// of the softmax (256 threads), the epilogue and the others (128 each): 512 x 128 in all
-constexpr int kSoftmaxRegs = 136, kOutRegs = 128, kOtherRegs = 112;
+// of the softmax's 256 threads and of the others
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
 constexpr uint32_t kBarBytes = 6144;
-constexpr long long kWaitCycles = 4000000000ll;          // about 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                            // weights stay below 2^8
 
@@ -67,11 +67,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // A unit of work as the roles read it.
@@ -151,29 +146,6 @@ __device__ __forceinline__ bool softmax_vote(bool p) {
     return r != 0;
 }
 
-// A place in the ring and the parity of its use, one block after the other.
-struct Place {
-    int at = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void step(int ring) {
-        if (++at == ring) { at = 0; parity ^= 1; }
-    }
-};
-
-// A wait that ends early when another role gave up.  The clock is the SM's: reading
-// the global timer between two tries cost up to 2,000 cycles after the arrival.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity))
-        if (*abort != 0 || clock64() - t0 > kWaitCycles) return false;
-    return true;
-}
-// The same made by a whole warp: all lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
-    return __all_sync(0xffffffffu, wait(bar, parity, abort));
-}
-
 // Room for either kind of unit.
 __host__ __device__ constexpr uint32_t unit_size(int nk, int v_dim) {
     const uint32_t k = nk * kKBlock, v = v_dim / 128 * (kK * 128);
@@ -244,8 +216,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     pdl_wait();
     pdl_trigger();
     if (warp < kTmaWarp) regs_inc<kSoftmaxRegs>();
-    else if (warp < kOutWarp) regs_dec<kOtherRegs>();
-    static_assert(kOutRegs == 128, "as launched");
+    else regs_dec<kOtherRegs>();
 
     if (warp == kTmaWarp) {
         if (lane == 0) {                                           // ---- TMA
@@ -610,9 +581,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
     } else {                                                       // ---- epilogue
         const int r = threadIdx.x & 127, row = (int)rank * kRows + r;
-        const int r0 = (int)rank * kRows + (warp & 3) * 32;        // the warp's first
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        uint8_t* stage = Rs + ring * unit_bytes + (warp & 3) * kStage;
         int32_t busy = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
@@ -636,8 +605,6 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float l = s.l[busy & 1][r] + s.l[busy & 1][r + 128], m = s.m[busy & 1][r];
             ++busy;
             const bool poison = *(volatile int32_t*)&s.poison[busy & 1] == busy;
-            if (mine && a.n_split > 1) *ml = make_float2(m, l);
-            if (mine && a.n_split == 1 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
             if (poison) {                                          // what the cleaners took out and the row sees
                 const int64_t from = (int64_t)(w.partial > w.kt0 ? w.partial : w.kt0) * kK;
                 const int64_t sees = w.first + row, end = (int64_t)(w.kt0 + w.n) * kK;
@@ -660,87 +627,43 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tmem_st_32cols(lane_addr + kOCol + c, o);
                 }
             }
-            // 128 bytes of each of the warp's rows: a row of a thread's, then whole lines
-            auto put = [&](const uint4 (&x)[8]) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = x[e];
-            };
-            auto write = [&](uint8_t* base, int64_t row_bytes) {
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = e * 4 + (lane >> 3);
-                    const uint4 y = *reinterpret_cast<const uint4*>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
-                    if (r0 + i < w.n_q)
-                        *reinterpret_cast<uint4*>(base + (w.q0 + r0 + i) * row_bytes + (lane & 7) * 16) = y;
-                }
-                __syncwarp();
-            };
-            auto read_all = [&] {                                  // O may be written again
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
-            };
             if (a.n_split > 1) {
-                const int64_t row_bytes = (int64_t)a.heads * a.n_split * VD * 4;
-                uint8_t* base = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)w.h * a.n_split + w.split) * VD);
-#pragma unroll 1
+                float* out = a.part_o + (qh * a.n_split + w.split) * VD;
+#pragma unroll 2
                 for (int c = 0; c < VD; c += 32) {
-                    uint4 x[8];
+                    float o[32];
+                    tmem_ld_32cols(lane_addr + kOCol + c, o);
+                    if (!mine) continue;
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        float o[16];
-                        tmem_ld_16cols(lane_addr + kOCol + c + d * 16, o);
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t x[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[d * 4 + e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                                                      __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[e + i]);
+                        store_sector(out + c + e, x);
                     }
-                    if (c + 32 == VD) read_all();
-                    put(x);
-                    write(base + c * 4, row_bytes);
                 }
             } else {
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + qh * VD;
                 const float inv = 1.f / l;
-                const int64_t row_bytes = (int64_t)a.heads * VD * 2;
-                uint8_t* base = reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)w.h * VD);
-                auto load = [&](int c, uint4 (&x)[8]) {            // 64 columns as bf16
+#pragma unroll 2
+                for (int c = 0; c < VD; c += 32) {
+                    float o[32];
+                    tmem_ld_32cols(lane_addr + kOCol + c, o);
+                    if (!mine) continue;
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {
-                        float o[32];
-                        tmem_ld_32cols(lane_addr + kOCol + c + d * 32, o);
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t x[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[d * 4 + e] = make_uint4(pack(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                                      pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                                      pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                                      pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                        for (int i = 0; i < 8; ++i) x[i] = pack(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
+                        store_sector(out + c + e, x);
                     }
-                };
-                // O out of TMEM as soon as shared memory and registers take it
-                uint4 x[8], y[8];
-                load(0, x);
-                put(x);
-                load(64, x);
-                if constexpr (VD == 256) {
-                    load(128, y);
-                    write(base, row_bytes);
-                    put(x);
-                    load(192, x);
-                    read_all();
-                    write(base + 128, row_bytes);
-                    put(y);
-                    write(base + 256, row_bytes);
-                    put(x);
-                    write(base + 384, row_bytes);
-                } else {
-                    read_all();
-                    write(base, row_bytes);
-                    put(x);
-                    write(base + 128, row_bytes);
                 }
             }
+            tc_fence_before();                                     // O may be written again
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
+            if (mine && a.n_split > 1) *ml = make_float2(m, l);
+            if (mine && a.n_split == 1 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
         }
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 66);
@@ -780,7 +703,7 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int nk = (int)(d / 64);
-    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock - kRows / 32 * kStage) / unit_size(nk, VD));
+    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
     return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr,

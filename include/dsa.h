@@ -445,7 +445,8 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  *   k_nope [n_rows, heads, nope_dim] dtype out: w_uk[h] . latent
  *   v      [n_rows, heads, v_dim] dtype out: w_uv[h] . latent
  * float32 accumulation, rounded once.  nope_dim a multiple of 64 with nope_dim +
- * rope_dim <= 256, v_dim 128 or 256, n_rows <= 2^24.  Pointers 16-byte aligned.
+ * rope_dim <= 256, v_dim 128 or 256, n_rows <= 2^24.  Pointers 16-byte aligned,
+ * k_nope and v 32-byte.
  * Workspace: DSA_OP_PROJECT (the error word).
  *
  * dsa_expanded_mla_attn: causal attention over them, the batch as for the other
@@ -465,7 +466,7 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  * weight exp(z_j - m) to the value product rounded to bf16 (2^-8 of itself at most), the
  * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <
  * 2^31.  A sequence whose offsets break the host bounds is skipped and sets the
- * error word (code 2).  Pointers 16-byte aligned (lse 4).  Workspace:
+ * error word (code 2).  Pointers 16-byte aligned (out 32, lse 4).  Workspace:
  * DSA_OP_EXPANDED_MLA; it serves every batch of no more queries whose max_kv_len
  * is no larger. */
 dsa_status dsa_expand_kv(const dsa_shape *shape, int64_t n_rows, int32_t nope_dim, int32_t v_dim,
