@@ -8,9 +8,9 @@
 // output.  Two matrix products of the rows [n_rows, kv_lora] with the weights
 // [heads * d, kv_lora], both with the sum along contiguous memory, in one launch.
 //
-// bf16 runs on the tensor cores (expand_kv_tc.cu).  Float32, on CUDA cores: tiles of 128 rows by 128 outputs, 8 x 8 of them to a thread,
-// 16 terms of the sum at a time through shared memory while the next are
-// loaded into registers.
+// bf16 runs on the tensor cores (expand_kv_tc.cu).  Float32, on CUDA cores: tiles of 64 rows
+// by 256 outputs, 8 x 8 of them to a thread, 16 terms of the sum at a time through
+// two buffers of shared memory, the next in flight in registers.
 #include "dsa_kernels.cuh"
 #include "sm100.cuh"
 
@@ -19,52 +19,56 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 128, kDepth = 16, kLd = kTile + 4;
+constexpr int kRows = 64, kCols = 256, kDepth = 16;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 expand_simt(const float* __restrict__ rows, const float* __restrict__ w_uk, const float* __restrict__ w_uv,
             float* __restrict__ k_nope, float* __restrict__ v, int64_t n_rows, int32_t width, int32_t kv_lora,
             int32_t n_k, int32_t n_v) {
-    __shared__ float As[kDepth][kLd], Bs[kDepth][kLd];
-    const int tiles = (n_k + n_v) / kTile;
-    const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kTile;
-    int n0 = (int)(blockIdx.x % tiles) * kTile;
-    const bool is_v = n0 >= n_k;                         // both widths are multiples of a tile
+    __shared__ float As[2][kDepth][kRows + 4], Bs[2][kDepth][kCols + 4];
+    const int tiles = (n_k + n_v) / kCols;
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kRows;
+    int n0 = (int)(blockIdx.x % tiles) * kCols;
+    const bool is_v = n0 >= n_k;                         // both widths are multiples of a tile's
     if (is_v) n0 -= n_k;
     const float* w = is_v ? w_uv : w_uk;
     float* out = is_v ? v : k_nope;
     const int ld = is_v ? n_v : n_k;
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
-    // this thread's two pieces of four terms of each operand's tile
-    float4 a[2], b[2];
+    const int t = threadIdx.x, tx = t & 31, ty = t >> 5;
+    // this thread's pieces of four terms: one of the rows, four of the weights
+    const int line = t >> 2, k4 = (t & 3) * 4;
+    const bool has = r0 + line < n_rows;
+    const float* pa = rows + (has ? r0 + line : 0) * width + k4;
+    const float* pb = w + (int64_t)(n0 + line) * kv_lora + k4;
+    float4 a, b[4];
     auto load = [&](int k0) {
+        a = has ? load4(pa + k0) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = t + i * 256, line = at >> 2, k = k0 + (at & 3) * 4;
-            a[i] = r0 + line < n_rows ? load4(rows + (r0 + line) * width + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-            b[i] = load4(w + (int64_t)(n0 + line) * kv_lora + k);
+        for (int i = 0; i < 4; ++i) b[i] = load4(pb + (int64_t)i * 64 * kv_lora + k0);
+    };
+    auto put = [&](int buf) {
+        As[buf][k4][line] = a.x; As[buf][k4 + 1][line] = a.y; As[buf][k4 + 2][line] = a.z; As[buf][k4 + 3][line] = a.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = line + i * 64;
+            Bs[buf][k4][n] = b[i].x; Bs[buf][k4 + 1][n] = b[i].y; Bs[buf][k4 + 2][n] = b[i].z; Bs[buf][k4 + 3][n] = b[i].w;
         }
     };
     float acc[8][8] = {};
     load(0);
-    for (int k0 = 0; k0 < kv_lora; k0 += kDepth) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = t + i * 256, line = at >> 2, k = (at & 3) * 4;
-            As[k][line] = a[i].x; As[k + 1][line] = a[i].y; As[k + 2][line] = a[i].z; As[k + 3][line] = a[i].w;
-            Bs[k][line] = b[i].x; Bs[k + 1][line] = b[i].y; Bs[k + 2][line] = b[i].z; Bs[k + 3][line] = b[i].w;
-        }
-        __syncthreads();
-        if (k0 + kDepth < kv_lora) load(k0 + kDepth);
+    put(0);
+    __syncthreads();
+    for (int k0 = 0, buf = 0; k0 < kv_lora; k0 += kDepth, buf ^= 1) {
+        const bool more = k0 + kDepth < kv_lora;
+        if (more) load(k0 + kDepth);
 #pragma unroll
         for (int k = 0; k < kDepth; ++k) {
-            const float4 a0 = load4(&As[k][ty * 4]), a1 = load4(&As[k][64 + ty * 4]);
-            const float4 b0 = load4(&Bs[k][tx * 4]), b1 = load4(&Bs[k][64 + tx * 4]);
+            const float4 a0 = load4(&As[buf][k][ty * 8]), a1 = load4(&As[buf][k][ty * 8 + 4]);
+            const float4 b0 = load4(&Bs[buf][k][tx * 4]), b1 = load4(&Bs[buf][k][128 + tx * 4]);
             const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
             const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -72,21 +76,23 @@ expand_simt(const float* __restrict__ rows, const float* __restrict__ w_uk, cons
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) fma2(acc[i][j], acc[i][j + 1], av[i], av[i], bv[j], bv[j + 1]);
         }
+        if (more) put(buf ^ 1);                          // read by all before the last barrier
+        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + (i >> 2) * 64 + ty * 4 + (i & 3);
+        const int64_t r = r0 + ty * 8 + i;
         if (r >= n_rows) continue;
         float* o = out + r * ld + n0 + tx * 4;
         store4(o, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        store4(o + 64, acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        store4(o + 128, acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
     }
 }
 
 cudaError_t launch_simt(const Shape& sh, int64_t n_rows, int32_t nope, int32_t v_dim, const void* rows,
                         const void* w_uk, const void* w_uv, void* k_nope, void* v, cudaStream_t st) {
     const int32_t n_k = sh.heads * nope, n_v = sh.heads * v_dim;
-    const int64_t grid = (n_rows + kTile - 1) / kTile * ((n_k + n_v) / kTile);
+    const int64_t grid = (n_rows + kRows - 1) / kRows * ((n_k + n_v) / kCols);
     return launch_plain(expand_simt, dim3((unsigned)grid), dim3(256), 0, st, static_cast<const float*>(rows),
                         static_cast<const float*>(w_uk), static_cast<const float*>(w_uv),
                         static_cast<float*>(k_nope), static_cast<float*>(v), n_rows, sh.width(), sh.kv_lora, n_k, n_v);

@@ -38,21 +38,22 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 }
 
 // Shared memory: the queries, a tile of keys (rows padded by four against bank
-// conflicts), a tile of values, the weights by key.
+// conflicts) and then its values in their place, the weights by key.  106 KB at
+// the widest, so that two CTAs on a multiprocessor hide each other's loads.
 __host__ __device__ constexpr int simt_smem_floats(int rows, int d, int v) {
-    return rows * (d + 4) + kKeys * (d + 4) + kKeys * v + kKeys * (rows + 4);
+    return rows * (d + 4) + kKeys * (d + 4 > v ? d + 4 : v) + kKeys * (rows + 4);
 }
 
 template <typename T, int RPT, int VD>
-__global__ void __launch_bounds__(256) expanded_simt(const ExpandedArgs a) {
+__global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     constexpr int BQ = 16 * RPT;
     constexpr int kVec = VD / 64;                        // groups of four output columns of a thread
     extern __shared__ __align__(16) float smem[];
     const int d = a.nope + a.rope, ld = d + 4;
     float* Qs = smem;
     float* Ks = Qs + BQ * ld;
-    float* Vs = Ks + kKeys * ld;
-    float* Ps = Vs + kKeys * VD;                         // [key][query], rows of BQ + 4
+    float* Vs = Ks;
+    float* Ps = Ks + kKeys * (ld > VD ? ld : VD);        // [key][query], rows of BQ + 4
 
     const int h = (int)(blockIdx.x % a.heads);
     const int split = (int)(blockIdx.x / a.heads % a.n_split);
@@ -91,10 +92,6 @@ __global__ void __launch_bounds__(256) expanded_simt(const ExpandedArgs a) {
                                : load4(rows + row * a.width + a.kv_lora + c - a.nope);
             store4(Ks + j * ld + c, x);
         }
-        for (int i = tid; i < kKeys * VD / 4; i += 256) {
-            const int j = i / (VD / 4), c = i % (VD / 4) * 4;
-            store4(Vs + j * VD + c, j0 + j < last ? load4(v + ((t.row0 + j0 + j) * a.heads + h) * VD + c) : zero);
-        }
         __syncthreads();
         float s[RPT][2] = {};
 #pragma unroll 4
@@ -131,7 +128,12 @@ __global__ void __launch_bounds__(256) expanded_simt(const ExpandedArgs a) {
             Ps[tx * (BQ + 4) + ty * RPT + r] = p0;
             Ps[(tx + 16) * (BQ + 4) + ty * RPT + r] = p1;
         }
-        __syncwarp();                                    // a warp reads the weights that it wrote
+        __syncthreads();                                 // the keys are read
+        for (int i = tid; i < kKeys * VD / 4; i += 256) {
+            const int j = i / (VD / 4), c = i % (VD / 4) * 4;
+            store4(Vs + j * VD + c, j0 + j < last ? load4(v + ((t.row0 + j0 + j) * a.heads + h) * VD + c) : zero);
+        }
+        __syncthreads();
         const bool all = j0 + kKeys <= t.first;          // every query sees every key of the tile
         auto values = [&](int j, bool checked) {
             float p[RPT];
