@@ -22,7 +22,6 @@ using namespace sm100;
 
 constexpr int kPer = 8;                      // columns a lane has of a chunk
 constexpr int kChunk = 32 * kPer;            // columns of a warp's chunk
-constexpr int kChunks = 4;                   // chunks a warp may have
 constexpr float kTop = 448.f;                // the largest e4m3 value
 constexpr float kLeast = 0x1p-126f;          // the least scale: its inverse is finite
 
@@ -98,167 +97,193 @@ __device__ __forceinline__ float scale_of(float amax) {
     return isnan(amax) ? amax : fmaxf(amax / kTop, kLeast);
 }
 
-template <typename T, bool E4M3, bool VEC, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) rms_norm_kernel(const NormArgs a) {
+// CTAs of a multiprocessor that the registers of a row and of the next one allow;
+// 0: the next row is not asked for ahead, and rows have CTAs of their own.
+template <typename T, bool VEC, int TPR, int C>
+constexpr int kCtas = !VEC ? 0 : (C == 4 ? 512 : sizeof(T) == 2 ? 1024 : 768) / (TPR == 32 ? 256 : TPR);
+
+// TPR threads to a row, each with up to C chunks' pieces; rows a stride apart, the
+// next one's loads in flight while a row is reduced and written.
+template <typename T, bool E4M3, bool VEC, int TPR, int C>
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kCtas<T, VEC, TPR, C> > 0 ? kCtas<T, VEC, TPR, C> : 1)
+rms_norm_kernel(const NormArgs a) {
     constexpr int kRows = TPR == 32 ? 8 : 1;             // rows of a CTA
     constexpr int kWarps = TPR / 32;                     // warps of a row
-    __shared__ float buf[3][kWarps];
+    __shared__ float bufs[2][3][kWarps];
     const int lane = threadIdx.x & 31;
     const int warp = TPR == 32 ? 0 : threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
+    const int64_t stride = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
     if (row >= a.n_rows) return;
     pdl_wait();
     pdl_trigger();
 
     // this lane's first column of chunk c; its others follow (VEC) or are 32 apart
     auto col = [&](int c) { return (c * kWarps + warp) * kChunk + lane * (VEC ? kPer : 1); };
-    const T* x = static_cast<const T*>(a.x) + row * a.x_ld;
-    alignas(16) Raw<T> rx[kChunks], ra[kChunks];
+    alignas(16) Raw<T> rx[C], ra[C];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        rx[c] = ra[c] = Raw<T>{};
-        load_chunk<VEC>(rx[c], x, col(c), a.width);
-    }
-    if (a.add != nullptr) {
-        const T* add = static_cast<const T*>(a.add) + row * a.add_ld;
+    for (int c = 0; c < C; ++c) rx[c] = ra[c] = Raw<T>{};
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) load_chunk<VEC>(ra[c], add, col(c), a.width);
-    }
-    float h[kChunks][kPer];
-    float ss = 0.f;
+        for (int c = 0; c < C; ++c) load_chunk<VEC>(rx[c], x, col(c), a.width);
+        if (a.add == nullptr) return;
+        const T* add = static_cast<const T*>(a.add) + r * a.add_ld;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < C; ++c) load_chunk<VEC>(ra[c], add, col(c), a.width);
+    };
+    fetch(row);
+    for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
+        // other words than the row before: a warp may still read those
+        float (&buf)[3][kWarps] = bufs[turn];
+        float h[C][kPer];
+        float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            h[c][e] = to_float(rx[c].v[e]) + to_float(ra[c].v[e]);   // zeros past the row
-            ss = fmaf(h[c][e], h[c][e], ss);
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                h[c][e] = to_float(rx[c].v[e]) + to_float(ra[c].v[e]);   // zeros past the row
+                ss = fmaf(h[c][e], h[c][e], ss);
+            }
+        if (kCtas<T, VEC, TPR, C> > 0 && row + stride < a.n_rows) fetch(row + stride);
+        ss = row_reduce<TPR, false>(ss, buf[0]);
+        float rstd;
+        // Squares beyond float32, or so small that they lose bits which eps does
+        // not cover: once more, of h times a power of two (all threads of the row)
+        const bool high = isinf(ss);
+        const bool low = ss < 0x1p-60f * (float)a.width && a.eps < 0x1p-60f;
+        if (high || low) {
+            const float f = high ? 0x1p-70f : 0x1p60f;
+            ss = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) ss = fmaf(h[c][e] * f, h[c][e] * f, ss);
+            ss = row_reduce<TPR, false>(ss, buf[1]);
+            rstd = f / sqrtf(ss / (float)a.width + a.eps * f * f);
+        } else {
+            rstd = 1.f / sqrtf(ss / (float)a.width + a.eps);
         }
-    ss = row_reduce<TPR, false>(ss, buf[0]);
-    float rstd;
-    // Squares beyond float32, or so small that they lose bits which eps does
-    // not cover: once more, of h times a power of two (all threads of the row)
-    const bool high = isinf(ss);
-    const bool low = ss < 0x1p-60f * (float)a.width && a.eps < 0x1p-60f;
-    if (high || low) {
-        const float f = high ? 0x1p-70f : 0x1p60f;
-        ss = 0.f;
+        if (a.total != nullptr) {
+            T* t = static_cast<T*>(a.total) + row * a.total_ld;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) ss = fmaf(h[c][e] * f, h[c][e] * f, ss);
-        ss = row_reduce<TPR, false>(ss, buf[1]);
-        rstd = f / sqrtf(ss / (float)a.width + a.eps * f * f);
-    } else {
-        rstd = 1.f / sqrtf(ss / (float)a.width + a.eps);
-    }
-    if (a.total != nullptr) {
-        T* t = static_cast<T*>(a.total) + row * a.total_ld;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) store_chunk<VEC>(t, h[c], col(c), a.width);
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {                  // y in the place of h
-        alignas(16) Raw<float> w;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) w.v[e] = 1.f;
-        if (a.weight != nullptr) load_chunk<VEC>(w, a.weight, col(c), a.width);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            h[c][e] = h[c][e] * rstd * w.v[e];
-            if (E4M3) amax = max_nan(amax, fabsf(h[c][e]));
+            for (int c = 0; c < C; ++c) store_chunk<VEC>(t, h[c], col(c), a.width);
         }
-    }
-    if constexpr (!E4M3) {
-        T* y = static_cast<T*>(a.out) + row * a.out_ld;
+        float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) store_chunk<VEC>(y, h[c], col(c), a.width);
-    } else {
-        const int n_groups = a.group == 0 ? 1 : (a.width + a.group - 1) / a.group;
-        float* scales = a.scales + row * n_groups;
-        uint8_t* codes = static_cast<uint8_t*>(a.out) + row * a.out_ld;
-        float s = 0.f;
-        if (a.group == 0) {
-            s = scale_of(row_reduce<TPR, true>(amax, buf[2]));
-            if (warp == 0 && lane == 0) scales[0] = s;
+        for (int c = 0; c < C; ++c) {                  // y in the place of h
+            alignas(16) Raw<float> w;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) w.v[e] = 1.f;
+            if (a.weight != nullptr) load_chunk<VEC>(w, a.weight, col(c), a.width);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                h[c][e] = h[c][e] * rstd * w.v[e];
+                if (E4M3 && a.group == 0) amax = max_nan(amax, fabsf(h[c][e]));
+            }
         }
+        if constexpr (!E4M3) {
+            T* y = static_cast<T*>(a.out) + row * a.out_ld;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int at = (c * kWarps + warp) * kChunk;
-            if (at >= a.width) break;                    // the whole warp
-            float inv[kPer];
+            for (int c = 0; c < C; ++c) store_chunk<VEC>(y, h[c], col(c), a.width);
+        } else {
+            const int n_groups = a.group == 0 ? 1 : (a.width + a.group - 1) / a.group;
+            float* scales = a.scales + row * n_groups;
+            uint8_t* codes = static_cast<uint8_t*>(a.out) + row * a.out_ld;
+            float s = 0.f;
             if (a.group == 0) {
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
-            } else if (VEC) {
-                // a group is 4, 8 or 16 lanes
-                float m = 0.f;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) m = max_nan(m, fabsf(h[c][e]));
-                const int lanes = a.group / kPer;
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const float m8 = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                const float m16 = max_nan(m8, __shfl_xor_sync(0xffffffffu, m8, 8));
-                s = scale_of(lanes == 4 ? m : lanes == 8 ? m8 : m16);
-                if (lane % lanes == 0 && col(c) < a.width) scales[col(c) / a.group] = s;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
-            } else {
-                // a group is 1, 2 or 4 neighbouring elements of all lanes
-                const int n = a.group / 32;
-                float m[kPer];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    m[e] = fabsf(h[c][e]);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
-                        m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
-                }
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) {
-                    const float m2 = max_nan(m[e & ~1], m[e | 1]);
-                    const float m4 = max_nan(max_nan(m[e & ~3], m[(e & ~3) + 1]),
-                                             max_nan(m[(e & ~3) + 2], m[e | 3]));
-                    s = scale_of(n == 1 ? m[e] : n == 2 ? m2 : m4);
-                    if (lane == 0 && e % n == 0 && at + 32 * e < a.width)
-                        scales[(at + 32 * e) / a.group] = s;
-                    inv[e] = 1.f / s;
-                }
+                s = scale_of(row_reduce<TPR, true>(amax, buf[2]));
+                if (warp == 0 && lane == 0) scales[0] = s;
             }
-            // to nearest even; a NaN stays one.  The product with 1 / s may be
-            // the neighbouring code of the quotient's only where that lies within
-            // 2^-23 of the middle between two codes.
-            alignas(8) uint8_t q[kPer];
 #pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-                    make_float2(h[c][e] * inv[e], h[c][e + 1] * inv[e + 1]), __NV_SATFINITE, __NV_E4M3);
-                q[e] = (uint8_t)(two & 0xff);
-                q[e + 1] = (uint8_t)(two >> 8);
-            }
-            if (VEC) {
-                if (col(c) < a.width)
-                    *reinterpret_cast<uint2*>(codes + col(c)) = *reinterpret_cast<const uint2*>(q);
-            } else {
+            for (int c = 0; c < C; ++c) {
+                const int at = (c * kWarps + warp) * kChunk;
+                if (at >= a.width) break;                    // the whole warp
+                float inv[kPer];
+                if (a.group == 0) {
 #pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (col(c) + 32 * e < a.width) codes[col(c) + 32 * e] = q[e];
+                    for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
+                } else if (VEC) {
+                    // a group is 4, 8 or 16 lanes
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) m = max_nan(m, fabsf(h[c][e]));
+                    const int lanes = a.group / kPer;
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    const float m8 = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    const float m16 = max_nan(m8, __shfl_xor_sync(0xffffffffu, m8, 8));
+                    s = scale_of(lanes == 4 ? m : lanes == 8 ? m8 : m16);
+                    if (lane % lanes == 0 && col(c) < a.width) scales[col(c) / a.group] = s;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
+                } else {
+                    // a group is 1, 2 or 4 neighbouring elements of all lanes
+                    const int n = a.group / 32;
+                    float m[kPer];
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        m[e] = fabsf(h[c][e]);
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
+                    }
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        const float m2 = max_nan(m[e & ~1], m[e | 1]);
+                        const float m4 = max_nan(max_nan(m[e & ~3], m[(e & ~3) + 1]),
+                                                 max_nan(m[(e & ~3) + 2], m[e | 3]));
+                        s = scale_of(n == 1 ? m[e] : n == 2 ? m2 : m4);
+                        if (lane == 0 && e % n == 0 && at + 32 * e < a.width)
+                            scales[(at + 32 * e) / a.group] = s;
+                        inv[e] = 1.f / s;
+                    }
+                }
+                // to nearest even; a NaN stays one.  The product with 1 / s may be
+                // the neighbouring code of the quotient's only where that lies within
+                // 2^-23 of the middle between two codes.
+                alignas(8) uint8_t q[kPer];
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) {
+                    const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                        make_float2(h[c][e] * inv[e], h[c][e + 1] * inv[e + 1]), __NV_SATFINITE, __NV_E4M3);
+                    q[e] = (uint8_t)(two & 0xff);
+                    q[e + 1] = (uint8_t)(two >> 8);
+                }
+                if (VEC) {
+                    if (col(c) < a.width)
+                        *reinterpret_cast<uint2*>(codes + col(c)) = *reinterpret_cast<const uint2*>(q);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        if (col(c) + 32 * e < a.width) codes[col(c) + 32 * e] = q[e];
+                }
             }
         }
     }
 }
 
+template <typename T, bool E4M3, bool VEC, int TPR, int C>
+cudaError_t launch(const NormArgs& a, cudaStream_t st) {
+    constexpr int kRows = TPR == 32 ? 8 : 1;
+    int64_t blocks = (a.n_rows + kRows - 1) / kRows;
+    const int64_t wave = (int64_t)sm_count() * kCtas<T, VEC, TPR, C>;
+    if (wave > 0 && blocks > wave) blocks = wave;
+    return launch_pdl(rms_norm_kernel<T, E4M3, VEC, TPR, C>, dim3((unsigned)blocks),
+                      dim3(TPR == 32 ? 256 : TPR), 0, st, a);
+}
+
 template <typename T, bool E4M3, bool VEC>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
-    // a warp to a row of up to 1,024 columns; else 128 or 512 threads
-    if (a.width <= kChunk * kChunks)
-        return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 32>, dim3((unsigned)((a.n_rows + 7) / 8)),
-                          dim3(256), 0, st, a);
-    if (a.width <= 4 * kChunk * kChunks)
-        return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 128>, dim3((unsigned)a.n_rows), dim3(128), 0,
-                          st, a);
-    return launch_pdl(rms_norm_kernel<T, E4M3, VEC, 512>, dim3((unsigned)a.n_rows), dim3(512), 0, st, a);
+    // a warp to a row of up to 1,024 columns; beyond, as many threads as leave each
+    // two pieces of eight columns: its registers then let 1,500 threads or more of a
+    // multiprocessor have loads in flight
+    if (a.width <= 512) return launch<T, E4M3, VEC, 32, 2>(a, st);
+    if (a.width <= 1024) return launch<T, E4M3, VEC, 32, 4>(a, st);
+    if (a.width <= 2048) return launch<T, E4M3, VEC, 128, 2>(a, st);
+    if (a.width <= 4096) return launch<T, E4M3, VEC, 256, 2>(a, st);
+    if (a.width <= 8192) return launch<T, E4M3, VEC, 512, 2>(a, st);
+    return launch<T, E4M3, VEC, 512, 4>(a, st);
 }
 
 template <typename T>
