@@ -611,7 +611,7 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
         return DSA_ERR_INVALID_ARG;
     if (width > 16384 || n_rows >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
     const NormArgs a{n_rows, x_ld, add_ld, total_ld, out_ld, x,     add, weight,
-                     total,  out,  scales, width,    group,  eps};
+                     total,  out,  scales, width,    group,  eps,   (float)(1.0 / width)};
     return cuda_status(launch_rms_norm(a, dtype, e4m3, static_cast<cudaStream_t>(stream)), "rms_norm");
 }
 

@@ -256,7 +256,7 @@ struct NormArgs {
     void *total, *out;
     float* scales;
     int32_t width, group;
-    float eps;
+    float eps, mean;                                     // mean: 1 / width
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int32_t dtype, bool e4m3, cudaStream_t st);
 

@@ -114,26 +114,6 @@ __device__ __forceinline__ int64_t answer_block(const uint4* answer) {
     return given ? (int64_t)x : -1;
 }
 
-// Two at a time: x * a + b, and sums.
-__device__ __forceinline__ float2 fma_x2(float2 x, float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, a, b, d;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %5};\n\tmov.b64 b, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, x, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add_x2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\t"
-        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // The softmax warps meet here, and learn whether any thread's `p` holds.
 __device__ __forceinline__ bool softmax_vote(bool p) {
     uint32_t r;

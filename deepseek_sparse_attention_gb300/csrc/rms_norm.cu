@@ -25,20 +25,45 @@ constexpr int kChunk = 32 * kPer;            // columns of a warp's chunk
 constexpr float kTop = 448.f;                // the largest e4m3 value
 constexpr float kLeast = 0x1p-126f;          // the least scale: its inverse is finite
 
-// Eight elements as they are in memory.
-template <typename T>
-struct Raw {
-    T v[kPer];
+// Eight elements as they are in memory: neighbours (VEC) or 32 apart.
+template <typename T, bool VEC>
+struct Raw;
+template <bool VEC>
+struct Raw<float, VEC> {
+    float v[kPer];
+    __device__ __forceinline__ float2 pair(int i) const { return make_float2(v[2 * i], v[2 * i + 1]); }
+    __device__ __forceinline__ void set(int i, float2 x) { v[2 * i] = x.x; v[2 * i + 1] = x.y; }
+};
+template <>
+struct Raw<__nv_bfloat16, true> {
+    uint32_t v[kPer / 2];
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+    }
+    __device__ __forceinline__ void set(int i, float2 x) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
+        v[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+};
+template <>
+struct Raw<__nv_bfloat16, false> {
+    __nv_bfloat16 v[kPer];
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(__bfloat162float(v[2 * i]), __bfloat162float(v[2 * i + 1]));
+    }
+    __device__ __forceinline__ void set(int i, float2 x) {
+        v[2 * i] = __float2bfloat16_rn(x.x);
+        v[2 * i + 1] = __float2bfloat16_rn(x.y);
+    }
 };
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_chunk(Raw<T>& r, const T* p, int col, int width) {
-    if (VEC) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_chunk(Raw<T, VEC>& r, const T* p, int col, int width) {
+    if constexpr (VEC) {
         if (col >= width) return;
-        constexpr int n = sizeof(Raw<T>) / 16;
+        constexpr int n = sizeof(r) / 16;
 #pragma unroll
-        for (int i = 0; i < n; ++i)
-            reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p + col)[i];
+        for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p + col)[i];
     } else {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
@@ -46,20 +71,16 @@ __device__ __forceinline__ void load_chunk(Raw<T>& r, const T* p, int col, int w
     }
 }
 
-__device__ __forceinline__ void round_to(float* d, float v) { *d = v; }
-__device__ __forceinline__ void round_to(__nv_bfloat16* d, float v) { *d = __float2bfloat16_rn(v); }
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_chunk(T* p, const float (&h)[kPer], int col, int width) {
-    alignas(16) Raw<T> r;
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* p, const float2 (&h)[kPer / 2], int col, int width) {
+    alignas(16) Raw<T, VEC> r;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) round_to(&r.v[e], h[e]);
-    if (VEC) {
+    for (int i = 0; i < kPer / 2; ++i) r.set(i, h[i]);
+    if constexpr (VEC) {
         if (col >= width) return;
-        constexpr int n = sizeof(Raw<T>) / 16;
+        constexpr int n = sizeof(r) / 16;
 #pragma unroll
-        for (int i = 0; i < n; ++i)
-            reinterpret_cast<uint4*>(p + col)[i] = reinterpret_cast<const uint4*>(&r)[i];
+        for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(p + col)[i] = reinterpret_cast<const uint4*>(&r)[i];
     } else {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
@@ -86,15 +107,22 @@ __device__ __forceinline__ float row_reduce(float v, float* buf) {
     if (TPR > 32) {
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = buf[0];
+        v = buf[threadIdx.x % (TPR / 32)];               // the warps' values, several times over
 #pragma unroll
-        for (int w = 1; w < TPR / 32; ++w) v = MAX ? max_nan(v, buf[w]) : v + buf[w];
+        for (int o = TPR / 64; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(0xffffffffu, v, o);
+            v = MAX ? max_nan(v, u) : v + u;
+        }
     }
     return v;
 }
 
-__device__ __forceinline__ float scale_of(float amax) {
-    return isnan(amax) ? amax : fmaxf(amax / kTop, kLeast);
+__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kTop), kLeast); }
+// 1 / s within a unit in the last place, for s from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
 }
 
 // CTAs of a multiprocessor that the registers of a row and of the next one allow;
@@ -120,33 +148,32 @@ rms_norm_kernel(const NormArgs a) {
 
     // this lane's first column of chunk c; its others follow (VEC) or are 32 apart
     auto col = [&](int c) { return (c * kWarps + warp) * kChunk + lane * (VEC ? kPer : 1); };
-    alignas(16) Raw<T> rx[C], ra[C];
+    alignas(16) Raw<T, VEC> rx[C], ra[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) rx[c] = ra[c] = Raw<T>{};
+    for (int c = 0; c < C; ++c) rx[c] = ra[c] = Raw<T, VEC>{};
     auto fetch = [&](int64_t r) {
         const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk<VEC>(rx[c], x, col(c), a.width);
+        for (int c = 0; c < C; ++c) load_chunk(rx[c], x, col(c), a.width);
         if (a.add == nullptr) return;
         const T* add = static_cast<const T*>(a.add) + r * a.add_ld;
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk<VEC>(ra[c], add, col(c), a.width);
+        for (int c = 0; c < C; ++c) load_chunk(ra[c], add, col(c), a.width);
     };
     fetch(row);
     for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
         // other words than the row before: a warp may still read those
         float (&buf)[3][kWarps] = bufs[turn];
-        float h[C][kPer];
-        float ss = 0.f;
+        float2 h[C][kPer / 2], sq = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                h[c][e] = to_float(rx[c].v[e]) + to_float(ra[c].v[e]);   // zeros past the row
-                ss = fmaf(h[c][e], h[c][e], ss);
+            for (int i = 0; i < kPer / 2; ++i) {
+                h[c][i] = add_x2(rx[c].pair(i), ra[c].pair(i));   // zeros past the row
+                sq = fma_x2(h[c][i], h[c][i], sq);
             }
         if (kCtas<T, VEC, TPR, C> > 0 && row + stride < a.n_rows) fetch(row + stride);
-        ss = row_reduce<TPR, false>(ss, buf[0]);
+        float ss = row_reduce<TPR, false>(sq.x + sq.y, buf[0]);
         float rstd;
         // Squares beyond float32, or so small that they lose bits which eps does
         // not cover: once more, of h times a power of two (all threads of the row)
@@ -158,37 +185,43 @@ rms_norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) ss = fmaf(h[c][e] * f, h[c][e] * f, ss);
+                for (int i = 0; i < kPer / 2; ++i)
+                    ss = fmaf(h[c][i].y * f, h[c][i].y * f, fmaf(h[c][i].x * f, h[c][i].x * f, ss));
             ss = row_reduce<TPR, false>(ss, buf[1]);
-            rstd = f / sqrtf(ss / (float)a.width + a.eps * f * f);
+            rstd = f * rsqrtf(ss * a.mean + a.eps * f * f);
         } else {
-            rstd = 1.f / sqrtf(ss / (float)a.width + a.eps);
+            rstd = rsqrtf(ss * a.mean + a.eps);
         }
         if (a.total != nullptr) {
             T* t = static_cast<T*>(a.total) + row * a.total_ld;
 #pragma unroll
-            for (int c = 0; c < C; ++c) store_chunk<VEC>(t, h[c], col(c), a.width);
+            for (int c = 0; c < C; ++c) store_chunk<T, VEC>(t, h[c], col(c), a.width);
         }
         float amax = 0.f;
+        const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {                  // y in the place of h
-            alignas(16) Raw<float> w;
+        for (int c = 0; c < C; ++c) {                    // y in the place of h
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) w.v[e] = 1.f;
-            if (a.weight != nullptr) load_chunk<VEC>(w, a.weight, col(c), a.width);
+            for (int i = 0; i < kPer / 2; ++i) h[c][i] = mul_x2(h[c][i], rstd2);
+            if (a.weight != nullptr) {
+                alignas(16) Raw<float, VEC> w;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                h[c][e] = h[c][e] * rstd * w.v[e];
-                if (E4M3 && a.group == 0) amax = max_nan(amax, fabsf(h[c][e]));
+                for (int e = 0; e < kPer; ++e) w.v[e] = 0.f;
+                load_chunk(w, a.weight, col(c), a.width);
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) h[c][i] = mul_x2(h[c][i], w.pair(i));
             }
+            if (E4M3 && a.group == 0)
+#pragma unroll
+                for (int i = 0; i < kPer / 2; ++i) amax = max_nan(max_nan(amax, fabsf(h[c][i].x)), fabsf(h[c][i].y));
         }
         if constexpr (!E4M3) {
             T* y = static_cast<T*>(a.out) + row * a.out_ld;
 #pragma unroll
-            for (int c = 0; c < C; ++c) store_chunk<VEC>(y, h[c], col(c), a.width);
+            for (int c = 0; c < C; ++c) store_chunk<T, VEC>(y, h[c], col(c), a.width);
         } else {
-            const int n_groups = a.group == 0 ? 1 : (a.width + a.group - 1) / a.group;
-            float* scales = a.scales + row * n_groups;
+            const int shift = a.group == 0 ? 30 : 31 - __clz(a.group);   // a column's scale: its number >> shift
+            float* scales = a.scales + row * (((a.width - 1) >> shift) + 1);
             uint8_t* codes = static_cast<uint8_t*>(a.out) + row * a.out_ld;
             float s = 0.f;
             if (a.group == 0) {
@@ -198,32 +231,29 @@ rms_norm_kernel(const NormArgs a) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int at = (c * kWarps + warp) * kChunk;
-                if (at >= a.width) break;                    // the whole warp
-                float inv[kPer];
-                if (a.group == 0) {
+                if (at >= a.width) break;                // the whole warp
+                float2 inv[VEC ? 1 : kPer / 2];
+                if (VEC || a.group == 0) {
+                    if (a.group != 0) {                  // 4, 8 or 16 lanes
+                        float m = 0.f;
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
-                } else if (VEC) {
-                    // a group is 4, 8 or 16 lanes
-                    float m = 0.f;
+                        for (int i = 0; i < kPer / 2; ++i) m = max_nan(max_nan(m, fabsf(h[c][i].x)), fabsf(h[c][i].y));
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        if (shift > 5) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        if (shift > 6) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        s = scale_of(m);
+                        if ((col(c) & (a.group - 1)) == 0 && col(c) < a.width) scales[col(c) >> shift] = s;
+                    }
+                    const float r = inverse(s);
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) m = max_nan(m, fabsf(h[c][e]));
-                    const int lanes = a.group / kPer;
-                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    const float m8 = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    const float m16 = max_nan(m8, __shfl_xor_sync(0xffffffffu, m8, 8));
-                    s = scale_of(lanes == 4 ? m : lanes == 8 ? m8 : m16);
-                    if (lane % lanes == 0 && col(c) < a.width) scales[col(c) / a.group] = s;
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) inv[e] = 1.f / s;
-                } else {
-                    // a group is 1, 2 or 4 neighbouring elements of all lanes
+                    for (int i = 0; i < (VEC ? 1 : kPer / 2); ++i) inv[i] = make_float2(r, r);
+                } else {                                 // 1, 2 or 4 neighbouring elements of all lanes
                     const int n = a.group / 32;
                     float m[kPer];
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
-                        m[e] = fabsf(h[c][e]);
+                        m[e] = fabsf(e & 1 ? h[c][e / 2].y : h[c][e / 2].x);
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1)
                             m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
@@ -234,21 +264,20 @@ rms_norm_kernel(const NormArgs a) {
                         const float m4 = max_nan(max_nan(m[e & ~3], m[(e & ~3) + 1]),
                                                  max_nan(m[(e & ~3) + 2], m[e | 3]));
                         s = scale_of(n == 1 ? m[e] : n == 2 ? m2 : m4);
-                        if (lane == 0 && e % n == 0 && at + 32 * e < a.width)
-                            scales[(at + 32 * e) / a.group] = s;
-                        inv[e] = 1.f / s;
+                        if (lane == 0 && e % n == 0 && at + 32 * e < a.width) scales[(at + 32 * e) >> shift] = s;
+                        (e & 1 ? inv[VEC ? 0 : e / 2].y : inv[VEC ? 0 : e / 2].x) = inverse(s);
                     }
                 }
                 // to nearest even; a NaN stays one.  The product with 1 / s may be
                 // the neighbouring code of the quotient's only where that lies within
-                // 2^-23 of the middle between two codes.
+                // 2^-22 of the middle between two codes.
                 alignas(8) uint8_t q[kPer];
 #pragma unroll
-                for (int e = 0; e < kPer; e += 2) {
-                    const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
-                        make_float2(h[c][e] * inv[e], h[c][e + 1] * inv[e + 1]), __NV_SATFINITE, __NV_E4M3);
-                    q[e] = (uint8_t)(two & 0xff);
-                    q[e + 1] = (uint8_t)(two >> 8);
+                for (int i = 0; i < kPer / 2; ++i) {
+                    const __nv_fp8x2_storage_t two =
+                        __nv_cvt_float2_to_fp8x2(mul_x2(h[c][i], inv[VEC ? 0 : i]), __NV_SATFINITE, __NV_E4M3);
+                    q[2 * i] = (uint8_t)(two & 0xff);
+                    q[2 * i + 1] = (uint8_t)(two >> 8);
                 }
                 if (VEC) {
                     if (col(c) < a.width)
