@@ -57,13 +57,24 @@ struct Raw<__nv_bfloat16, false> {
     }
 };
 
-template <typename T, bool VEC>
+// ONCE: not kept in L1, where the weights shall stay.
+template <bool ONCE, typename T, bool VEC>
 __device__ __forceinline__ void load_chunk(Raw<T, VEC>& r, const T* p, int col, int width) {
     if constexpr (VEC) {
         if (col >= width) return;
         constexpr int n = sizeof(r) / 16;
 #pragma unroll
-        for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p + col)[i];
+        for (int i = 0; i < n; ++i) {
+            const uint4* q = reinterpret_cast<const uint4*>(p + col) + i;
+            uint4& x = reinterpret_cast<uint4*>(&r)[i];
+            if constexpr (ONCE)
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                             : "l"(q)
+                             : "memory");
+            else
+                x = *q;
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
@@ -154,11 +165,11 @@ rms_norm_kernel(const NormArgs a) {
     auto fetch = [&](int64_t r) {
         const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk(rx[c], x, col(c), a.width);
+        for (int c = 0; c < C; ++c) load_chunk<true>(rx[c], x, col(c), a.width);
         if (a.add == nullptr) return;
         const T* add = static_cast<const T*>(a.add) + r * a.add_ld;
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk(ra[c], add, col(c), a.width);
+        for (int c = 0; c < C; ++c) load_chunk<true>(ra[c], add, col(c), a.width);
     };
     fetch(row);
     for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
@@ -172,7 +183,16 @@ rms_norm_kernel(const NormArgs a) {
                 h[c][i] = add_x2(rx[c].pair(i), ra[c].pair(i));   // zeros past the row
                 sq = fma_x2(h[c][i], h[c][i], sq);
             }
-        if (kCtas<T, VEC, TPR, C> > 0 && row + stride < a.n_rows) fetch(row + stride);
+        if (kCtas<T, VEC, TPR, C> > 0 && row + stride < a.n_rows) {
+            fetch(row + stride);
+            // and the one after it into L2 (16-byte pieces, as the loads are)
+            const int64_t later = row + 2 * stride;
+            if (warp == 0 && lane == 0 && later < a.n_rows) {
+                const uint32_t bytes = (uint32_t)a.width * sizeof(T);
+                prefetch_l2_bytes(static_cast<const T*>(a.x) + later * a.x_ld, bytes);
+                if (a.add != nullptr) prefetch_l2_bytes(static_cast<const T*>(a.add) + later * a.add_ld, bytes);
+            }
+        }
         float ss = row_reduce<TPR, false>(sq.x + sq.y, buf[0]);
         float rstd;
         // Squares beyond float32, or so small that they lose bits which eps does
@@ -207,7 +227,7 @@ rms_norm_kernel(const NormArgs a) {
                 alignas(16) Raw<float, VEC> w;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) w.v[e] = 0.f;
-                load_chunk(w, a.weight, col(c), a.width);
+                load_chunk<false>(w, a.weight, col(c), a.width);
 #pragma unroll
                 for (int i = 0; i < kPer / 2; ++i) h[c][i] = mul_x2(h[c][i], w.pair(i));
             }
