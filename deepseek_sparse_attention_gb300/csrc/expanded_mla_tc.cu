@@ -84,7 +84,6 @@ struct Shared {
     uint64_t work_full[kWorks], work_free[kWorks], next_full[2], next_free[2];
     alignas(16) uint4 next[2];                           // answers to the requests for work
     Work work[kWorks];
-    float top[2][kSoftmax];                              // maxima of a row's halves, of every other tile
     float l[2][kSoftmax], m[2][kRows];                   // a unit's sums of halves, and its maxima
     uint32_t tmem;
     int32_t abort, poison[2];                            // poison: the last unit that met odd values
@@ -274,13 +273,13 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         for (int c = 0; c < VD / 128 && ok; ++c)
                             tma_load_3d_pair(dst + c * kVBlock, &tm_v, bar, rank * (VD / 2) + c * 64, w.h, y);
                     };
-                    keys(w.kt0);
-                    ok = ok && (busy == 0 || wait(&s.q_free, (busy - 1) & 1, abort));
+                    ok = (busy == 0 || wait(&s.q_free, (busy - 1) & 1, abort));
                     if (!ok) break;
                     if (rank == 0) mbar_arrive_expect_tx(&s.q_full, 2 * nk * kQBlock);
                     for (int b = 0; b < nk; ++b)
                         tma_load_3d_pair(Qs + b * kQBlock, &tm_q, cluster_addr(&s.q_full, 0), b * 64, w.h,
                                          (int32_t)(w.q0 + rank * kRows));
+                    keys(w.kt0);
                     for (int i = 0; i < w.n && ok; ++i) {
                         if (i + 1 < w.n) keys(w.kt0 + i + 1);
                         if (ok) values(w.kt0 + i);
@@ -508,10 +507,14 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
                 // of -inf: any logit above it
                 if (softmax_vote(top > m + kSlack || !ok)) {
-                    s.top[g & 1][threadIdx.x] = top;
+                    // through the columns of S behind P: the products leave shared memory
+                    // little bandwidth for others
+                    tmem_st_1col(at + kK / 2 + half, top);
+                    tc_fence_before();
                     ok = !softmax_vote(!ok);
                     if (!ok) break;
-                    top = fmaxf(top, s.top[g & 1][threadIdx.x ^ 128]);
+                    tc_fence_after();
+                    top = fmaxf(top, tmem_ld_1col(at + kK / 2 + (half ^ 1)));
                     const float mn = top > m + kSlack ? top : m;
                     const float f = mn == m ? 1.f : ex2(m - mn);
                     if (__any_sync(0xffffffffu, mn != m) && i > 0) {

@@ -608,5 +608,20 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const float (&v)[
         : "memory");
 }
 
+// One column of this thread's TMEM lane.
+__device__ __forceinline__ float tmem_ld_1col(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(taddr)
+                 : "memory");
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st_1col(uint32_t taddr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+                 "r"(__float_as_uint(v))
+                 : "memory");
+}
+
 }  // namespace sm100
 }  // namespace dsa
