@@ -11,7 +11,9 @@
 //             last tile of the rows before has read it; a ring of weight blocks;
 //   warp 5    in the first CTA issues the products for both;
 //   warps 0-3 epilogue, a row to a thread: bf16 in whole sectors.
-// Bound by the tensor cores for prompts, by reading the weights (29 MB) for a few rows.
+// Bound by writing for prompts: 4,096 rows are 235 MB of keys and values, 63 us at the
+// rate of 3.7 TB/s at which this memory takes writes alone; without the stores the
+// products take 56 us.  A few rows: by reading the weights (29 MB).
 #include "dsa_kernels.cuh"
 #include "pair.cuh"
 
@@ -23,21 +25,21 @@ using namespace sm100;
 constexpr int kM = 256, kRows = 128;                     // rows of a tile and of a CTA
 constexpr int kDepth = 512, kKB = kDepth / 64;           // the sum, in blocks of 64
 constexpr uint32_t kABlock = kRows * 128;
-constexpr int kRing = 5;
+template <int NT>
+constexpr int kRing = NT == 256 ? 6 : 12;                // weight blocks: 96 KB of them
 constexpr int kThreads = 192;
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
 constexpr uint32_t kBarBytes = 1024;
 
 struct Shared {
-    uint64_t a_full[kKB], a_free[kKB], full[kRing], empty[kRing], acc_full[2], acc_free[2], drain;
+    uint64_t a_full[kKB], a_free[kKB], full[12], empty[12], acc_full[2], acc_free[2], drain;
     uint32_t tmem;
     int32_t abort;
 };
 static_assert(sizeof(Shared) <= kBarBytes, "barriers");
 
-__host__ __device__ constexpr uint32_t smem_bytes(int nt) {
-    return 1024 + kBarBytes + kKB * kABlock + kRing * (nt / 2) * 128;
-}
+template <int NT>
+constexpr uint32_t kSmem = 1024 + kBarBytes + kKB * kABlock + kRing<NT> * (NT / 2) * 128;
 
 template <int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -62,7 +64,7 @@ expand_tc(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ C
             mbar_init(&s.a_full[i], 1);
             mbar_init(&s.a_free[i], 1);
         }
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < kRing<NT>; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -114,7 +116,7 @@ expand_tc(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ C
                     if (rank == 0) mbar_arrive_expect_tx(&s.full[p.at], 2 * kBBlock);
                     tma_load_2d_pair(Bs + p.at * kBBlock, is_v ? &tm_uv : &tm_uk, cluster_addr(&s.full[p.at], 0),
                                      kb * 64, y);
-                    p.step(kRing);
+                    p.step(kRing<NT>);
                 }
                 if (fresh) ++loads;
                 if (++n == n_tiles) { n = 0; ++m; }
@@ -148,7 +150,7 @@ expand_tc(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ C
                                          sdesc_kmajor_sw128(b_addr + p.at * kBBlock + kk * 32), idesc, (kb | kk) != 0);
                     mma_commit_pair(&s.empty[p.at]);
                     if (last) mma_commit_pair(&s.a_free[kb]);
-                    p.step(kRing);
+                    p.step(kRing<NT>);
                 }
                 if (ok) mma_commit_pair(&s.acc_full[t & 1]);
                 if (fresh) ++loads;
@@ -224,12 +226,12 @@ cudaError_t launch(const Shape& sh, int64_t n_rows, int32_t n_k, int32_t n_v, co
         !map(&tv, w_uv, n_v, kDepth, NT / 2))
         return cudaErrorInvalidValue;
     auto kern = expand_tc<NT>;
-    cudaError_t e = ensure_dyn_smem((const void*)kern, (int)smem_bytes(NT));
+    cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem<NT>);
     if (e != cudaSuccess) return e;
     const int64_t total = (n_rows + kM - 1) / kM * ((n_k + n_v) / NT);
     int64_t pairs = sm_count() / 2;
     if (pairs > total) pairs = total;
-    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem_bytes(NT), st, tr, tk, tv,
+    return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem<NT>, st, tr, tk, tv,
                       static_cast<__nv_bfloat16*>(k_nope), static_cast<__nv_bfloat16*>(v), n_rows, n_k, n_v, err);
 }
 
