@@ -46,7 +46,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_tc(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_uk,
           const __grid_constant__ CUtensorMap tm_uv, __nv_bfloat16* __restrict__ k_nope,
           __nv_bfloat16* __restrict__ v, const int64_t n_rows, const int32_t n_k, const int32_t n_v,
-          int32_t* err) {
+          const int32_t box_rows, int32_t* err) {
     constexpr uint32_t kBBlock = NT / 2 * 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -107,7 +107,7 @@ expand_tc(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ C
                     if (fresh) {
                         ok = loads == 0 || wait(&s.a_free[kb], (loads - 1) & 1, abort);
                         if (!ok) break;
-                        if (rank == 0) mbar_arrive_expect_tx(&s.a_full[kb], 2 * kABlock);
+                        if (rank == 0) mbar_arrive_expect_tx(&s.a_full[kb], 2 * box_rows * 128);
                         tma_load_2d_pair(As + kb * kABlock, &tm_rows, cluster_addr(&s.a_full[kb], 0), kb * 64,
                                          (int32_t)(m * kM + rank * kRows));
                     }
@@ -222,7 +222,9 @@ cudaError_t launch(const Shape& sh, int64_t n_rows, int32_t n_k, int32_t n_v, co
         const uint32_t b[2] = {64, box};
         return encode_bf16_map(m, base, 2, dims, strides, b);
     };
-    if (!map(&tr, rows, n_rows, sh.width(), kRows) || !map(&tk, w_uk, n_k, kDepth, NT / 2) ||
+    // few rows: no more of a tile is loaded (its other rows' results are not stored)
+    const int32_t box_rows = n_rows < kRows ? (int32_t)(n_rows + 7) / 8 * 8 : kRows;
+    if (!map(&tr, rows, n_rows, sh.width(), box_rows) || !map(&tk, w_uk, n_k, kDepth, NT / 2) ||
         !map(&tv, w_uv, n_v, kDepth, NT / 2))
         return cudaErrorInvalidValue;
     auto kern = expand_tc<NT>;
@@ -232,7 +234,7 @@ cudaError_t launch(const Shape& sh, int64_t n_rows, int32_t n_k, int32_t n_v, co
     int64_t pairs = sm_count() / 2;
     if (pairs > total) pairs = total;
     return launch_pdl(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem<NT>, st, tr, tk, tv,
-                      static_cast<__nv_bfloat16*>(k_nope), static_cast<__nv_bfloat16*>(v), n_rows, n_k, n_v, err);
+                      static_cast<__nv_bfloat16*>(k_nope), static_cast<__nv_bfloat16*>(v), n_rows, n_k, n_v, box_rows, err);
 }
 
 }  // namespace
