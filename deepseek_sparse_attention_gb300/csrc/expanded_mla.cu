@@ -1,5 +1,8 @@
-// expanded_mla.cu -- causal attention over expanded keys and values: the plan
-// of its splits, the kernel on CUDA cores, and the merge of splits.
+// expanded_mla.cu -- causal attention over expanded keys and values: float32 on
+// CUDA cores, with the plan of its splits and their merge.  bf16 runs on the
+// tensor cores (expanded_mla_tc.cu), without splits: 64 heads are 64 units of work
+// for 76 pairs of CTAs, and seven splits of each were 2% faster over 130,000 rows,
+// 10% slower over 30,000.
 //
 //   z_j = scale * (q_nope . k_nope[j, h] + q_rope . rope[j]),  j < L
 //   out = sum_j softmax(z)_j v[j, h],  lse = log sum_j exp(z_j)
@@ -20,22 +23,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kKeys = 32;
-constexpr int kMaxTileQ = 256;                           // queries of the largest tile
+constexpr int kMaxTileQ = 64;                            // queries of the largest tile
 constexpr int kMaxSplit = 16;
+constexpr int64_t kSplitWaves = 2;                       // waves of a split call's CTAs, two to a multiprocessor
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
-                       __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                              *reinterpret_cast<const uint32_t*>(&hi));
-}
 
 // Shared memory: the queries, a tile of keys (rows padded by four against bank
 // conflicts) and then its values in their place, the weights by key.  106 KB at
@@ -44,7 +38,7 @@ __host__ __device__ constexpr int simt_smem_floats(int rows, int d, int v) {
     return rows * (d + 4) + kKeys * (d + 4 > v ? d + 4 : v) + kKeys * (rows + 4);
 }
 
-template <typename T, int RPT, int VD>
+template <int RPT, int VD>
 __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     constexpr int BQ = 16 * RPT;
     constexpr int kVec = VD / 64;                        // groups of four output columns of a thread
@@ -63,10 +57,10 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     ExpandedTile t;
     if (!expanded_tile(a.b, slot, split, a.n_split, BQ, kKeys, a.err, 60, t)) return;
 
-    const T* q = static_cast<const T*>(a.q);
-    const T* kn = static_cast<const T*>(a.k_nope);
-    const T* rows = static_cast<const T*>(a.rows);
-    const T* v = static_cast<const T*>(a.v);
+    const float* q = static_cast<const float*>(a.q);
+    const float* kn = static_cast<const float*>(a.k_nope);
+    const float* rows = static_cast<const float*>(a.rows);
+    const float* v = static_cast<const float*>(a.v);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = tid; i < BQ * d / 4; i += 256) {
@@ -176,7 +170,7 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
             if (tx == 0)
                 *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + split) * 2) = make_float2(m[r], l[r]);
         } else {
-            T* out = static_cast<T*>(a.out) + qh * VD;
+            float* out = static_cast<float*>(a.out) + qh * VD;
             const float inv = 1.f / l[r];
 #pragma unroll
             for (int c = 0; c < kVec; ++c)
@@ -188,7 +182,7 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
 }
 
 // One warp per (query, head): the splits' sums weighted by their maxima.
-template <typename T, int VD>
+template <int VD>
 __global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int64_t n) {
     const int64_t qh = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -214,16 +208,16 @@ __global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int6
         }
     }
     const float inv = 1.f / l;
-    T* out = static_cast<T*>(a.out) + qh * VD;
+    float* out = static_cast<float*>(a.out) + qh * VD;
 #pragma unroll
     for (int c = 0; c < VD / 128; ++c)
         store4(out + (c * 32 + lane) * 4, make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv));
     if (lane == 0 && a.lse != nullptr) a.lse[qh] = expanded_lse(top, l);
 }
 
-template <typename T, int RPT, int VD>
-cudaError_t launch_simt(const ExpandedArgs& a, cudaStream_t st) {
-    auto kern = expanded_simt<T, RPT, VD>;
+template <int RPT, int VD>
+cudaError_t launch_tiles(const ExpandedArgs& a, cudaStream_t st) {
+    auto kern = expanded_simt<RPT, VD>;
     const int bytes = simt_smem_floats(16 * RPT, a.nope + a.rope, VD) * 4;
     cudaError_t e = ensure_dyn_smem((const void*)kern, bytes);
     if (e != cudaSuccess) return e;
@@ -231,44 +225,29 @@ cudaError_t launch_simt(const ExpandedArgs& a, cudaStream_t st) {
     return launch_pdl(kern, dim3((unsigned)grid), dim3(256), (size_t)bytes, st, a);
 }
 
-template <typename T, int VD>
-cudaError_t launch_all(const ExpandedArgs& a, bool few, cudaStream_t st) {
-    cudaError_t e;
-    if constexpr (sizeof(T) == 2) e = launch_expanded_tc(a, st);
-    else e = few ? launch_simt<T, 1, VD>(a, st) : launch_simt<T, 4, VD>(a, st);
+template <int VD>
+cudaError_t launch_simt(const ExpandedArgs& a, bool few, cudaStream_t st) {
+    cudaError_t e = few ? launch_tiles<1, VD>(a, st) : launch_tiles<4, VD>(a, st);
     if (e != cudaSuccess || a.n_split == 1) return e;
     const int64_t n = (int64_t)a.b.n_q * a.heads;
-    return launch_pdl(expanded_merge<T, VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
+    return launch_pdl(expanded_merge<VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
 }
 
-// Queries of a tile on CUDA cores: 16 where no sequence has more, else 64.
+// Queries of a tile: 16 where no sequence has more, else 64.
 bool few_queries(const BatchDev& b) { return b.max_q_len <= 16; }
 
-struct TileSize {
-    int queries, keys;
-};
-TileSize tile_size(const Shape& sh, const BatchDev& b) {
-    if (sh.dtype == DSA_BF16) return {kExpandedTcQ, kExpandedTcK};
-    return {few_queries(b) ? 16 : 64, kKeys};
-}
-
 }  // namespace
-
-// CTAs of a split call at most, in waves of one per multiprocessor.
-constexpr int64_t kSplitWaves = 4;
 
 // Splits of the key tiles: as many as end soonest, counting a wave of CTAs as
 // its longest split and a split's partial sums as one more tile.
 int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b) {
-    if (b.n_q < 1) return 1;
-    const TileSize ts = tile_size(sh, b);
-    const int64_t units = expanded_slots(b.n_q, b.n_seq, ts.queries) * sh.heads;
-    const int64_t sms = sh.dtype == DSA_BF16 ? sm_count() / 2 : sm_count();   // CTAs, or pairs, at once
-    const int64_t tiles = (b.max_kv_len + ts.keys - 1) / ts.keys;
+    if (b.n_q < 1 || sh.dtype == DSA_BF16) return 1;
+    const int64_t units = expanded_slots(b.n_q, b.n_seq, few_queries(b) ? 16 : 64) * sh.heads;
+    const int64_t wave = 2 * sm_count(), tiles = (b.max_kv_len + kKeys - 1) / kKeys;
     int32_t best = 1;
     int64_t least = INT64_MAX;
-    for (int32_t s = 1; s <= kMaxSplit && s <= tiles && (s == 1 || units * s <= kSplitWaves * sms); ++s) {
-        const int64_t cost = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + (s > 1 ? 1 : 0));
+    for (int32_t s = 1; s <= kMaxSplit && s <= tiles && (s == 1 || units * s <= kSplitWaves * wave); ++s) {
+        const int64_t cost = (units * s + wave - 1) / wave * ((tiles + s - 1) / s + (s > 1 ? 1 : 0));
         if (cost < least) { least = cost; best = s; }
     }
     return best;
@@ -278,8 +257,8 @@ int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b) {
 // may get more splits, but a tile's queries times its splits stay below the
 // bound on a split call's CTAs.
 size_t expanded_mla_scratch_bytes(const Shape& sh, const BatchDev& b) {
-    if (b.max_kv_len <= kKeys) return 0;
-    const int64_t most = kSplitWaves * sm_count() * kMaxTileQ / sh.heads;
+    if (sh.dtype == DSA_BF16 || b.max_kv_len <= kKeys) return 0;
+    const int64_t most = kSplitWaves * 2 * sm_count() * kMaxTileQ / sh.heads;
     const int64_t all = (int64_t)b.n_q * kMaxSplit;
     return (size_t)(all < most ? all : most) * sh.heads * (256 + 2) * sizeof(float);
 }
@@ -295,10 +274,9 @@ cudaError_t launch_expanded_mla(const Shape& sh, const BatchDev& b, int32_t nope
     a.n_split = plan_expanded_splits(sh, b);
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + (size_t)b.n_q * sh.heads * a.n_split * v_dim;
+    if (sh.dtype == DSA_BF16) return launch_expanded_tc(a, st);
     const bool few = few_queries(b);
-    if (sh.dtype == DSA_BF16)
-        return v_dim == 256 ? launch_all<__nv_bfloat16, 256>(a, few, st) : launch_all<__nv_bfloat16, 128>(a, few, st);
-    return v_dim == 256 ? launch_all<float, 256>(a, few, st) : launch_all<float, 128>(a, few, st);
+    return v_dim == 256 ? launch_simt<256>(a, few, st) : launch_simt<128>(a, few, st);
 }
 
 }  // namespace dsa

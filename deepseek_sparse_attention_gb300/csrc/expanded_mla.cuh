@@ -11,7 +11,7 @@ struct ExpandedArgs {
     const void *q, *k_nope, *rows, *v;
     void* out;
     float* lse;
-    float *part_o, *part_ml;       // partial sums of splits, where there are several
+    float *part_o, *part_ml;       // partial sums of splits (float32), where there are several
     int32_t heads, nope, rope, v_dim, kv_lora, width;
     int32_t n_split;
     float scale;
@@ -19,7 +19,7 @@ struct ExpandedArgs {
     int32_t* err;
 };
 
-// A tile of up to BQ queries of one sequence and the key tiles of one split.
+// A tile of up to `bq` queries of one sequence and the key tiles of one split.
 struct ExpandedTile {
     int64_t q0;                    // first query of the tile
     int64_t row0;                  // first cache row of the sequence
@@ -28,8 +28,8 @@ struct ExpandedTile {
     int32_t kt0, kt1;              // key tiles of the split
 };
 
-// Tiles have slots: sequence s has the slots from q_off[s] / BQ + s on, which is
-// room for its ceil(q_len / BQ) tiles whatever the others' lengths are, so a slot
+// Tiles have slots: sequence s has the slots from q_off[s] / bq + s on, which is
+// room for its ceil(q_len / bq) tiles whatever the others' lengths are, so a slot
 // finds its sequence by a search over the offsets and nothing is planned ahead.
 // Slots left over have no tile.
 __host__ __device__ inline int64_t expanded_slots(int64_t n_q, int64_t n_seq, int bq) {

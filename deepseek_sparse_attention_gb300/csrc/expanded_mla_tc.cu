@@ -4,8 +4,7 @@
 //   S = Q K^T (M = 256 queries, N = 128 keys, K = the head's width), one pass over
 //   the key tiles with a running maximum, O += P V (M = 256, N = v_dim, K = 128 keys)
 //
-// A unit of work is a tile of 256 queries of a sequence, a head and a split of the key
-// tiles; a pair of CTAs (cta_group::2) takes one after the other, each with 128 of the
+// A unit of work is a tile of 256 queries of a sequence and a head; a pair of CTAs (cta_group::2) takes one after the other, each with 128 of the
 // queries, their S, P and O, and half of the keys' rows and of the values' columns to load.
 // The next unit is one whose launch the pair cancels (clusterlaunchcontrol), asked for a unit
 // ahead, so that its copies and first products run while the last one's output is written.
@@ -24,8 +23,7 @@
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
 //              epilogue to the queries that see them;
-//   warps 12-15 epilogue: a unit's O to the output or the split's part, a row to a
-//              thread in whole sectors, beside the next unit's first scores.  (Through shared
+//   warps 12-15 epilogue: a unit's O to the output, a row to a thread in whole sectors, beside the next unit's first scores.  (Through shared
 //              memory to whole lines it took 10 to 20% longer over short units: the
 //              products leave its bandwidth to no one.)
 // A key tile takes 2,050 cycles (head width and v_dim 256), which are the products' own: S
@@ -72,9 +70,9 @@ __device__ __forceinline__ float ex2(float x) {
 // A unit of work as the roles read it.
 struct Work {
     int64_t q0, row0, first;                             // as ExpandedTile, of the pair
-    int32_t n_q, kt0, n;                                 // n: its key tiles, -1: no more work
+    int32_t n_q, n;                                      // n: its key tiles, -1: no more work
     int32_t partial;                                     // key tiles from this one on are not seen in full by every query
-    int32_t h, split;
+    int32_t h;
 };
 
 struct Shared {
@@ -239,16 +237,14 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 w.n = -1;
                 if (block >= 0) {
                     const uint32_t unit = (uint32_t)(block / 2);
-                    w.split = (int)(unit % a.n_split);
-                    w.h = (int)(unit / a.n_split / slots);
-                    const int64_t slot = slots - 1 - (int64_t)(unit / a.n_split % slots);
-                    if (!expanded_tile(a.b, slot, w.split, a.n_split, kQ, kK, w.h == 0 ? a.err : nullptr, 61, t)) {
-                        t.n_q = 0;
-                        t.kt0 = t.kt1 = 0;
+                    w.h = (int)(unit / slots);
+                    const int64_t slot = slots - 1 - (int64_t)(unit % slots);
+                    if (!expanded_tile(a.b, slot, 0, 1, kQ, kK, w.h == 0 ? a.err : nullptr, 61, t)) {
+                        t.n_q = t.kt1 = 0;
                         t.q0 = t.row0 = t.first = 0;
                     }
                     w.q0 = t.q0; w.row0 = t.row0; w.first = t.first;
-                    w.n_q = t.n_q; w.kt0 = t.kt0; w.n = t.kt1 - t.kt0;
+                    w.n_q = t.n_q; w.n = t.kt1;
                     w.partial = (int)(t.first / kK);
                 }
                 ok = k < kWorks || wait(&s.work_free[k % kWorks], (k / kWorks - 1) & 1, abort);
@@ -279,10 +275,10 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     for (int b = 0; b < nk; ++b)
                         tma_load_3d_pair(Qs + b * kQBlock, &tm_q, cluster_addr(&s.q_full, 0), b * 64, w.h,
                                          (int32_t)(w.q0 + rank * kRows));
-                    keys(w.kt0);
+                    keys(0);
                     for (int i = 0; i < w.n && ok; ++i) {
-                        if (i + 1 < w.n) keys(w.kt0 + i + 1);
-                        if (ok) values(w.kt0 + i);
+                        if (i + 1 < w.n) keys(i + 1);
+                        if (ok) values(i);
                     }
                     ++busy;
                 }
@@ -350,7 +346,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     ok = ok && wait(bar, parity, abort);
                     if (!ok) return;
                     n_next = s.work[k % kWorks].n;
-                    partial_next = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
+                    partial_next = s.work[k % kWorks].partial;
                     mbar_arrive(&s.work_free[k % kWorks]);
                     ++k;
                     known = n_next < 0 ? -1 : n_next > 0 ? 1 : 0;
@@ -419,13 +415,13 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             ok = warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
             if (!ok) break;
             const int n = s.work[k % kWorks].n;
-            const int partial = s.work[k % kWorks].partial - s.work[k % kWorks].kt0;
+            const int partial = s.work[k % kWorks].partial;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
             if (n < 0) break;
             if (n == 0) continue;
             ++busy;
-            for (int i = partial > 0 ? partial : 0; i < n; ++i) {
+            for (int i = partial; i < n; ++i) {
                 // before tile i's values: keys of tiles 0 .. min(i + 1, n - 1), values of 0 .. i - 1
                 const uint32_t at = (before + (uint32_t)((i + 1 < n ? i + 2 : n) + i)) % ring;
                 ok = warp_wait(&s.part[at], (parted >> at) & 1, abort);
@@ -477,8 +473,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             ok = ok && warp_wait(&s.work_full[k % kWorks], (k / kWorks) & 1, abort);
             if (softmax_vote(!ok)) { ok = false; break; }          // all go on, or none
             const Work& w = s.work[k % kWorks];
-            const int n = w.n, partial = w.partial - w.kt0;
-            const int64_t sees = w.first + row - (int64_t)w.kt0 * kK;   // keys of the split, and more
+            const int n = w.n, partial = w.partial;
+            const int64_t sees = w.first + row;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
             if (n < 0) break;
@@ -576,11 +572,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (w.n < 0) break;
             const int64_t qh = (w.q0 + row) * a.heads + w.h;
             const bool mine = row < w.n_q;
-            float2* ml = reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + w.split) * 2);
-            if (w.n == 0) {                                        // a split without keys
-                if (mine && a.n_split > 1) *ml = make_float2(-INFINITY, 0.f);
-                continue;
-            }
+            if (w.n == 0) continue;
             // the softmax may be two units ahead of this, hence its two barriers
             ok = warp_wait(&s.l_full[busy & 1], (busy >> 1) & 1, abort) && warp_wait(&s.o_last, busy & 1, abort);
             if (!ok) break;
@@ -589,9 +581,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             ++busy;
             const bool poison = *(volatile int32_t*)&s.poison[busy & 1] == busy;
             if (poison) {                                          // what the cleaners took out and the row sees
-                const int64_t from = (int64_t)(w.partial > w.kt0 ? w.partial : w.kt0) * kK;
-                const int64_t sees = w.first + row, end = (int64_t)(w.kt0 + w.n) * kK;
-                const int64_t to = !mine ? from : sees < end ? sees : end;
+                const int64_t from = (int64_t)w.partial * kK, to = mine ? w.first + row : from;
 #pragma unroll 1
                 for (int c = 0; c < VD; c += 32) {
                     float o[32];
@@ -610,43 +600,25 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tmem_st_32cols(lane_addr + kOCol + c, o);
                 }
             }
-            if (a.n_split > 1) {
-                float* out = a.part_o + (qh * a.n_split + w.split) * VD;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + qh * VD;
+            const float inv = 1.f / l;
 #pragma unroll 2
-                for (int c = 0; c < VD; c += 32) {
-                    float o[32];
-                    tmem_ld_32cols(lane_addr + kOCol + c, o);
-                    if (!mine) continue;
+            for (int c = 0; c < VD; c += 32) {
+                float o[32];
+                tmem_ld_32cols(lane_addr + kOCol + c, o);
+                if (!mine) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t x[8];
+                for (int e = 0; e < 32; e += 16) {
+                    uint32_t x[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(o[e + i]);
-                        store_sector(out + c + e, x);
-                    }
-                }
-            } else {
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + qh * VD;
-                const float inv = 1.f / l;
-#pragma unroll 2
-                for (int c = 0; c < VD; c += 32) {
-                    float o[32];
-                    tmem_ld_32cols(lane_addr + kOCol + c, o);
-                    if (!mine) continue;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                        uint32_t x[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = pack(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
-                        store_sector(out + c + e, x);
-                    }
+                    for (int i = 0; i < 8; ++i) x[i] = pack(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
+                    store_sector(out + c + e, x);
                 }
             }
             tc_fence_before();                                     // O may be written again
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
-            if (mine && a.n_split > 1) *ml = make_float2(m, l);
-            if (mine && a.n_split == 1 && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
+            if (mine && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
         }
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 66);
@@ -689,7 +661,7 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
-    return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads * a.n_split)), dim3(kThreads), kSmem, st, tq, tk, tr,
+    return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads)), dim3(kThreads), kSmem, st, tq, tk, tr,
                       tv, a, (int32_t)slots, (int32_t)ring);
 }
 
