@@ -9,11 +9,14 @@
 //
 // The rope part of the key is the cache row's tail, shared by all heads.
 //
-// One CTA per (tile of 16 RPT queries, head, split of the key tiles): one pass over
-// tiles of 32 keys with a running maximum and sum.  16 lanes share a thread's
-// RPT query rows: of the logits a thread has those rows and two keys, of the
-// output the rows and every 16th group of four columns.  Bound by shared-memory
-// reads (a logit's operands are used RPT and twice) and float32 arithmetic.
+// One CTA per (tile of 8 RPW queries, head, split of the key tiles): one pass over
+// tiles of 32 keys with a running maximum and sum.  A warp has RPW queries.  Of
+// their logits a lane sums a quarter of the columns (every fourth group of four) for
+// all of them and four keys, so that an element read serves four or RPW products, and the
+// quarters meet in shuffles that leave each lane its key.  Of the output a lane has every
+// 32nd group of four columns.  Reads of shared memory and float32 arithmetic bound it
+// about equally: 7,200 wavefronts and 8,200 cycles a tile of 64 queries.  (With a key
+// to a lane, or two and 16 lanes to a query, 14,000 wavefronts.)
 #include "expanded_mla.cuh"
 #include "sm100.cuh"
 
@@ -38,20 +41,21 @@ __host__ __device__ constexpr int simt_smem_floats(int rows, int d, int v) {
     return rows * (d + 4) + kKeys * (d + 4 > v ? d + 4 : v) + kKeys * (rows + 4);
 }
 
-template <int RPT, int VD>
+template <int RPW, int VD>
 __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
-    constexpr int BQ = 16 * RPT;
-    constexpr int kVec = VD / 64;                        // groups of four output columns of a thread
+    constexpr int BQ = 8 * RPW, kLdP = BQ + 4;
+    constexpr int kVec = VD / 128;                       // groups of four output columns of a lane
     extern __shared__ __align__(16) float smem[];
     const int d = a.nope + a.rope, ld = d + 4;
     float* Qs = smem;
     float* Ks = Qs + BQ * ld;
     float* Vs = Ks;
-    float* Ps = Ks + kKeys * (ld > VD ? ld : VD);        // [key][query], rows of BQ + 4
+    float* Ps = Ks + kKeys * (ld > VD ? ld : VD);        // [key][query], rows of kLdP
 
     const int h = (int)(blockIdx.x % a.heads);
     const int split = (int)(blockIdx.x / a.heads % a.n_split);
-    const int64_t slot = blockIdx.x / a.heads / a.n_split;
+    // a sequence's longest tiles first
+    const int64_t slot = gridDim.x / a.heads / a.n_split - 1 - blockIdx.x / a.heads / a.n_split;
     pdl_wait();
     pdl_trigger();
     ExpandedTile t;
@@ -61,123 +65,173 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     const float* kn = static_cast<const float*>(a.k_nope);
     const float* rows = static_cast<const float*>(a.rows);
     const float* v = static_cast<const float*>(a.v);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;   // a warp's queries: warp + 8 r
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = tid; i < BQ * d / 4; i += 256) {
-        const int r = i / (d / 4), c = i % (d / 4) * 4;
-        store4(Qs + r * ld + c, r < t.n_q ? load4(q + ((t.q0 + r) * a.heads + h) * d + c) : zero);
-    }
-    float o[RPT][kVec][4] = {};
-    float m[RPT], l[RPT];
+    // a warp copies every eighth row; its loads are all in flight before the first store
+    // (one after the other they were 14,000 cycles a tile)
+    for (int r0 = warp; r0 < BQ; r0 += 32) {
+        float4 x[4][2];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * u, c = e * 128 + lane * 4;
+                x[u][e] = r < t.n_q && c < d ? load4(q + ((t.q0 + r) * a.heads + h) * d + c) : zero;
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (r0 + 8 * u < BQ && e * 128 + lane * 4 < d) store4(Qs + (r0 + 8 * u) * ld + e * 128 + lane * 4, x[u][e]);
+    }
+    float2 o[RPW][kVec][2] = {};
+    float m[RPW], l[RPW];                                // l: of this lane's keys
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
     const float scale = a.scale * kLog2e;
     const int64_t last = t.first + t.n_q - 1;            // rows that the tile's last query sees
 
     for (int kt = t.kt0; kt < t.kt1; ++kt) {
         const int64_t j0 = (int64_t)kt * kKeys;
         __syncthreads();
-        for (int i = tid; i < kKeys * d / 4; i += 256) {
-            const int j = i / (d / 4), c = i % (d / 4) * 4;
-            const int64_t row = t.row0 + j0 + j;
-            float4 x = zero;
-            if (j0 + j < last)
-                x = c < a.nope ? load4(kn + (row * a.heads + h) * a.nope + c)
-                               : load4(rows + row * a.width + a.kv_lora + c - a.nope);
-            store4(Ks + j * ld + c, x);
+        {
+            float4 x[4][2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = warp + 8 * u, c = e * 128 + lane * 4;
+                    const int64_t row = t.row0 + j0 + j;
+                    x[u][e] = j0 + j >= last || c >= d ? zero
+                              : c < a.nope             ? load4(kn + (row * a.heads + h) * a.nope + c)
+                                                       : load4(rows + row * a.width + a.kv_lora + c - a.nope);
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (e * 128 + lane * 4 < d) store4(Ks + (warp + 8 * u) * ld + e * 128 + lane * 4, x[u][e]);
         }
         __syncthreads();
-        float s[RPT][2] = {};
-#pragma unroll 4
-        for (int c = 0; c < d; c += 4) {
-            const float4 k0 = load4(Ks + tx * ld + c), k1 = load4(Ks + (tx + 16) * ld + c);
+        const int quarter = lane >> 3, k8 = lane & 7;
+        float s[RPW][4] = {};                            // of keys k8 + 8 k
+#pragma unroll 1
+        for (int c = quarter * 4; c < d; c += 16) {
+            float4 k[4];
 #pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const float4 x = load4(Qs + (ty * RPT + r) * ld + c);
-                s[r][0] = fmaf(x.x, k0.x, fmaf(x.y, k0.y, fmaf(x.z, k0.z, fmaf(x.w, k0.w, s[r][0]))));
-                s[r][1] = fmaf(x.x, k1.x, fmaf(x.y, k1.y, fmaf(x.z, k1.z, fmaf(x.w, k1.w, s[r][1]))));
+            for (int e = 0; e < 4; ++e) k[e] = load4(Ks + (k8 + 8 * e) * ld + c);
+#pragma unroll
+            for (int r = 0; r < RPW; ++r) {
+                const float4 x = load4(Qs + (warp + 8 * r) * ld + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[r][e] = fmaf(x.x, k[e].x, fmaf(x.y, k[e].y, fmaf(x.z, k[e].z, fmaf(x.w, k[e].w, s[r][e]))));
             }
         }
+        // the quarters' sums: a lane gives away those of the keys that it does not keep,
+        // and keeps key k8 + 8 quarter = lane
+        float p[RPW];
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) {
-            const int64_t sees = t.first + ty * RPT + r;
-            const float s0 = j0 + tx < sees ? s[r][0] * scale : -INFINITY;
-            const float s1 = j0 + tx + 16 < sees ? s[r][1] * scale : -INFINITY;
-            float top = fmaxf(s0, s1);
+        for (int r = 0; r < RPW; ++r) {
+            const bool hi = (quarter & 2) != 0, odd = (quarter & 1) != 0;
+            const float a0 = (hi ? s[r][2] : s[r][0]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][0] : s[r][2], 16);
+            const float a1 = (hi ? s[r][3] : s[r][1]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][1] : s[r][3], 16);
+            const float dot = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+            const float z = j0 + lane < t.first + warp + 8 * r ? dot * scale : -INFINITY;
+            float top = z;
 #pragma unroll
-            for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const float mn = fmaxf(m[r], top);
             const float base = mn == -INFINITY ? 0.f : mn;   // nothing to see so far
             const float f = exp2f(m[r] - base);
-            const float p0 = exp2f(s0 - base), p1 = exp2f(s1 - base);
-            float sum = p0 + p1;
-#pragma unroll
-            for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            l[r] = l[r] * f + sum;
+            p[r] = exp2f(z - base);
+            l[r] = l[r] * f + p[r];
             m[r] = mn;
+            const float2 f2 = make_float2(f, f);
 #pragma unroll
-            for (int c = 0; c < kVec; ++c)
+            for (int c = 0; c < kVec; ++c) {
+                o[r][c][0] = mul_x2(o[r][c][0], f2);
+                o[r][c][1] = mul_x2(o[r][c][1], f2);
+            }
+        }
+        if constexpr (RPW == 8) {
+            store4(Ps + lane * kLdP + warp * RPW, make_float4(p[0], p[1], p[2], p[3]));
+            store4(Ps + lane * kLdP + warp * RPW + 4, make_float4(p[4], p[5], p[6], p[7]));
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
-            Ps[tx * (BQ + 4) + ty * RPT + r] = p0;
-            Ps[(tx + 16) * (BQ + 4) + ty * RPT + r] = p1;
+            for (int r = 0; r < RPW; ++r) Ps[lane * kLdP + warp * RPW + r] = p[r];
         }
-        __syncthreads();                                 // the keys are read
-        for (int i = tid; i < kKeys * VD / 4; i += 256) {
-            const int j = i / (VD / 4), c = i % (VD / 4) * 4;
-            store4(Vs + j * VD + c, j0 + j < last ? load4(v + ((t.row0 + j0 + j) * a.heads + h) * VD + c) : zero);
+        __syncthreads();                                 // the keys are read, the warp's weights written
+        float4 odd = zero;                               // NaN if a value is no number
+        {
+            float4 x[4][kVec];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const int64_t j = j0 + warp + 8 * u;
+                    x[u][e] = j < last ? load4(v + ((t.row0 + j) * a.heads + h) * VD + e * 128 + lane * 4) : zero;
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float4 y = x[u][e];
+                    store4(Vs + (warp + 8 * u) * VD + e * 128 + lane * 4, y);
+                    odd.x = fmaf(y.x, 0.f, odd.x); odd.y = fmaf(y.y, 0.f, odd.y);
+                    odd.z = fmaf(y.z, 0.f, odd.z); odd.w = fmaf(y.w, 0.f, odd.w);
+                }
         }
-        __syncthreads();
-        const bool all = j0 + kKeys <= t.first;          // every query sees every key of the tile
+        // 0 times infinity is NaN: where some query does not see a key of the tile and a
+        // value is no number, each weight is looked at
+        const bool careful = __syncthreads_or((odd.x + odd.y) + (odd.z + odd.w) != 0.f) && j0 + kKeys > t.first;
         auto values = [&](int j, bool checked) {
-            float p[RPT];
-            if constexpr (RPT == 4) {
-                const float4 x = load4(Ps + j * (BQ + 4) + ty * 4);
-                p[0] = x.x; p[1] = x.y; p[2] = x.z; p[3] = x.w;
+            float w[RPW];
+            if constexpr (RPW == 8) {
+                const float4 x = load4(Ps + j * kLdP + warp * RPW), y = load4(Ps + j * kLdP + warp * RPW + 4);
+                w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
             } else {
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) p[r] = Ps[j * (BQ + 4) + ty * RPT + r];
+                for (int r = 0; r < RPW; ++r) w[r] = Ps[j * kLdP + warp * RPW + r];
             }
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                const float4 x = load4(Vs + j * VD + (c * 16 + tx) * 4);
+                const float4 x = load4(Vs + j * VD + (c * 32 + lane) * 4);
 #pragma unroll
-                for (int r = 0; r < RPT; ++r) {
-                    // a hidden value may be anything: 0 times infinity is NaN
-                    if (checked && j0 + j >= t.first + ty * RPT + r) continue;
-                    fma2(o[r][c][0], o[r][c][1], p[r], p[r], x.x, x.y);
-                    fma2(o[r][c][2], o[r][c][3], p[r], p[r], x.z, x.w);
+                for (int r = 0; r < RPW; ++r) {
+                    if (checked && j0 + j >= t.first + warp + 8 * r) continue;
+                    const float2 w2 = make_float2(w[r], w[r]);
+                    o[r][c][0] = fma_x2(w2, make_float2(x.x, x.y), o[r][c][0]);
+                    o[r][c][1] = fma_x2(w2, make_float2(x.z, x.w), o[r][c][1]);
                 }
             }
         };
-        if (all) {
+        if (!careful) {
 #pragma unroll 4
             for (int j = 0; j < kKeys; ++j) values(j, false);
         } else {
+#pragma unroll 1
             for (int j = 0; j < kKeys; ++j) values(j, true);
         }
     }
 #pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-        const int i = ty * RPT + r;
-        if (i >= t.n_q) continue;
-        const int64_t qh = (t.q0 + i) * a.heads + h;
-        if (a.n_split > 1) {
-            float* po = a.part_o + (qh * a.n_split + split) * VD;
+    for (int r = 0; r < RPW; ++r) {
+        float sum = l[r];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c)
-                store4(po + (c * 16 + tx) * 4, make_float4(o[r][c][0], o[r][c][1], o[r][c][2], o[r][c][3]));
-            if (tx == 0)
-                *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + split) * 2) = make_float2(m[r], l[r]);
-        } else {
-            float* out = static_cast<float*>(a.out) + qh * VD;
-            const float inv = 1.f / l[r];
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (warp + 8 * r >= t.n_q) continue;
+        const int64_t qh = (t.q0 + warp + 8 * r) * a.heads + h;
+        const bool parts = a.n_split > 1;
+        float* out = parts ? a.part_o + (qh * a.n_split + split) * VD : static_cast<float*>(a.out) + qh * VD;
+        const float f = parts ? 1.f : 1.f / sum;
 #pragma unroll
-            for (int c = 0; c < kVec; ++c)
-                store4(out + (c * 16 + tx) * 4, make_float4(o[r][c][0] * inv, o[r][c][1] * inv,
-                                                            o[r][c][2] * inv, o[r][c][3] * inv));
-            if (tx == 0 && a.lse != nullptr) a.lse[qh] = expanded_lse(m[r], l[r]);
-        }
+        for (int c = 0; c < kVec; ++c)
+            store4(out + (c * 32 + lane) * 4, make_float4(o[r][c][0].x * f, o[r][c][0].y * f, o[r][c][1].x * f,
+                                                          o[r][c][1].y * f));
+        if (lane != 0) continue;
+        if (parts) *reinterpret_cast<float2*>(a.part_ml + (qh * a.n_split + split) * 2) = make_float2(m[r], sum);
+        else if (a.lse != nullptr) a.lse[qh] = expanded_lse(m[r], sum);
     }
 }
 
@@ -215,19 +269,19 @@ __global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int6
     if (lane == 0 && a.lse != nullptr) a.lse[qh] = expanded_lse(top, l);
 }
 
-template <int RPT, int VD>
+template <int RPW, int VD>
 cudaError_t launch_tiles(const ExpandedArgs& a, cudaStream_t st) {
-    auto kern = expanded_simt<RPT, VD>;
-    const int bytes = simt_smem_floats(16 * RPT, a.nope + a.rope, VD) * 4;
+    auto kern = expanded_simt<RPW, VD>;
+    const int bytes = simt_smem_floats(8 * RPW, a.nope + a.rope, VD) * 4;
     cudaError_t e = ensure_dyn_smem((const void*)kern, bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = expanded_slots(a.b.n_q, a.b.n_seq, 16 * RPT) * a.heads * a.n_split;
+    const int64_t grid = expanded_slots(a.b.n_q, a.b.n_seq, 8 * RPW) * a.heads * a.n_split;
     return launch_pdl(kern, dim3((unsigned)grid), dim3(256), (size_t)bytes, st, a);
 }
 
 template <int VD>
 cudaError_t launch_simt(const ExpandedArgs& a, bool few, cudaStream_t st) {
-    cudaError_t e = few ? launch_tiles<1, VD>(a, st) : launch_tiles<4, VD>(a, st);
+    cudaError_t e = few ? launch_tiles<2, VD>(a, st) : launch_tiles<8, VD>(a, st);
     if (e != cudaSuccess || a.n_split == 1) return e;
     const int64_t n = (int64_t)a.b.n_q * a.heads;
     return launch_pdl(expanded_merge<VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
