@@ -651,8 +651,8 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, int32_t dtype, int64_t n_tok, int
         const bool inner = heads == 1 || out_head >= d, outer = n_tok == 1 || out_tok >= d;
         if (!inner || !outer) return DSA_ERR_INVALID_ARG;
         if (heads > 1 && n_tok > 1) {
-            const bool tok_outer = out_tok >= (heads - 1) * out_head + d;
-            const bool head_outer = out_head / d >= n_tok || out_head >= (n_tok - 1) * out_tok + d;
+            const bool tok_outer = (__int128)out_tok >= (__int128)(heads - 1) * out_head + d;
+            const bool head_outer = (__int128)out_head >= (__int128)(n_tok - 1) * out_tok + d;
             if (!tok_outer && !head_outer) return DSA_ERR_INVALID_ARG;
         }
         if (x == out && ((n_tok > 1 && x_tok != out_tok) || (heads > 1 && x_head != out_head)))

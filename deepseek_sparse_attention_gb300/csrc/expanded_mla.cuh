@@ -28,12 +28,18 @@ struct ExpandedTile {
     int32_t kt0, kt1;              // key tiles of the split
 };
 
-// Tiles have slots: sequence s has the slots from q_off[s] / bq + s on, which is
-// room for its ceil(q_len / bq) tiles whatever the others' lengths are, so a slot
-// finds its sequence by a search over the offsets and nothing is planned ahead.
-// Slots left over have no tile.
+// Tiles have slots: sequence s has the slots from start(s) = q_off[s] / bq + min(s,
+// q_off[s]) on, up to start(s + 1).  That is room for its ceil(q_len / bq) tiles:
+// where q_len > 0 the first term grows by q_len / bq rounded down at least and the
+// second by one at least.  So a slot finds its sequence by a search over the offsets,
+// nothing is planned ahead, and idle sequences, of which a batch may have many, add no
+// slots beyond the queries' number.  Slots left over have no tile.
 __host__ __device__ inline int64_t expanded_slots(int64_t n_q, int64_t n_seq, int bq) {
-    return n_q / bq + n_seq;
+    return n_q / bq + (n_seq < n_q ? n_seq : n_q);
+}
+__device__ __forceinline__ int64_t expanded_start(const BatchDev& b, int32_t s, int bq) {
+    const int64_t q = b.q_off[s];
+    return q / bq + (s < q ? s : q);
 }
 
 // False if the slot has no tile, or its sequence's offsets break the host's
@@ -44,10 +50,10 @@ __device__ __forceinline__ bool expanded_tile(const BatchDev& b, int64_t slot, i
     int32_t lo = 0, hi = b.n_seq - 1;
     while (lo < hi) {                                    // last s whose slots start at or before this one
         const int32_t mid = lo + (hi - lo + 1) / 2;
-        if (b.q_off[mid] / bq + mid <= slot) lo = mid; else hi = mid - 1;
+        if (expanded_start(b, mid, bq) <= slot) lo = mid; else hi = mid - 1;
     }
     const int64_t q0 = b.q_off[lo], q1 = b.q_off[lo + 1], r0 = b.row_off[lo], r1 = b.row_off[lo + 1];
-    const int64_t at = slot - (q0 / bq + lo);
+    const int64_t at = slot - (q0 / bq + (lo < q0 ? lo : q0));
     if (slot == 0 && (b.q_off[0] != 0 || b.q_off[b.n_seq] != b.n_q))
         record_error(err, kDevBadBatch, b.n_seq, where);
     if (q0 < 0 || q1 < q0 || q1 > b.n_q || q1 - q0 > b.max_q_len || r0 < 0 || r1 > b.total_rows ||

@@ -74,6 +74,9 @@ def check(q_lens, kv_lens, q, k, cache, v, out, lse, heads=(0, 1, 37, 63)):
     bf16 = q.dtype == torch.bfloat16
     q0 = r0 = 0
     for nq, nk in zip(q_lens, kv_lens):
+        if nq == 0:                                        # an idle sequence
+            r0 += nk
+            continue
         hidden = torch.ones((nq, nk), dtype=torch.bool, device="cuda").triu(nk - nq + 1)
         for h in heads:
             qh = q[q0:q0 + nq, h].double()
@@ -104,6 +107,8 @@ BATCHES = {
     "decode": ([1] * 9, [1, 31, 32, 33, 127, 128, 129, 500, 64]),
     "long_split": ([3], [5003]),
     "few_of_many": ([16, 1, 2], [300, 2000, 2]),
+    "idle": ([0, 0, 1, 0, 300, 0, 0, 0, 1, 0], [0, 9, 700, 0, 300, 64, 0, 0, 65, 0]),
+    "many_tiles": ([1000, 513], [1000, 1500]),
 }
 
 
@@ -240,6 +245,31 @@ def test_attention_of_bad_offsets(row_off, q_off, dtype):
     assert dsa.dsa_check_device_error(ws) == 2
     if row_off[:2] == [0, 50] and q_off[:2] == [0, 10]:
         check([10], [50], x[0][:10], *x[1:], out, None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_follows_and_precedes_other_kernels(dtype):
+    """Inputs written by the kernels just before and outputs read by those just after, over and
+    over, on a stream of its own."""
+    q_lens, kv_lens = [3, 60], [400, 300]
+    x = make_inputs(q_lens, kv_lens, 192, 64, 256, dtype, seed=40)
+    sh, b = dsa.make_shape(dtype=dtype, scale=SCALE), make_batch(q_lens, kv_lens)
+    ws, want = workspace(sh, b), attend(q_lens, kv_lens, *x, dtype)[0]
+    now = [torch.zeros_like(t) for t in x]
+    out = torch.empty_like(want)
+    stream, kept = torch.cuda.Stream(), []
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(5):
+            for t, src in zip(now, x):
+                t.copy_(src)
+            dsa.dsa_expanded_mla_attn(sh, b, *now, out, None, ws)
+            kept.append(out.clone())
+            for t in now:
+                t.zero_()
+            out.zero_()
+    stream.synchronize()
+    assert all(torch.equal(k, want) for k in kept) and dsa.dsa_check_device_error(ws) == 0
 
 
 def test_attention_in_captured_graphs_on_two_streams():

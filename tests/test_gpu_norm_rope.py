@@ -124,6 +124,24 @@ def test_norm_writes_over_its_inputs(width):
     check_norm(x, add, x0, add0, None, 1e-5)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,width", [(6001, 512), (6001, 1000), (2503, 2048), (1300, 4096), (701, 8192), (400, 16384)])
+def test_norm_of_more_rows_than_a_wave(rows, width, dtype):
+    """Rows one after the other in a CTA, over the inputs themselves, and with codes."""
+    g = _gen(rows)
+    x = torch.randn((rows, width), generator=g, device="cuda").to(T[dtype])
+    add = torch.randn((rows, width), generator=g, device="cuda").to(T[dtype])
+    w = torch.randn(width, generator=g, device="cuda")
+    codes = torch.empty((rows, width), dtype=torch.uint8, device="cuda")
+    for group in (0, 128):
+        scales = torch.empty((rows, -(-width // (group or width))), device="cuda")
+        dsa.dsa_rms_norm(x, w, 1e-5, codes, add=add, scales=scales, group=group)
+        check_codes(codes, scales, norm_formula(x, add, w, 1e-5)[1], group)
+    x0, add0 = x.clone(), add.clone()
+    dsa.dsa_rms_norm(x, w, 1e-5, x, add=add, total=add)
+    check_norm(x, add, x0, add0, w, 1e-5)
+
+
 @pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-22, 1e-12, 1e12, 1e19, 1e25, 1e37])
 @pytest.mark.parametrize("width,eps", [(64, 1e-5), (64, 1e-30), (3000, 1e-30), (3000, 1e-38), (9000, 1e-5)])
 def test_norm_over_float32s_range(size, width, eps):

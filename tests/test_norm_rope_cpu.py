@@ -2,6 +2,7 @@
 and the rope's rates.  CPU only: every refusal comes before anything is enqueued."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -92,7 +93,8 @@ def _rope(lib, plan=None, **kw):
 @pytest.mark.parametrize("change,code", [
     (dict(dtype=5), 1), (dict(n_tok=-1), 1), (dict(heads=-1), 1), (dict(x=None), 1), (dict(pos=None), 1), (dict(out=None), 1),
     (dict(x=OFF), 1), (dict(out=OFF), 1), (dict(pos=OFF), 1), (dict(out_head=63), 1), (dict(out_tok=0), 1),
-    (dict(out_tok=200), 1), (dict(x_tok=-300), 1), (dict(out=A, out_tok=400), 1), (dict(out=A, out_head=64), 1),
+    (dict(out_tok=200), 1), (dict(out_tok=1000, out_head=256, heads=65), 1), (dict(out_tok=1 << 62, out_head=1 << 62), 1),
+    (dict(x_tok=-300), 1), (dict(out=A, out_tok=400), 1), (dict(out=A, out_head=64), 1),
     (dict(n_tok=1 << 31), 2), (dict(heads=65537, out_tok=65537 * 100), 2),
     (dict(n_tok=0, x=None, out=None, pos=None), 0), (dict(heads=0, x=None, out=None, pos=None), 0),
 ])
@@ -164,6 +166,31 @@ def test_attention_workspace_grows_with_the_batch():
         assert n == sorted(n) and n[0] >= 0 and n[-1] >= last
         last = n[-1]
     assert last < 256 << 20
+
+
+@pytest.mark.parametrize("bq", [16, 64, 256])
+def test_slots_hold_every_tile(bq):
+    """The rule that finds a tile's sequence from its slot, for batches with idle sequences: every
+    sequence's tiles have slots of their own within the bound, and the search finds them."""
+    rng = random.Random(bq)
+    for _ in range(300):
+        n = rng.choice([1, 2, 7, 60])
+        lens = [rng.choice([0, 0, 1, bq - 1, bq, bq + 1, rng.randrange(3 * bq)]) for _ in range(n)]
+        off = [0]
+        for x in lens:
+            off.append(off[-1] + x)
+        start = [q // bq + min(s, q) for s, q in enumerate(off)]
+        slots = off[-1] // bq + min(n, off[-1])
+        found = set()
+        for slot in range(slots):
+            lo, hi = 0, n - 1
+            while lo < hi:
+                mid = lo + (hi - lo + 1) // 2
+                lo, hi = (mid, hi) if start[mid] <= slot else (lo, mid - 1)
+            at = slot - start[lo]
+            if 0 <= at and at * bq < lens[lo]:
+                found.add((lo, at))
+        assert found == {(s, t) for s, x in enumerate(lens) for t in range(-(-x // bq))}
 
 
 def test_binding_refuses():
