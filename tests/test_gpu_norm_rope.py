@@ -10,8 +10,8 @@ Bars, from the arithmetic (u = 2^-24, float32's half step):
   normal numbers (2^-6 of the scale); a scale is within 42 u.
 * rope: the turns are cut at 2^-32 and rounded to float32 within 2^-24 of half a
   turn (1.9e-7 in radians), the rate is within 2^-53 of itself; sine and cosine are within two
-  units in the last place (2.4e-7), the magnitude rounds once and the products and their sum three
-  times (2.4e-7): 8e-7 + 2^-52 pos rate of |a| + |b|, times the magnitude.
+  units in the last place (2.4e-7; bf16: 2^-21.4 = 3.6e-7), the magnitude rounds once and the products and
+  their sum three times (2.4e-7): 8e-7 + 2^-52 pos rate of |a| + |b|, times the magnitude.
 """
 import math
 
