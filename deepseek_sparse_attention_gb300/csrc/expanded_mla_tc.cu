@@ -23,9 +23,12 @@
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
 //              epilogue to the queries that see them;
-//   warps 12-15 epilogue: a unit's O to the output, a row to a thread in whole sectors, beside the next unit's first scores.  (Through shared
-//              memory to whole lines it took 10 to 20% longer over short units: the
-//              products leave its bandwidth to no one.)
+//   warps 12-15 epilogue: a unit's O to the output beside the next unit's first scores, a
+//              row to a thread, 64 columns of a warp's rows at a time through shared memory
+//              and a TMA store; straight from registers in whole sectors where a
+//              sequence ends among the warp's rows.  (From registers always: 64 prompts of 200
+//              tokens 260 us instead of 242, the stores of 32 rows each keep the softmax
+//              out of the load-store unit.)
 // A key tile takes 2,050 cycles (head width and v_dim 256), which are the products' own: S
 // and O of 1,024 each.  What it took before: a unit's launch to itself, with its start, its
 // output and nothing beside them, 11,000 cycles; copies and products handed over in eight
@@ -57,7 +60,8 @@ constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 constexpr int kCleaners = 64;
 constexpr uint32_t kOCol = 256, kTmemCols = 512;         // S0, S1 at 0 and 128
 constexpr uint32_t kSmem = 227 * 1024;
-constexpr uint32_t kBarBytes = 6144;
+constexpr uint32_t kBarBytes = 5120;
+constexpr uint32_t kStage = 32 * 128;                    // 64 columns of an epilogue warp's rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                            // weights stay below 2^8
 
@@ -133,7 +137,7 @@ template <int VD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v,
-            const ExpandedArgs a, const int32_t slots, const int32_t ring) {
+            const __grid_constant__ CUtensorMap tm_o, const ExpandedArgs a, const int32_t slots, const int32_t ring) {
     constexpr uint32_t kVBlock = kK * 128;               // 64 columns of a tile's values
     constexpr uint32_t kVBytes = VD / 128 * kVBlock;     // a CTA's half of them
     extern __shared__ uint8_t smem_raw[];
@@ -561,6 +565,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     } else {                                                       // ---- epilogue
         const int r = threadIdx.x & 127, row = (int)rank * kRows + r;
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint8_t* stage = Rs + ring * unit_bytes + (warp & 3) * kStage;
         int32_t busy = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
@@ -600,26 +605,46 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tmem_st_32cols(lane_addr + kOCol + c, o);
                 }
             }
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + qh * VD;
             const float inv = 1.f / l;
-#pragma unroll 2
-            for (int c = 0; c < VD; c += 32) {
-                float o[32];
-                tmem_ld_32cols(lane_addr + kOCol + c, o);
-                if (!mine) continue;
+            const int r0 = (int)rank * kRows + (warp & 3) * 32;    // the warp's first query
+            const bool whole = r0 + 32 <= w.n_q;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + qh * VD;
+#pragma unroll 1
+            for (int c = 0; c < VD; c += 64) {
+                uint32_t x[32];
+                {
+                    float o[2][32];
+                    tmem_ld_32cols_x2(lane_addr + kOCol + c, lane_addr + kOCol + c + 32, o[0], o[1]);
 #pragma unroll
-                for (int e = 0; e < 32; e += 16) {
-                    uint32_t x[8];
+                    for (int e = 0; e < 32; ++e)
+                        x[e] = pack(o[e >> 4][(e & 15) * 2] * inv, o[e >> 4][(e & 15) * 2 + 1] * inv);
+                }
+                if (c + 64 == VD) {                                // O may be written again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
+                }
+                if (whole) {
+                    if (lane == 0) tma_store_wait_read<0>();       // the piece before has left
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = pack(o[e + 2 * i] * inv, o[e + 2 * i + 1] * inv);
-                    store_sector(out + c + e, x);
+                    for (int e = 0; e < 8; ++e)                    // the map's 128-byte swizzle
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&tm_o, stage, c, w.h, (int32_t)(w.q0 + r0));
+                        tma_store_commit();
+                    }
+                } else if (mine) {                                 // the rows behind are another sequence's
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) store_sector(out + c + e * 16, &x[8 * e]);
                 }
             }
-            tc_fence_before();                                     // O may be written again
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&s.o_free, 0));
             if (mine && a.lse != nullptr) a.lse[qh] = expanded_lse(m, l);
         }
+        if (lane == 0) tma_store_wait<0>();
         if (!ok) {
             if (lane == 0) record_error(a.err, kDevTimeout, blockIdx.x, 66);
             *abort = 1;
@@ -639,14 +664,15 @@ template <int VD>
 cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     const uint64_t rows = (uint64_t)a.b.total_rows, heads = (uint64_t)a.heads;
     const uint64_t d = (uint64_t)(a.nope + a.rope);
-    CUtensorMap tq, tk, tr, tv;
+    CUtensorMap tq, tk, tr, tv, to;
     auto heads_map = [&](CUtensorMap* m, const void* base, uint64_t width, uint64_t n, uint32_t box) {
         const uint64_t dims[3] = {width, heads, n}, strides[2] = {width * 2, heads * width * 2};
         const uint32_t b[3] = {64, 1, box};
         return encode_bf16_map(m, base, 3, dims, strides, b);
     };
     if (!heads_map(&tq, a.q, d, (uint64_t)a.b.n_q, kRows) ||
-        !heads_map(&tk, a.k_nope, (uint64_t)a.nope, rows, kK / 2) || !heads_map(&tv, a.v, VD, rows, kK))
+        !heads_map(&tk, a.k_nope, (uint64_t)a.nope, rows, kK / 2) || !heads_map(&tv, a.v, VD, rows, kK) ||
+        !heads_map(&to, a.out, VD, (uint64_t)a.b.n_q, 32))
         return cudaErrorInvalidValue;
     tr = tk;
     if (a.rope > 0) {
@@ -658,11 +684,11 @@ cudaError_t launch(const ExpandedArgs& a, cudaStream_t st) {
     cudaError_t e = ensure_dyn_smem((const void*)kern, (int)kSmem);
     if (e != cudaSuccess) return e;
     const int nk = (int)(d / 64);
-    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock) / unit_size(nk, VD));
+    int ring = (int)((kSmem - 1024 - kBarBytes - nk * kQBlock - 4 * kStage) / unit_size(nk, VD));
     if (ring > kMaxRing) ring = kMaxRing;
     const int64_t slots = expanded_slots(a.b.n_q, a.b.n_seq, kQ);
     return launch_pdl(kern, dim3((unsigned)(2 * slots * a.heads)), dim3(kThreads), kSmem, st, tq, tk, tr,
-                      tv, a, (int32_t)slots, (int32_t)ring);
+                      tv, to, a, (int32_t)slots, (int32_t)ring);
 }
 
 }  // namespace

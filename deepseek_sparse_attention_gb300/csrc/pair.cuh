@@ -15,7 +15,7 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 
 // 32 bytes to a 32-byte aligned address.
-__device__ __forceinline__ void store_sector(void* p, const uint32_t (&x)[8]) {
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* x) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
                  "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                  : "memory");
