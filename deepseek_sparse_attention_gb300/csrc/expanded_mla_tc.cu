@@ -4,8 +4,9 @@
 //   S = Q K^T (M = 256 queries, N = 128 keys, K = the head's width), one pass over
 //   the key tiles with a running maximum, O += P V (M = 256, N = v_dim, K = 128 keys)
 //
-// A unit of work is a tile of 256 queries of a sequence and a head; a pair of CTAs (cta_group::2) takes one after the other, each with 128 of the
-// queries, their S, P and O, and half of the keys' rows and of the values' columns to load.
+// A unit of work is a tile of 256 queries of a sequence and a head; a pair of CTAs
+// (cta_group::2) takes one after the other, each with 128 of the queries, their S, P and O, and
+// half of the keys' rows and of the values' columns to load.
 // The next unit is one whose launch the pair cancels (clusterlaunchcontrol), asked for a unit
 // ahead, so that its copies and first products run while the last one's output is written.
 // In each CTA
@@ -88,7 +89,10 @@ struct Shared {
     Work work[kWorks];
     float l[2][kSoftmax], m[2][kRows];                   // a unit's sums of halves, and its maxima
     uint32_t tmem;
-    int32_t abort, poison[2];                            // poison: the last unit that met odd values
+    int32_t abort;
+    // the last unit that met odd values, by its number: the cleaners may be two units ahead of
+    // the epilogue (their queries' place is free once a unit's scores are issued), not three
+    int32_t poison[4];
 };
 static_assert(sizeof(Shared) <= kBarBytes, "barriers");
 
@@ -164,8 +168,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_init(&s.p_full[i], 2 * kSoftmax / 32);
             mbar_init(&s.next_full[i], 1);
             mbar_init(&s.next_free[i], 1);
-            s.poison[i] = 0;
         }
+        for (int i = 0; i < 4; ++i) s.poison[i] = 0;
         for (int i = 0; i < kWorks; ++i) {
             mbar_init(&s.work_full[i], 1);
             // the softmax's, the cleaners' and the epilogue's warps, and the products' thread
@@ -452,8 +456,8 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         p[(e0 + e) * kCleaners] = make_uint4(clean(x[e].x), clean(x[e].y), clean(x[e].z), clean(x[e].w));
                 }
                 if (bad) {                                         // both CTAs give them back
-                    *(volatile int32_t*)&s.poison[busy & 1] = busy;
-                    st_cluster(cluster_addr(&s.poison[busy & 1], rank ^ 1), busy);
+                    *(volatile int32_t*)&s.poison[busy & 3] = busy;
+                    st_cluster(cluster_addr(&s.poison[busy & 3], rank ^ 1), busy);
                     fence_cluster();
                 }
                 fence_proxy_async_smem();
@@ -584,7 +588,7 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tc_fence_after();
             const float l = s.l[busy & 1][r] + s.l[busy & 1][r + 128], m = s.m[busy & 1][r];
             ++busy;
-            const bool poison = *(volatile int32_t*)&s.poison[busy & 1] == busy;
+            const bool poison = *(volatile int32_t*)&s.poison[busy & 3] == busy;
             if (poison) {                                          // what the cleaners took out and the row sees
                 const int64_t from = (int64_t)w.partial * kK, to = mine ? w.first + row : from;
 #pragma unroll 1

@@ -173,6 +173,31 @@ def test_attention_hidden_rows_may_hold_anything(where, bad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length,spare", [(100, 0), (40, 3), (200, 1)])
+def test_attention_of_many_sequences_with_a_bad_value_each(length, spare, dtype):
+    """Short units one after the other on each pair of CTAs, all of them with an infinity that
+    later queries see: none takes another's for its own, none loses it."""
+    n = 61
+    q_lens, kv_lens = [length] * n, [length + (i * spare) % 7 for i in range(n)]
+    q, k, cache, v = make_inputs(q_lens, kv_lens, 64, 64, 128, dtype, seed=7)
+    clean = attend(q_lens, kv_lens, q, k, cache, v, dtype)
+    bad = torch.zeros((n * length,), dtype=torch.bool, device="cuda")
+    for i in range(n):
+        at = (i * 13) % length                                  # the new row that is bad
+        v[sum(kv_lens[:i]) + kv_lens[i] - length + at, :, i] = math.inf
+        bad[i * length + at:(i + 1) * length] = True
+    column = torch.arange(n, device="cuda").repeat_interleave(length)
+    for _ in range(3):
+        out, lse = attend(q_lens, kv_lens, q, k, cache, v, dtype)
+        assert torch.equal(lse, clean[1])
+        hit = torch.zeros((n * length, 128), dtype=torch.bool, device="cuda")
+        hit[torch.arange(n * length, device="cuda"), column] = bad
+        hit = hit[:, None].expand(-1, HEADS, -1)
+        assert (out[hit].float() == math.inf).all()
+        assert torch.equal(out[~hit], clean[0][~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_of_infinite_queries(dtype):
     """A query of NaN or infinity is NaN by itself."""
     q, k, cache, v = make_inputs([140], [140], 192, 64, 256, dtype, seed=3)
