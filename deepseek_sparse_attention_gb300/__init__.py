@@ -552,8 +552,9 @@ def dsa_expanded_mla_attn(shape, batch, q, k_nope, cache, v, out, lse, ws, strea
     ``v`` [rows, heads, v_dim], the rope part of the keys in ``cache`` (see dsa.h)."""
     d, dt = torch.cuda.current_device(), _TORCH_DTYPE[shape.dtype]
     heads, rope, n_q, rows = shape.heads, shape.rope_dim, batch.n_q, batch.total_rows
-    if k_nope is None or v is None or k_nope.dim() != 3 or v.dim() != 3:
-        raise ValueError("k_nope and v are [rows, heads, columns]")
+    if k_nope is None or v is None or k_nope.dim() != 3 or v.dim() != 3 or \
+            k_nope.shape[1] != heads or v.shape[1] != heads:
+        raise ValueError(f"k_nope and v are [rows, {heads}, columns]")
     nope, v_dim = k_nope.shape[2], v.shape[2]
     _call("dsa_expanded_mla_attn", shape, batch, nope, v_dim,
           _at(q, dt, d, n_q * heads * (nope + rope), "q"),

@@ -610,6 +610,14 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
         !aligned(weight, 4) || !aligned(scales, 4))
         return DSA_ERR_INVALID_ARG;
     if (width > 16384 || n_rows >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+    // an output in an input's place has its rows where they are, and its type
+    auto apart = [&](const void* o, int64_t ld, const void* in, int64_t in_ld, bool same_type) {
+        return o == nullptr || o != in || (same_type && (n_rows < 2 || ld == in_ld));
+    };
+    if (!apart(out, out_ld, x, x_ld, !e4m3) || !apart(out, out_ld, add, add_ld, !e4m3) ||
+        !apart(total, total_ld, x, x_ld, true) || !apart(total, total_ld, add, add_ld, true) ||
+        !apart(out, out_ld, total, total_ld, false))
+        return DSA_ERR_INVALID_ARG;
     const NormArgs a{n_rows, x_ld, add_ld, total_ld, out_ld, x,     add, weight,
                      total,  out,  scales, width,    group,  eps,   (float)(1.0 / width)};
     return cuda_status(launch_rms_norm(a, dtype, e4m3, static_cast<cudaStream_t>(stream)), "rms_norm");

@@ -363,7 +363,8 @@ dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, c
  *          2^-126 and the group's largest |y| / 448; a code is y / scale rounded
  *          to nearest even, and stands for code * scale.  Not read otherwise,
  *          and group = 0.
- * out and total may be x or add themselves (same stride); no other overlap.
+ * total, and out in dtype, may be x or add themselves (same stride; refused with
+ * another); no other overlap.
  * Columns between a row's width and the next row are neither read nor written.
  * float32 arithmetic; sums of squares beyond float32's range are formed again of
  * scaled values, so that any finite h gives its norm.  A row with an infinity
@@ -461,7 +462,7 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  *       z_j = scale * (q_nope . k_nope[j, h] + q_rope . rope[j]),  j < L
  *       out = sum_j softmax(z)_j v[j, h],  lse = log sum_j exp(z_j)
  * Rows that a query does not see have no part in its result, whatever they hold.
- * A NaN or infinite logit, or attended logits of -inf alone, give NaN.
+ * A logit of NaN or +inf, or attended logits of -inf alone, give NaN.
  * float32 logits, maxima, sums and accumulation; bf16 operands give each
  * weight exp(z_j - m) to the value product rounded to bf16 (2^-8 of itself at most), the
  * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <

@@ -225,6 +225,22 @@ def test_attention_of_logits_at_minus_infinity(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_one_logit_at_minus_infinity(dtype):
+    """Among others it has the weight zero: the result is that of a key with a very low logit."""
+    q_lens, kv_lens = [150, 3], [170, 90]
+    q, k, cache, v = make_inputs(q_lens, kv_lens, 64, 64, 128, dtype, seed=12)
+    q[..., 5] = 2.0 ** 70
+    k[..., 5] = 0
+    for row in (9, 169, 171):
+        k[row, :, 5] = -1
+    low = attend(q_lens, kv_lens, q, k, cache, v, dtype)
+    for row in (9, 169, 171):
+        k[row, :, 5] = -2.0 ** 70
+    out, lse = attend(q_lens, kv_lens, q, k, cache, v, dtype)
+    assert torch.isfinite(lse).all() and torch.equal(lse, low[1]) and torch.equal(out, low[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("size", [30.0, 1000.0])
 def test_attention_of_large_logits(size, dtype):
     """Maxima that rise through the whole list, by up to thousands, and fall again."""
@@ -235,6 +251,14 @@ def test_attention_of_large_logits(size, dtype):
     q[:, 0::2, 0], q[:, 1::2, 0] = 16.0, -16.0
     out, lse = attend(q_lens, kv_lens, q, k, cache, v, dtype)
     check(q_lens, kv_lens, q, k, cache, v, out, lse, heads=(0, 1))
+
+
+def test_attention_refuses_keys_of_other_heads():
+    """Large enough, but not of the shape's 64 heads."""
+    q, k, cache, v = make_inputs([2], [8], 128, 64, 128, "bf16", seed=13)
+    for bad_k, bad_v in ((k.view(16, 32, 128), v), (k, v.view(4, 128, 128))):
+        with pytest.raises(ValueError, match="64"):
+            attend([2], [8], q, bad_k, cache, bad_v, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

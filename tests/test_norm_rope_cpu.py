@@ -40,6 +40,19 @@ def test_norm_refuses(lib, change, code):
     assert _norm(lib, **change) == code
 
 
+B, C, D = (ctypes.c_void_p(4096 * i) for i in (2, 3, 4))
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=A, out_ld=72), dict(out=B, out_ld=72), dict(total=A, total_ld=72), dict(total=B, total_ld=72),
+    dict(total=D), dict(total=D, n_rows=1),
+    dict(fmt=1, scales=A, out=A), dict(fmt=1, scales=A, out=B), dict(fmt=1, scales=A, out=C),
+    dict(fmt=1, scales=A, out=A, n_rows=1),
+])
+def test_norm_refuses_outputs_over_other_rows(lib, change):
+    assert _norm(lib, **{**dict(x=A, add=B, total=C, out=D), **change}) == 1
+
+
 def _init(lib, plan, **kw):
     d = dict(dims=64, layout=0, inverse=0, base=8e6, factor=1.0, original_len=0.0, beta_fast=32.0, beta_slow=1.0,
              magnitude=1.0)
