@@ -41,25 +41,16 @@ __host__ __device__ constexpr int simt_smem_floats(int rows, int d, int v) {
     return rows * (d + 4) + kKeys * (d + 4 > v ? d + 4 : v) + kKeys * (rows + 4);
 }
 
+// A tile of up to 8 RPW queries.
 template <int RPW, int VD>
-__global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
+__device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedTile& t, int h, int split, float* smem) {
     constexpr int BQ = 8 * RPW, kLdP = BQ + 4;
     constexpr int kVec = VD / 128;                       // groups of four output columns of a lane
-    extern __shared__ __align__(16) float smem[];
     const int d = a.nope + a.rope, ld = d + 4;
     float* Qs = smem;
     float* Ks = Qs + BQ * ld;
     float* Vs = Ks;
     float* Ps = Ks + kKeys * (ld > VD ? ld : VD);        // [key][query], rows of kLdP
-
-    const int h = (int)(blockIdx.x % a.heads);
-    const int split = (int)(blockIdx.x / a.heads % a.n_split);
-    // a sequence's longest tiles first
-    const int64_t slot = gridDim.x / a.heads / a.n_split - 1 - blockIdx.x / a.heads / a.n_split;
-    pdl_wait();
-    pdl_trigger();
-    ExpandedTile t;
-    if (!expanded_tile(a.b, slot, split, a.n_split, BQ, kKeys, a.err, 60, t)) return;
 
     const float* q = static_cast<const float*>(a.q);
     const float* kn = static_cast<const float*>(a.k_nope);
@@ -235,6 +226,24 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     }
 }
 
+// Tiles of 8 RPW queries, with fewer to a warp in one that has no more than a
+// quarter of them: it still takes most of a tile's loads, but a quarter of the
+// arithmetic (three prompts of 1, 129 and 257 queries: 177 us instead of 212).
+template <int RPW, int VD>
+__global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
+    extern __shared__ __align__(16) float smem[];
+    const int h = (int)(blockIdx.x % a.heads);
+    const int split = (int)(blockIdx.x / a.heads % a.n_split);
+    // a sequence's longest tiles first
+    const int64_t slot = gridDim.x / a.heads / a.n_split - 1 - blockIdx.x / a.heads / a.n_split;
+    pdl_wait();
+    pdl_trigger();
+    ExpandedTile t;
+    if (!expanded_tile(a.b, slot, split, a.n_split, 8 * RPW, kKeys, a.err, 60, t)) return;
+    if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
+    else simt_tile<RPW, VD>(a, t, h, split, smem);
+}
+
 // One warp per (query, head): the splits' sums weighted by their maxima.
 template <int VD>
 __global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int64_t n) {
@@ -280,15 +289,19 @@ cudaError_t launch_tiles(const ExpandedArgs& a, cudaStream_t st) {
 }
 
 template <int VD>
-cudaError_t launch_simt(const ExpandedArgs& a, bool few, cudaStream_t st) {
-    cudaError_t e = few ? launch_tiles<2, VD>(a, st) : launch_tiles<8, VD>(a, st);
+cudaError_t launch_simt(const ExpandedArgs& a, int bq, cudaStream_t st) {
+    cudaError_t e = bq == 16   ? launch_tiles<2, VD>(a, st)
+                    : bq == 32 ? launch_tiles<4, VD>(a, st)
+                               : launch_tiles<8, VD>(a, st);
     if (e != cudaSuccess || a.n_split == 1) return e;
     const int64_t n = (int64_t)a.b.n_q * a.heads;
     return launch_pdl(expanded_merge<VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
 }
 
-// Queries of a tile: 16 where no sequence has more, else 64.
-bool few_queries(const BatchDev& b) { return b.max_q_len <= 16; }
+// Queries of a tile: 16 or 32 where no sequence has more, else 64 (two prompts of 1 and
+// 20 tokens behind 100 and 0 rows: 18.5 us with 32, 23.1 with 64; eight of up to 32
+// behind up to 1,000: 270 and 375).
+int tile_queries(const BatchDev& b) { return b.max_q_len <= 16 ? 16 : b.max_q_len <= 32 ? 32 : kMaxTileQ; }
 
 }  // namespace
 
@@ -296,7 +309,7 @@ bool few_queries(const BatchDev& b) { return b.max_q_len <= 16; }
 // its longest split and a split's partial sums as one more tile.
 int32_t plan_expanded_splits(const Shape& sh, const BatchDev& b) {
     if (b.n_q < 1 || sh.dtype == DSA_BF16) return 1;
-    const int64_t units = expanded_slots(b.n_q, b.n_seq, few_queries(b) ? 16 : 64) * sh.heads;
+    const int64_t units = expanded_slots(b.n_q, b.n_seq, tile_queries(b)) * sh.heads;
     const int64_t wave = 2 * sm_count(), tiles = (b.max_kv_len + kKeys - 1) / kKeys;
     int32_t best = 1;
     int64_t least = INT64_MAX;
@@ -329,8 +342,8 @@ cudaError_t launch_expanded_mla(const Shape& sh, const BatchDev& b, int32_t nope
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + (size_t)b.n_q * sh.heads * a.n_split * v_dim;
     if (sh.dtype == DSA_BF16) return launch_expanded_tc(a, st);
-    const bool few = few_queries(b);
-    return v_dim == 256 ? launch_simt<256>(a, few, st) : launch_simt<128>(a, few, st);
+    const int bq = tile_queries(b);
+    return v_dim == 256 ? launch_simt<256>(a, bq, st) : launch_simt<128>(a, bq, st);
 }
 
 }  // namespace dsa

@@ -131,6 +131,20 @@ def test_attention_head_widths(nope, rope, v_dim, dtype):
     check(q_lens, kv_lens, *x, out, lse)
 
 
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([17], [17]), ([32, 1], [40, 700]), ([20, 31, 2, 32], [500, 31, 2, 65]), ([33, 16], [33, 300]),
+    ([64, 65, 16, 80, 1], [64, 100, 16, 3000, 129]), ([25] * 3, [25, 5000, 64]),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_of_few_queries(q_lens, kv_lens, dtype):
+    """Tiles of 16, 32 and 64 queries and nearly empty ones, in a workspace for more queries."""
+    sh = dsa.make_shape(rope_dim=64, dtype=dtype, scale=SCALE)
+    ws = workspace(sh, make_batch(q_lens + [40], kv_lens + [40]))
+    q, k, cache, v = make_inputs(q_lens, kv_lens, 192, 64, 256, dtype, seed=14)
+    out, lse = attend(q_lens, kv_lens, q, k, cache, v, dtype, ws=ws)
+    check(q_lens, kv_lens, q, k, cache, v, out, lse)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_without_lse_and_past_its_sequences(dtype):
     """No lse, a cache with rows behind the last sequence, of NaN."""
