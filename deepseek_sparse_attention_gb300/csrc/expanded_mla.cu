@@ -46,6 +46,10 @@ template <int RPW, int VD>
 __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedTile& t, int h, int split, float* smem) {
     constexpr int BQ = 8 * RPW, kLdP = BQ + 4;
     constexpr int kVec = VD / 128;                       // groups of four output columns of a lane
+    // Few queries, bound by the loads: these are asked for a product ahead, and warps without
+    // a query do nothing else.  16 of them over up to 2,000 rows take 447 us, 4.1 TB/s; loads
+    // where they are used, and two queries to every warp, 968.
+    constexpr bool kAhead = RPW <= 2;
     const int d = a.nope + a.rope, ld = d + 4;
     float* Qs = smem;
     float* Ks = Qs + BQ * ld;
@@ -75,94 +79,103 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
             for (int e = 0; e < 2; ++e)
                 if (r0 + 8 * u < BQ && e * 128 + lane * 4 < d) store4(Qs + (r0 + 8 * u) * ld + e * 128 + lane * 4, x[u][e]);
     }
+    const bool busy = !kAhead || warp < t.n_q;
     float2 o[RPW][kVec][2] = {};
     float m[RPW], l[RPW];                                // l: of this lane's keys
 #pragma unroll
     for (int r = 0; r < RPW; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
     const float scale = a.scale * kLog2e;
     const int64_t last = t.first + t.n_q - 1;            // rows that the tile's last query sees
+    // this warp's rows of a tile's keys, or of its values
+    float4 x[4][2];
+    auto load_keys = [&](int64_t j0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = warp + 8 * u, c = e * 128 + lane * 4;
+                const int64_t row = t.row0 + j0 + j;
+                x[u][e] = j0 + j >= last || c >= d ? zero
+                          : c < a.nope             ? load4(kn + (row * a.heads + h) * a.nope + c)
+                                                   : load4(rows + row * a.width + a.kv_lora + c - a.nope);
+            }
+    };
+    auto load_values = [&](int64_t j0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int64_t j = j0 + warp + 8 * u;
+                x[u][e] = j < last ? load4(v + ((t.row0 + j) * a.heads + h) * VD + e * 128 + lane * 4) : zero;
+            }
+    };
+    if (kAhead) load_keys((int64_t)t.kt0 * kKeys);
 
     for (int kt = t.kt0; kt < t.kt1; ++kt) {
         const int64_t j0 = (int64_t)kt * kKeys;
+        if (!kAhead) load_keys(j0);
         __syncthreads();
-        {
-            float4 x[4][2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = warp + 8 * u, c = e * 128 + lane * 4;
-                    const int64_t row = t.row0 + j0 + j;
-                    x[u][e] = j0 + j >= last || c >= d ? zero
-                              : c < a.nope             ? load4(kn + (row * a.heads + h) * a.nope + c)
-                                                       : load4(rows + row * a.width + a.kv_lora + c - a.nope);
-                }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (e * 128 + lane * 4 < d) store4(Ks + (warp + 8 * u) * ld + e * 128 + lane * 4, x[u][e]);
-        }
+            for (int e = 0; e < 2; ++e)
+                if (e * 128 + lane * 4 < d) store4(Ks + (warp + 8 * u) * ld + e * 128 + lane * 4, x[u][e]);
         __syncthreads();
-        const int quarter = lane >> 3, k8 = lane & 7;
-        float s[RPW][4] = {};                            // of keys k8 + 8 k
+        if (kAhead) load_values(j0);
+        if (busy) {
+            const int quarter = lane >> 3, k8 = lane & 7;
+            float s[RPW][4] = {};                        // of keys k8 + 8 k
 #pragma unroll 1
-        for (int c = quarter * 4; c < d; c += 16) {
-            float4 k[4];
+            for (int c = quarter * 4; c < d; c += 16) {
+                float4 k[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) k[e] = load4(Ks + (k8 + 8 * e) * ld + c);
+                for (int e = 0; e < 4; ++e) k[e] = load4(Ks + (k8 + 8 * e) * ld + c);
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) {
+                    const float4 x = load4(Qs + (warp + 8 * r) * ld + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[r][e] = fmaf(x.x, k[e].x, fmaf(x.y, k[e].y, fmaf(x.z, k[e].z, fmaf(x.w, k[e].w, s[r][e]))));
+                }
+            }
+            // the quarters' sums: a lane gives away those of the keys that it does not keep,
+            // and keeps key k8 + 8 quarter = lane
+            float p[RPW];
 #pragma unroll
             for (int r = 0; r < RPW; ++r) {
-                const float4 x = load4(Qs + (warp + 8 * r) * ld + c);
+                const bool hi = (quarter & 2) != 0, odd = (quarter & 1) != 0;
+                const float a0 = (hi ? s[r][2] : s[r][0]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][0] : s[r][2], 16);
+                const float a1 = (hi ? s[r][3] : s[r][1]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][1] : s[r][3], 16);
+                const float dot = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+                const float z = j0 + lane < t.first + warp + 8 * r ? dot * scale : -INFINITY;
+                float top = z;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[r][e] = fmaf(x.x, k[e].x, fmaf(x.y, k[e].y, fmaf(x.z, k[e].z, fmaf(x.w, k[e].w, s[r][e]))));
+                for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float mn = fmaxf(m[r], top);
+                const float base = mn == -INFINITY ? 0.f : mn;   // nothing to see so far
+                const float f = exp2f(m[r] - base);
+                p[r] = exp2f(z - base);
+                l[r] = l[r] * f + p[r];
+                m[r] = mn;
+                const float2 f2 = make_float2(f, f);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    o[r][c][0] = mul_x2(o[r][c][0], f2);
+                    o[r][c][1] = mul_x2(o[r][c][1], f2);
+                }
+            }
+            if constexpr (RPW == 8) {
+                store4(Ps + lane * kLdP + warp * RPW, make_float4(p[0], p[1], p[2], p[3]));
+                store4(Ps + lane * kLdP + warp * RPW + 4, make_float4(p[4], p[5], p[6], p[7]));
+            } else {
+#pragma unroll
+                for (int r = 0; r < RPW; ++r) Ps[lane * kLdP + warp * RPW + r] = p[r];
             }
         }
-        // the quarters' sums: a lane gives away those of the keys that it does not keep,
-        // and keeps key k8 + 8 quarter = lane
-        float p[RPW];
-#pragma unroll
-        for (int r = 0; r < RPW; ++r) {
-            const bool hi = (quarter & 2) != 0, odd = (quarter & 1) != 0;
-            const float a0 = (hi ? s[r][2] : s[r][0]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][0] : s[r][2], 16);
-            const float a1 = (hi ? s[r][3] : s[r][1]) + __shfl_xor_sync(0xffffffffu, hi ? s[r][1] : s[r][3], 16);
-            const float dot = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
-            const float z = j0 + lane < t.first + warp + 8 * r ? dot * scale : -INFINITY;
-            float top = z;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float mn = fmaxf(m[r], top);
-            const float base = mn == -INFINITY ? 0.f : mn;   // nothing to see so far
-            const float f = exp2f(m[r] - base);
-            p[r] = exp2f(z - base);
-            l[r] = l[r] * f + p[r];
-            m[r] = mn;
-            const float2 f2 = make_float2(f, f);
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                o[r][c][0] = mul_x2(o[r][c][0], f2);
-                o[r][c][1] = mul_x2(o[r][c][1], f2);
-            }
-        }
-        if constexpr (RPW == 8) {
-            store4(Ps + lane * kLdP + warp * RPW, make_float4(p[0], p[1], p[2], p[3]));
-            store4(Ps + lane * kLdP + warp * RPW + 4, make_float4(p[4], p[5], p[6], p[7]));
-        } else {
-#pragma unroll
-            for (int r = 0; r < RPW; ++r) Ps[lane * kLdP + warp * RPW + r] = p[r];
-        }
+        if (!kAhead) load_values(j0);
         __syncthreads();                                 // the keys are read, the warp's weights written
         float4 odd = zero;                               // NaN if a value is no number
         {
-            float4 x[4][kVec];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const int64_t j = j0 + warp + 8 * u;
-                    x[u][e] = j < last ? load4(v + ((t.row0 + j) * a.heads + h) * VD + e * 128 + lane * 4) : zero;
-                }
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -173,6 +186,7 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
                     odd.z = fmaf(y.z, 0.f, odd.z); odd.w = fmaf(y.w, 0.f, odd.w);
                 }
         }
+        if (kAhead && kt + 1 < t.kt1) load_keys(j0 + kKeys);
         // 0 times infinity is NaN: where some query does not see a key of the tile and a
         // value is no number, each weight is looked at
         const bool careful = __syncthreads_or((odd.x + odd.y) + (odd.z + odd.w) != 0.f) && j0 + kKeys > t.first;
@@ -198,6 +212,7 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
                 }
             }
         };
+        if (!busy) continue;
         if (!careful) {
 #pragma unroll 4
             for (int j = 0; j < kKeys; ++j) values(j, false);
@@ -226,9 +241,9 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
     }
 }
 
-// Tiles of 8 RPW queries, with fewer to a warp in one that has no more than a
-// quarter of them: it still takes most of a tile's loads, but a quarter of the
-// arithmetic (three prompts of 1, 129 and 257 queries: 177 us instead of 212).
+// Tiles of 8 RPW queries, with fewer to a warp in one that has few: it still takes the
+// tile's loads, but less arithmetic and shared memory (three prompts of 1, 129 and 257
+// queries: 174 us instead of 212).
 template <int RPW, int VD>
 __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     extern __shared__ __align__(16) float smem[];
@@ -240,7 +255,8 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     pdl_trigger();
     ExpandedTile t;
     if (!expanded_tile(a.b, slot, split, a.n_split, 8 * RPW, kKeys, a.err, 60, t)) return;
-    if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
+    if (t.n_q <= 8) simt_tile<1, VD>(a, t, h, split, smem);
+    else if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
     else simt_tile<RPW, VD>(a, t, h, split, smem);
 }
 
