@@ -428,6 +428,11 @@ def dsa_paged_mla_attn(shape, batch, pages, q_abs, codes, scales, block_table, i
 _DSA_DTYPE = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16}
 
 
+# The current device, without the look at whether CUDA is there (a tensor of the call is on
+# it, or refused): 0.12 of 0.25 us.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _dtype(t, what: str) -> int:
     if t is None:
         raise ValueError(f"{what} is missing")
@@ -442,13 +447,13 @@ def _rows_at(t, like, dtype, device: int, what: str):
     parts of wider ones."""
     if t is None:
         raise ValueError(f"{what} is missing")
-    shape, (ld, step) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
-    if shape != like or t.dtype is not dtype or t.get_device() != device:
-        if shape != like:
-            raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(shape)}")
+    if t.shape != like or t.dtype is not dtype or t.get_device() != device:
+        if t.shape != like:
+            raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(t.shape)}")
         _refuse(t, dtype, device, 0, what)
+    ld, step = t.stride()
     rows, width = like
-    if width > 1 and step != 1:
+    if step != 1 and width > 1:
         raise ValueError(f"{what}'s rows are contiguous: its last stride is 1")
     return t.data_ptr(), ld if rows > 1 else width
 
@@ -458,10 +463,10 @@ def dsa_rms_norm(x, weight, eps, out, add=None, total=None, scales=None, group=0
     """Norm of the rows of ``x`` [rows, width], or of ``x + add`` (see dsa.h);
     ``total`` gets the sum.  ``out`` has x's type, or one-byte elements (e4m3
     codes) with ``scales`` [rows, ceil(width / group)] float32 (group 0: [rows, 1])."""
-    like, d, kind = getattr(x, "shape", None), torch.cuda.current_device(), _dtype(x, "x")
+    kind, d = _dtype(x, "x"), _device()
+    like, dt = x.shape, x.dtype
     if len(like) != 2:
         raise ValueError("x is a matrix of rows")
-    dt = x.dtype
     rows, width = like
     px, x_ld = _rows_at(x, like, dt, d, "x")
     pa, a_ld = (None, 0) if add is None else _rows_at(add, like, dt, d, "add")
@@ -499,9 +504,9 @@ def _heads_at(t, like, dtype, device: int, what: str):
     [tokens, dims], the last dimension contiguous."""
     if t is None:
         raise ValueError(f"{what} is missing")
-    if t.shape != like:
-        raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(t.shape)}")
-    if t.dtype is not dtype or t.get_device() != device:
+    if t.shape != like or t.dtype is not dtype or t.get_device() != device:
+        if t.shape != like:
+            raise ValueError(f"{what} has the shape {tuple(like)}, not {tuple(t.shape)}")
         _refuse(t, dtype, device, 0, what)
     s = t.stride()
     if s[-1] != 1:
@@ -512,14 +517,15 @@ def _heads_at(t, like, dtype, device: int, what: str):
 def dsa_rope(rope, x, pos, out, stream=None) -> None:
     """``x`` [tokens, heads, dims] or [tokens, dims] (views of the rotated columns)
     turned by ``pos`` [tokens] int64 into ``out``, which may be x (see dsa.h)."""
-    d, kind = torch.cuda.current_device(), _dtype(x, "x")
-    like = x.shape
+    kind, d = _dtype(x, "x"), _device()
+    like, dt = x.shape, x.dtype
     if len(like) not in (2, 3) or like[-1] != rope.dims:
         raise ValueError(f"x is [tokens, heads, {rope.dims}] or [tokens, {rope.dims}]")
-    px, x_tok, x_head = _heads_at(x, like, x.dtype, d, "x")
-    po, o_tok, o_head = _heads_at(out, like, x.dtype, d, "out")
-    _call("dsa_rope", rope, kind, like[0], like[1] if len(like) == 3 else 1, px, x_tok, x_head,
-          _at(pos, torch.int64, d, like[0], "pos"), po, o_tok, o_head, _stream_at(stream, d))
+    tokens = like[0]
+    px, x_tok, x_head = _heads_at(x, like, dt, d, "x")
+    po, o_tok, o_head = _heads_at(out, like, dt, d, "out")
+    _call("dsa_rope", rope, kind, tokens, like[1] if len(like) == 3 else 1, px, x_tok, x_head,
+          _at(pos, torch.int64, d, tokens, "pos"), po, o_tok, o_head, _stream_at(stream, d))
 
 
 def _weights_at(t, shape, device: int, what: str):
@@ -535,7 +541,7 @@ def _weights_at(t, shape, device: int, what: str):
 def dsa_expand_kv(shape, cache, w_uk, w_uv, k_nope, v, ws, stream=None) -> None:
     """``cache`` [rows, W] expanded into ``k_nope`` [rows, heads, nope] and ``v``
     [rows, heads, v_dim] (see dsa.h)."""
-    d, dt = torch.cuda.current_device(), _TORCH_DTYPE[shape.dtype]
+    d, dt = _device(), _TORCH_DTYPE[shape.dtype]
     pk, nope = _weights_at(w_uk, shape, d, "w_uk")
     pv, v_dim = _weights_at(w_uv, shape, d, "w_uv")
     if cache is None or cache.dim() != 2 or cache.shape[1] != shape.kv_lora + shape.rope_dim:
@@ -550,7 +556,7 @@ def dsa_expand_kv(shape, cache, w_uk, w_uv, k_nope, v, ws, stream=None) -> None:
 def dsa_expanded_mla_attn(shape, batch, q, k_nope, cache, v, out, lse, ws, stream=None) -> None:
     """Causal attention over expanded keys ``k_nope`` [rows, heads, nope] and values
     ``v`` [rows, heads, v_dim], the rope part of the keys in ``cache`` (see dsa.h)."""
-    d, dt = torch.cuda.current_device(), _TORCH_DTYPE[shape.dtype]
+    d, dt = _device(), _TORCH_DTYPE[shape.dtype]
     heads, rope, n_q, rows = shape.heads, shape.rope_dim, batch.n_q, batch.total_rows
     if k_nope is None or v is None or k_nope.dim() != 3 or v.dim() != 3 or \
             k_nope.shape[1] != heads or v.shape[1] != heads:
