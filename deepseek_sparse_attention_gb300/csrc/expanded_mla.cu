@@ -48,7 +48,8 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
     constexpr int kVec = VD / 128;                       // groups of four output columns of a lane
     // Few queries, bound by the loads: these are asked for a product ahead, and warps without
     // a query do nothing else.  16 of them over up to 2,000 rows take 447 us, 4.1 TB/s; loads
-    // where they are used, and two queries to every warp, 968.
+    // where they are used, and two queries to every warp, 968.  (Tiles of 32 gain nothing from
+    // loads ahead, tiles of 64 have no registers for them: 183 us instead of 174.)
     constexpr bool kAhead = RPW <= 2;
     const int d = a.nope + a.rope, ld = d + 4;
     float* Qs = smem;
@@ -243,7 +244,7 @@ __device__ __forceinline__ void simt_tile(const ExpandedArgs& a, const ExpandedT
 
 // Tiles of 8 RPW queries, with fewer to a warp in one that has few: it still takes the
 // tile's loads, but less arithmetic and shared memory (three prompts of 1, 129 and 257
-// queries: 174 us instead of 212).
+// queries: 174 us instead of 217).
 template <int RPW, int VD>
 __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     extern __shared__ __align__(16) float smem[];
@@ -315,8 +316,8 @@ cudaError_t launch_simt(const ExpandedArgs& a, int bq, cudaStream_t st) {
 }
 
 // Queries of a tile: 16 or 32 where no sequence has more, else 64 (two prompts of 1 and
-// 20 tokens behind 100 and 0 rows: 18.5 us with 32, 23.1 with 64; eight of up to 32
-// behind up to 1,000: 270 and 375).
+// 20 tokens behind 100 and 0 rows: 13.3 us with 32, 19.9 with 64; eight of up to 32
+// behind up to 1,000: 234 and 331).
 int tile_queries(const BatchDev& b) { return b.max_q_len <= 16 ? 16 : b.max_q_len <= 32 ? 32 : kMaxTileQ; }
 
 }  // namespace
