@@ -9,7 +9,9 @@
 // lane eight of them: neighbours, moved as 16 bytes, where pointers and strides
 // allow it (VEC), else every 32nd, so that a warp's accesses of single elements
 // are contiguous.  Either way the columns of a scale lie in one warp's chunk,
-// and their maximum is a shuffle.
+// and their maximum is a shuffle.  Where inputs alone are not aligned for it (rows an odd
+// stride apart, say) and the output is codes, the aligned 16 bytes around each piece are
+// read and shifted into place (SHIFT).
 #include <cuda_fp8.h>
 
 #include "dsa_kernels.cuh"
@@ -82,6 +84,51 @@ __device__ __forceinline__ void load_chunk(Raw<T, VEC>& r, const T* p, int col, 
     }
 }
 
+// The aligned 16-byte words around a lane's eight columns of a row that begins anywhere;
+// what they hold beside the row is not read.
+template <typename T>
+struct Around {
+    static constexpr int kWords = kPer * sizeof(T) / 4 + 4;
+    uint32_t w[kWords];
+};
+template <typename T>
+__device__ __forceinline__ void load_around(Around<T>& r, const T* row, int col, int width) {
+    const T* end = row + width;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
+    const T* p = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(row + col) - off);
+#pragma unroll
+    for (int g = 0; g < Around<T>::kWords / 4; ++g) {
+        constexpr int n = 16 / sizeof(T);
+        const T* q = p + g * n;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (col < width && (off != 0 || g + 1 < Around<T>::kWords / 4)) {
+            if (q >= row && q + n <= end) {
+                x = *reinterpret_cast<const uint4*>(q);
+            } else {                                     // the row's first or last columns
+                alignas(16) T e[n];
+#pragma unroll
+                for (int i = 0; i < n; ++i) e[i] = q + i >= row && q + i < end ? q[i] : T(0.f);
+                x = *reinterpret_cast<const uint4*>(e);
+            }
+        }
+        r.w[4 * g] = x.x; r.w[4 * g + 1] = x.y; r.w[4 * g + 2] = x.z; r.w[4 * g + 3] = x.w;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void shift_in(Raw<T, true>& r, Around<T>& a, const T* row) {
+    constexpr int n = kPer * sizeof(T) / 4;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15);
+    if (off & 8)
+#pragma unroll
+        for (int i = 0; i < n + 2; ++i) a.w[i] = a.w[i + 2];
+    if (off & 4)
+#pragma unroll
+        for (int i = 0; i < n + 1; ++i) a.w[i] = a.w[i + 1];
+    uint32_t* out = reinterpret_cast<uint32_t*>(r.v);
+#pragma unroll
+    for (int i = 0; i < n; ++i) out[i] = sizeof(T) == 2 ? __funnelshift_r(a.w[i], a.w[i + 1], 8 * (off & 3)) : a.w[i];
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_chunk(T* p, const float2 (&h)[kPer / 2], int col, int width) {
     alignas(16) Raw<T, VEC> r;
@@ -143,9 +190,11 @@ constexpr int kCtas = !VEC ? 0 : (C == 4 ? 512 : sizeof(T) == 2 ? 1024 : 768) / 
 
 // TPR threads to a row, each with up to C chunks' pieces; rows a stride apart, the
 // next one's loads in flight while a row is reduced and written.
-template <typename T, bool E4M3, bool VEC, int TPR, int C>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kCtas<T, VEC, TPR, C> > 0 ? kCtas<T, VEC, TPR, C> : 1)
+template <typename T, bool E4M3, bool VEC, bool SHIFT, int TPR, int C>
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR,
+                                  kCtas<T, VEC && !SHIFT, TPR, C> > 0 ? kCtas<T, VEC && !SHIFT, TPR, C> : 1)
 rms_norm_kernel(const NormArgs a) {
+    constexpr int kAhead = kCtas<T, VEC && !SHIFT, TPR, C>;
     constexpr int kRows = TPR == 32 ? 8 : 1;             // rows of a CTA
     constexpr int kWarps = TPR / 32;                     // warps of a row
     __shared__ float bufs[2][3][kWarps];
@@ -164,12 +213,27 @@ rms_norm_kernel(const NormArgs a) {
     for (int c = 0; c < C; ++c) rx[c] = ra[c] = Raw<T, VEC>{};
     auto fetch = [&](int64_t r) {
         const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
+        if constexpr (SHIFT) {
+            const T* add = a.add == nullptr ? nullptr : static_cast<const T*>(a.add) + r * a.add_ld;
+            Around<T> wx[C], wa[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk<true>(rx[c], x, col(c), a.width);
-        if (a.add == nullptr) return;
-        const T* add = static_cast<const T*>(a.add) + r * a.add_ld;
+            for (int c = 0; c < C; ++c) load_around(wx[c], x, col(c), a.width);
+            if (add != nullptr)
 #pragma unroll
-        for (int c = 0; c < C; ++c) load_chunk<true>(ra[c], add, col(c), a.width);
+                for (int c = 0; c < C; ++c) load_around(wa[c], add, col(c), a.width);
+#pragma unroll
+            for (int c = 0; c < C; ++c) shift_in(rx[c], wx[c], x);
+            if (add != nullptr)
+#pragma unroll
+                for (int c = 0; c < C; ++c) shift_in(ra[c], wa[c], add);
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_chunk<true>(rx[c], x, col(c), a.width);
+            if (a.add == nullptr) return;
+            const T* add = static_cast<const T*>(a.add) + r * a.add_ld;
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_chunk<true>(ra[c], add, col(c), a.width);
+        }
     };
     fetch(row);
     for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
@@ -183,7 +247,7 @@ rms_norm_kernel(const NormArgs a) {
                 h[c][i] = add_x2(rx[c].pair(i), ra[c].pair(i));   // zeros past the row
                 sq = fma_x2(h[c][i], h[c][i], sq);
             }
-        if (kCtas<T, VEC, TPR, C> > 0 && row + stride < a.n_rows) {
+        if (kAhead > 0 && row + stride < a.n_rows) {
             fetch(row + stride);
             // and the one after it into L2 (16-byte pieces, as the loads are)
             const int64_t later = row + 2 * stride;
@@ -273,10 +337,9 @@ rms_norm_kernel(const NormArgs a) {
                     float m[kPer];
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
-                        m[e] = fabsf(e & 1 ? h[c][e / 2].y : h[c][e / 2].x);
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            m[e] = max_nan(m[e], __shfl_xor_sync(0xffffffffu, m[e], o));
+                        // as integers, which order as the numbers do, NaN above them
+                        m[e] = __uint_as_float(__reduce_max_sync(
+                            0xffffffffu, __float_as_uint(fabsf(e & 1 ? h[c][e / 2].y : h[c][e / 2].x))));
                     }
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
@@ -312,33 +375,36 @@ rms_norm_kernel(const NormArgs a) {
     }
 }
 
-template <typename T, bool E4M3, bool VEC, int TPR, int C>
+template <typename T, bool E4M3, bool VEC, bool SHIFT, int TPR, int C>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     constexpr int kRows = TPR == 32 ? 8 : 1;
     int64_t blocks = (a.n_rows + kRows - 1) / kRows;
-    const int64_t wave = (int64_t)sm_count() * kCtas<T, VEC, TPR, C>;
+    const int64_t wave = (int64_t)sm_count() * kCtas<T, VEC && !SHIFT, TPR, C>;
     if (wave > 0 && blocks > wave) blocks = wave;
-    return launch_pdl(rms_norm_kernel<T, E4M3, VEC, TPR, C>, dim3((unsigned)blocks),
+    return launch_pdl(rms_norm_kernel<T, E4M3, VEC, SHIFT, TPR, C>, dim3((unsigned)blocks),
                       dim3(TPR == 32 ? 256 : TPR), 0, st, a);
 }
 
-template <typename T, bool E4M3, bool VEC>
+template <typename T, bool E4M3, bool VEC, bool SHIFT>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     // a warp to a row of up to 1,024 columns; beyond, as many threads as leave each
     // two pieces of eight columns: its registers then let 1,500 threads or more of a
     // multiprocessor have loads in flight
-    if (a.width <= 512) return launch<T, E4M3, VEC, 32, 2>(a, st);
-    if (a.width <= 1024) return launch<T, E4M3, VEC, 32, 4>(a, st);
-    if (a.width <= 2048) return launch<T, E4M3, VEC, 128, 2>(a, st);
-    if (a.width <= 4096) return launch<T, E4M3, VEC, 256, 2>(a, st);
-    if (a.width <= 8192) return launch<T, E4M3, VEC, 512, 2>(a, st);
-    return launch<T, E4M3, VEC, 512, 4>(a, st);
+    if (a.width <= 512) return launch<T, E4M3, VEC, SHIFT, 32, 2>(a, st);
+    if (a.width <= 1024) return launch<T, E4M3, VEC, SHIFT, 32, 4>(a, st);
+    if (a.width <= 2048) return launch<T, E4M3, VEC, SHIFT, 128, 2>(a, st);
+    if (a.width <= 4096) return launch<T, E4M3, VEC, SHIFT, 256, 2>(a, st);
+    if (a.width <= 8192) return launch<T, E4M3, VEC, SHIFT, 512, 2>(a, st);
+    return launch<T, E4M3, VEC, SHIFT, 512, 4>(a, st);
 }
 
+enum class Access { kVec, kShift, kSingle };
+
 template <typename T>
-cudaError_t launch(const NormArgs& a, bool e4m3, bool vec, cudaStream_t st) {
-    if (e4m3) return vec ? launch<T, true, true>(a, st) : launch<T, true, false>(a, st);
-    return vec ? launch<T, false, true>(a, st) : launch<T, false, false>(a, st);
+cudaError_t launch(const NormArgs& a, bool e4m3, Access how, cudaStream_t st) {
+    if (how == Access::kShift) return launch<T, true, true, true>(a, st);
+    if (e4m3) return how == Access::kVec ? launch<T, true, true, false>(a, st) : launch<T, true, false, false>(a, st);
+    return how == Access::kVec ? launch<T, false, true, false>(a, st) : launch<T, false, false, false>(a, st);
 }
 
 }  // namespace
@@ -350,10 +416,13 @@ cudaError_t launch_rms_norm(const NormArgs& a, int32_t dtype, bool e4m3, cudaStr
     auto fits = [](const void* p, int64_t ld, int64_t size, int64_t unit) {
         return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * size)) & (unit - 1)) == 0;
     };
-    const bool vec = a.width % kPer == 0 && fits(a.x, a.x_ld, e, 16) && fits(a.add, a.add_ld, e, 16) &&
-                     fits(a.total, a.total_ld, e, 16) && fits(a.weight, 0, 4, 16) &&
+    const bool out = a.width % kPer == 0 && fits(a.total, a.total_ld, e, 16) && fits(a.weight, 0, 4, 16) &&
                      (e4m3 ? fits(a.out, a.out_ld, 1, 8) : fits(a.out, a.out_ld, e, 16));
-    return dtype == DSA_BF16 ? launch<__nv_bfloat16>(a, e4m3, vec, st) : launch<float>(a, e4m3, vec, st);
+    const bool in = fits(a.x, a.x_ld, e, 16) && fits(a.add, a.add_ld, e, 16);
+    // shifted for codes alone, whose scales want neighbours in a lane: 3,400 bf16 rows of 8,192
+    // columns, 8,195 apart, 48 us and one by one 87; to bf16 rows 52 and 47
+    const Access how = out && in ? Access::kVec : out && e4m3 ? Access::kShift : Access::kSingle;
+    return dtype == DSA_BF16 ? launch<__nv_bfloat16>(a, e4m3, how, st) : launch<float>(a, e4m3, how, st);
 }
 
 }  // namespace dsa

@@ -102,6 +102,44 @@ def test_norm_codes(width, ld, out_ld, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [8, 512, 520, 1024, 2048, 2056, 4096, 8192, 16384])
+def test_norm_of_inputs_at_any_place(width, dtype):
+    """Rows that begin at any element, x's and the residual's at different ones, between NaN.  As
+    codes the same bits as of aligned copies, whose sums have the same order."""
+    g = _gen(width + 1)
+    rows = 11
+    x = torch.randn((rows, width), generator=g, device="cuda").to(T[dtype])
+    add = torch.randn((rows, width), generator=g, device="cuda").to(T[dtype])
+    w = torch.randn(width, generator=g, device="cuda")
+
+    def placed(t, at, ld):
+        room = torch.full((at + (rows - 1) * ld + width,), math.nan, dtype=t.dtype, device="cuda")
+        view = torch.as_strided(room, (rows, width), (ld, 1), at)
+        view.copy_(t)
+        return view
+
+    def run(x, add, codes):
+        y = torch.full((rows, width), math.nan, dtype=T[dtype], device="cuda") if not codes else \
+            torch.full((rows, width), 0x55, dtype=torch.uint8, device="cuda")
+        total = torch.full((rows, width), math.nan, dtype=T[dtype], device="cuda")
+        scales = torch.full((rows, -(-width // 64)), 7.0, device="cuda") if codes else None
+        dsa.dsa_rms_norm(x, w, 1e-5, y, add=add, total=None if add is None else total, scales=scales,
+                         group=64 if codes else 0)
+        return [y] + ([] if add is None else [total]) + ([scales] if codes else [])
+
+    for codes in (False, True):
+        for with_add in (False, True):
+            want = run(x, add if with_add else None, codes)
+            for at, ld in [(0, width + 1), (1, width), (1, width + 3), (2, width + 8), (3, width + 5), (5, width + 7),
+                           (7, width + 2), (4, width + 4)]:
+                got = run(placed(x, at, ld), placed(add, 8 - at, ld + at) if with_add else None, codes)
+                if codes:
+                    assert all(torch.equal(p, q) for p, q in zip(got, want))
+                else:
+                    check_norm(got[0], got[1] if with_add else None, x, add if with_add else None, w, 1e-5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_of_part_of_a_row(dtype):
     """The latent columns of cache rows, in place; the rope columns stay as they are."""
     g = _gen(3)
