@@ -259,12 +259,15 @@ rms_norm_kernel(const NormArgs a) {
         }
         float ss = row_reduce<TPR, false>(sq.x + sq.y, buf[0]);
         float rstd;
-        // Squares beyond float32, or so small that they lose bits which eps does
-        // not cover: once more, of h times a power of two (all threads of the row)
-        const bool high = isinf(ss);
+        // Squares, or their mean and eps, beyond float32, or so small that they lose bits which
+        // eps does not cover: once more, of h times a power of two (all threads of the row).  High:
+        // of 16,384 squares of up to 2^128 each, times 2^-160, the sum is below 2^111; a root above
+        // 2^126 has a subnormal inverse, within 2^-22 of itself.
+        const float square = fmaf(ss, a.mean, a.eps);
+        const bool high = isinf(square);
         const bool low = ss < 0x1p-60f * (float)a.width && a.eps < 0x1p-60f;
         if (high || low) {
-            const float f = high ? 0x1p-70f : 0x1p60f;
+            const float f = high ? 0x1p-80f : 0x1p60f;
             ss = 0.f;
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -274,7 +277,7 @@ rms_norm_kernel(const NormArgs a) {
             ss = row_reduce<TPR, false>(ss, buf[1]);
             rstd = f * rsqrtf(ss * a.mean + a.eps * f * f);
         } else {
-            rstd = rsqrtf(ss * a.mean + a.eps);
+            rstd = rsqrtf(square);
         }
         if (a.total != nullptr) {
             T* t = static_cast<T*>(a.total) + row * a.total_ld;
