@@ -26,6 +26,7 @@ constexpr int kPer = 8;                      // columns a lane has of a chunk
 constexpr int kChunk = 32 * kPer;            // columns of a warp's chunk
 constexpr float kTop = 448.f;                // the largest e4m3 value
 constexpr float kLeast = 0x1p-126f;          // the least scale: its inverse is finite
+constexpr float kMost = 3.402823466e38f;     // float32's largest value
 
 // Eight elements as they are in memory: neighbours (VEC) or 32 apart.
 template <typename T, bool VEC>
@@ -175,12 +176,27 @@ __device__ __forceinline__ float row_reduce(float v, float* buf) {
     return v;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kTop), kLeast); }
-// 1 / s within a unit in the last place, for s from 2^-126 to 2^126.
-__device__ __forceinline__ float inverse(float s) {
-    float r;
+// The steps from a product with an inverse to the quotient, below: q + (y - q s) / s, whose
+// difference is exact ("Computation of elementary functions on the IBM RISC System/6000 processor",
+// Markstein, 1990).  From amax / 448 it gives the rounded quotient for each of the 2^23 mantissas.
+__device__ __forceinline__ float scale_of(float amax) {
+    const float q = amax * (1.f / kTop);
+    return max_nan(fmaf(fmaf(-fminf(q, kMost), kTop, amax), 1.f / kTop, q), kLeast);
+}
+// Two quotients y / s from r = 1 / s within a unit in the last place, rounded to float32 or, seldom, to
+// its neighbour.  Their codes are those of the rounded quotients: over every mantissa of a scale and
+// the nine y around each middle between two codes, a quotient is on its side of the middle, where
+// the product alone is on another for 6.5%.  (Of a scale below 2^-92 the difference may lose bits; the
+// quotient is then within 2^-22.  Keeping them by a power of two costs another product: 4,096 x
+// 8,192 with residual 42.4 us, 41.4 so, 40.2 without the step.)
+__device__ __forceinline__ float2 quotients(float2 y, float2 minus_s, float2 r) {
+    const float2 q = mul_x2(y, r);
+    return fma_x2(fma_x2(q, minus_s, y), r, q);
+}
+// The scale's part of them.  An infinite scale has finite quotients of zero.
+__device__ __forceinline__ void divide_by(float s, float& minus_s, float& r) {
+    minus_s = -fminf(s, kMost);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    return r;
 }
 
 // CTAs of a multiprocessor that the registers of a row and of the next one allow;
@@ -319,7 +335,7 @@ rms_norm_kernel(const NormArgs a) {
             for (int c = 0; c < C; ++c) {
                 const int at = (c * kWarps + warp) * kChunk;
                 if (at >= a.width) break;                // the whole warp
-                float2 inv[VEC ? 1 : kPer / 2];
+                float2 minus_s[VEC ? 1 : kPer / 2], inv[VEC ? 1 : kPer / 2];
                 if (VEC || a.group == 0) {
                     if (a.group != 0) {                  // 4, 8 or 16 lanes
                         float m = 0.f;
@@ -332,9 +348,13 @@ rms_norm_kernel(const NormArgs a) {
                         s = scale_of(m);
                         if ((col(c) & (a.group - 1)) == 0 && col(c) < a.width) scales[col(c) >> shift] = s;
                     }
-                    const float r = inverse(s);
+                    float ms, r;
+                    divide_by(s, ms, r);
 #pragma unroll
-                    for (int i = 0; i < (VEC ? 1 : kPer / 2); ++i) inv[i] = make_float2(r, r);
+                    for (int i = 0; i < (VEC ? 1 : kPer / 2); ++i) {
+                        minus_s[i] = make_float2(ms, ms);
+                        inv[i] = make_float2(r, r);
+                    }
                 } else {                                 // 1, 2 or 4 neighbouring elements of all lanes
                     const int n = a.group / 32;
                     float m[kPer];
@@ -351,17 +371,16 @@ rms_norm_kernel(const NormArgs a) {
                                                  max_nan(m[(e & ~3) + 2], m[e | 3]));
                         s = scale_of(n == 1 ? m[e] : n == 2 ? m2 : m4);
                         if (lane == 0 && e % n == 0 && at + 32 * e < a.width) scales[(at + 32 * e) >> shift] = s;
-                        (e & 1 ? inv[VEC ? 0 : e / 2].y : inv[VEC ? 0 : e / 2].x) = inverse(s);
+                        float2 &ms = minus_s[VEC ? 0 : e / 2], &r = inv[VEC ? 0 : e / 2];
+                        divide_by(s, e & 1 ? ms.y : ms.x, e & 1 ? r.y : r.x);
                     }
                 }
-                // to nearest even; a NaN stays one.  The product with 1 / s may be
-                // the neighbouring code of the quotient's only where that lies within
-                // 2^-22 of the middle between two codes.
+                // to nearest even; a NaN stays one
                 alignas(8) uint8_t q[kPer];
 #pragma unroll
                 for (int i = 0; i < kPer / 2; ++i) {
-                    const __nv_fp8x2_storage_t two =
-                        __nv_cvt_float2_to_fp8x2(mul_x2(h[c][i], inv[VEC ? 0 : i]), __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(
+                        quotients(h[c][i], minus_s[VEC ? 0 : i], inv[VEC ? 0 : i]), __NV_SATFINITE, __NV_E4M3);
                     q[2 * i] = (uint8_t)(two & 0xff);
                     q[2 * i + 1] = (uint8_t)(two >> 8);
                 }

@@ -361,8 +361,9 @@ dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, c
  *   scales DSA_NORM_E4M3: [n_rows, ceil(width / group)] float32 out, dense, one
  *          per `group` columns (32, 64 or 128; 0 = one per row): the larger of
  *          2^-126 and the group's largest |y| / 448; a code is y / scale rounded
- *          to nearest even, and stands for code * scale.  Not read otherwise,
- *          and group = 0.
+ *          to nearest even, and stands for code * scale.  Both quotients are the
+ *          rounded ones of float32; of scales below 2^-92 a code's is within 2^-22
+ *          of itself.  Not read otherwise, and group = 0.
  * total, and out in dtype, may be x or add themselves (same stride; refused with
  * another); no other overlap.
  * Columns between a row's width and the next row are neither read nor written.
