@@ -255,10 +255,12 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     pdl_wait();
     pdl_trigger();
     ExpandedTile t;
-    if (!expanded_tile(a.b, slot, split, a.n_split, 8 * RPW, kKeys, a.err, 60, t)) return;
-    if (t.n_q <= 8) simt_tile<1, VD>(a, t, h, split, smem);
-    else if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
-    else simt_tile<RPW, VD>(a, t, h, split, smem);
+    if (expanded_tile(a.b, slot, split, a.n_split, 8 * RPW, kKeys, t)) {
+        if (t.n_q <= 8) simt_tile<1, VD>(a, t, h, split, smem);
+        else if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
+        else simt_tile<RPW, VD>(a, t, h, split, smem);
+    }
+    expanded_check(a.b, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x, a.err, 60);
 }
 
 // One warp per (query, head): the splits' sums weighted by their maxima.

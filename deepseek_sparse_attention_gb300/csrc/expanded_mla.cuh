@@ -37,31 +37,39 @@ struct ExpandedTile {
 __host__ __device__ inline int64_t expanded_slots(int64_t n_q, int64_t n_seq, int bq) {
     return n_q / bq + (n_seq < n_q ? n_seq : n_q);
 }
-__device__ __forceinline__ int64_t expanded_start(const BatchDev& b, int32_t s, int bq) {
+__host__ __device__ inline int64_t expanded_start(const BatchDev& b, int32_t s, int bq) {
     const int64_t q = b.q_off[s];
     return q / bq + (s < q ? s : q);
 }
 
-// False if the slot has no tile, or its sequence's offsets break the host's
-// bounds (recorded once for the sequence).
-__device__ __forceinline__ bool expanded_tile(const BatchDev& b, int64_t slot, int32_t split,
-                                              int32_t n_split, int bq, int bk, int32_t* err,
-                                              int32_t where, ExpandedTile& t) {
+// Whether sequence s lies within the bounds that the host gave, and whether the batch's ends do.
+__host__ __device__ inline bool expanded_sound(const BatchDev& b, int32_t s) {
+    const int64_t q0 = b.q_off[s], q1 = b.q_off[s + 1], r0 = b.row_off[s], r1 = b.row_off[s + 1];
+    return q0 >= 0 && q1 >= q0 && q1 <= b.n_q && q1 - q0 <= b.max_q_len && r0 >= 0 && r1 >= r0 && r1 <= b.total_rows &&
+           r1 - r0 <= b.max_kv_len && q1 - q0 <= r1 - r0;
+}
+__host__ __device__ inline bool expanded_ends_sound(const BatchDev& b) {
+    return b.q_off[0] == 0 && b.q_off[b.n_seq] == b.n_q;
+}
+// Records sequences at, at + step, ... that are not.  The search for a slot's sequence need not
+// come to them: starts in disorder may hide one, and idle ones may have no slot.
+__device__ __forceinline__ void expanded_check(const BatchDev& b, int64_t at, int64_t step, int32_t* err, int32_t where) {
+    if (at == 0 && !expanded_ends_sound(b)) record_error(err, kDevBadBatch, b.n_seq, where);
+    for (; at < b.n_seq; at += step)
+        if (!expanded_sound(b, (int32_t)at)) record_error(err, kDevBadBatch, (int32_t)at, where);
+}
+
+// False if the slot has no tile, or its sequence is not sound.
+__host__ __device__ inline bool expanded_tile(const BatchDev& b, int64_t slot, int32_t split, int32_t n_split, int bq,
+                                              int bk, ExpandedTile& t) {
     int32_t lo = 0, hi = b.n_seq - 1;
     while (lo < hi) {                                    // last s whose slots start at or before this one
         const int32_t mid = lo + (hi - lo + 1) / 2;
         if (expanded_start(b, mid, bq) <= slot) lo = mid; else hi = mid - 1;
     }
-    const int64_t q0 = b.q_off[lo], q1 = b.q_off[lo + 1], r0 = b.row_off[lo], r1 = b.row_off[lo + 1];
+    if (!expanded_sound(b, lo)) return false;
+    const int64_t q0 = b.q_off[lo], q_len = b.q_off[lo + 1] - q0, r0 = b.row_off[lo], kv_len = b.row_off[lo + 1] - r0;
     const int64_t at = slot - (q0 / bq + (lo < q0 ? lo : q0));
-    if (slot == 0 && (b.q_off[0] != 0 || b.q_off[b.n_seq] != b.n_q))
-        record_error(err, kDevBadBatch, b.n_seq, where);
-    if (q0 < 0 || q1 < q0 || q1 > b.n_q || q1 - q0 > b.max_q_len || r0 < 0 || r1 > b.total_rows ||
-        r1 - r0 > b.max_kv_len || q1 - q0 > r1 - r0) {
-        if (at == 0) record_error(err, kDevBadBatch, lo, where);
-        return false;
-    }
-    const int64_t q_len = q1 - q0, kv_len = r1 - r0;
     if (at < 0 || at * bq >= q_len) return false;
     t.q0 = q0 + at * bq;
     t.row0 = r0;

@@ -23,7 +23,7 @@
 //              and only then they are exchanged and O is rescaled in TMEM;
 //   warps 10-11 values of tiles that some query sees only in part: NaN and infinities
 //              are taken out of shared memory (0 times either is NaN) and given back in the
-//              epilogue to the queries that see them;
+//              epilogue to the queries that see them; and the check of the sequences' offsets;
 //   warps 12-15 epilogue: a unit's O to the output beside the next unit's first scores, a
 //              row to a thread, 64 columns of a warp's rows at a time through shared memory
 //              and a TMA store; straight from registers in whole sectors where a
@@ -78,6 +78,7 @@ struct Work {
     int32_t n_q, n;                                      // n: its key tiles, -1: no more work
     int32_t partial;                                     // key tiles from this one on are not seen in full by every query
     int32_t h;
+    uint32_t unit;                                       // its number: each is handed out once
 };
 
 struct Shared {
@@ -244,10 +245,10 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 Work w;
                 w.n = -1;
                 if (block >= 0) {
-                    const uint32_t unit = (uint32_t)(block / 2);
-                    w.h = (int)(unit / slots);
-                    const int64_t slot = slots - 1 - (int64_t)(unit % slots);
-                    if (!expanded_tile(a.b, slot, 0, 1, kQ, kK, w.h == 0 ? a.err : nullptr, 61, t)) {
+                    w.unit = (uint32_t)(block / 2);
+                    w.h = (int)(w.unit / slots);
+                    const int64_t slot = slots - 1 - (int64_t)(w.unit % slots);
+                    if (!expanded_tile(a.b, slot, 0, 1, kQ, kK, t)) {
                         t.n_q = t.kt1 = 0;
                         t.q0 = t.row0 = t.first = 0;
                     }
@@ -424,9 +425,13 @@ expanded_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!ok) break;
             const int n = s.work[k % kWorks].n;
             const int partial = s.work[k % kWorks].partial;
+            const uint32_t unit = s.work[k % kWorks].unit;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.work_free[k % kWorks]);
             if (n < 0) break;
+            // the pair's share of the sequences, in warps that mostly have nothing to do
+            expanded_check(a.b, ((int64_t)unit * 2 + rank) * kCleaners + c, (int64_t)slots * a.heads * 2 * kCleaners, a.err,
+                           61);
             if (n == 0) continue;
             ++busy;
             for (int i = partial; i < n; ++i) {

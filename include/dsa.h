@@ -467,8 +467,9 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  * float32 logits, maxima, sums and accumulation; bf16 operands give each
  * weight exp(z_j - m) to the value product rounded to bf16 (2^-8 of itself at most), the
  * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <
- * 2^31.  A sequence whose offsets break the host bounds is skipped and sets the
- * error word (code 2).  Pointers 16-byte aligned (out 32, lse 4).  Workspace:
+ * 2^31.  A sequence whose offsets break the host bounds, idle or not, is skipped and
+ * sets the error word (code 2); where q_off falls, sequences behind the fall may be
+ * skipped with it.  Pointers 16-byte aligned (out 32, lse 4).  Workspace:
  * DSA_OP_EXPANDED_MLA; it serves every batch of no more queries whose max_kv_len
  * is no larger. */
 dsa_status dsa_expand_kv(const dsa_shape *shape, int64_t n_rows, int32_t nope_dim, int32_t v_dim,
