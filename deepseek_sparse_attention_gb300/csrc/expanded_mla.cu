@@ -263,14 +263,20 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
     expanded_check(a.b, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x, a.err, 60);
 }
 
-// One warp per (query, head): the splits' sums weighted by their maxima.
+// One warp per (query, head): the splits' sums weighted by their maxima.  A CTA has eight queries of a
+// slot's tile, so that queries of refused sequences, or of none, have no warp: no split was
+// written for them.  The offsets are read before the wait for the splits, whose CTAs began behind
+// theirs.
 template <int VD>
-__global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, int64_t n) {
-    const int64_t qh = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (qh >= n) return;
+__global__ void __launch_bounds__(256) expanded_merge(const ExpandedArgs a, const int bq) {
+    const int64_t unit = blockIdx.x / (bq / 8);
+    const int at = (int)(blockIdx.x % (bq / 8)) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    ExpandedTile t;
+    const bool any = expanded_tile(a.b, unit / a.heads, 0, 1, bq, kKeys, t);
     pdl_wait();
     pdl_trigger();
+    if (!any || at >= t.n_q) return;
+    const int64_t qh = (t.q0 + at) * a.heads + unit % a.heads;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + qh * a.n_split;
     const float* po = a.part_o + qh * a.n_split * VD;
     float top = -INFINITY;
@@ -313,8 +319,8 @@ cudaError_t launch_simt(const ExpandedArgs& a, int bq, cudaStream_t st) {
                     : bq == 32 ? launch_tiles<4, VD>(a, st)
                                : launch_tiles<8, VD>(a, st);
     if (e != cudaSuccess || a.n_split == 1) return e;
-    const int64_t n = (int64_t)a.b.n_q * a.heads;
-    return launch_pdl(expanded_merge<VD>, dim3((unsigned)((n + 7) / 8)), dim3(256), 0, st, a, n);
+    const int64_t grid = expanded_slots(a.b.n_q, a.b.n_seq, bq) * a.heads * (bq / 8);
+    return launch_pdl(expanded_merge<VD>, dim3((unsigned)grid), dim3(256), 0, st, a, bq);
 }
 
 // Queries of a tile: 16 or 32 where no sequence has more, else 64 (two prompts of 1 and

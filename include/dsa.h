@@ -469,7 +469,8 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <
  * 2^31.  A sequence whose offsets break the host bounds, idle or not, is skipped and
  * sets the error word (code 2); where q_off falls, sequences behind the fall may be
- * skipped with it.  Pointers 16-byte aligned (out 32, lse 4).  Workspace:
+ * skipped with it.  Outputs of skipped queries, and of those that no sequence has, are
+ * not written.  Pointers 16-byte aligned (out 32, lse 4).  Workspace:
  * DSA_OP_EXPANDED_MLA; it serves every batch of no more queries whose max_kv_len
  * is no larger. */
 dsa_status dsa_expand_kv(const dsa_shape *shape, int64_t n_rows, int32_t nope_dim, int32_t v_dim,

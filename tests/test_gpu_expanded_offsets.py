@@ -1,9 +1,9 @@
-"""The expanded attention under offsets that break the batch's bounds."""
+"""The expanded attention under offsets that break the batch's bounds, and what it leaves alone."""
 import pytest
 import torch
 
 import deepseek_sparse_attention_gb300 as dsa
-from test_gpu_expanded import HEADS, SCALE, T, make_inputs
+from test_gpu_expanded import HEADS, SCALE, T, check, make_inputs
 
 pytestmark = pytest.mark.gpu
 FILL = 77.0
@@ -62,3 +62,23 @@ def test_one_broken_idle_sequence_among_many(n_seq, q_lens, dtype):
         bad = list(row_off)
         bad[s + 1] = 101                               # outside the cache
         assert _attend(bad, q_off, n_q, 100, dtype, n_q, 100)[3] == 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("row_off,q_off,served", [
+    ([0, 50, 5000], [0, 10, 20], [(0, 10, 0, 50)]),
+    ([0, 50, 40], [0, 10, 20], [(0, 10, 0, 50)]),
+    ([0, 5, 100], [0, 10, 20], [(10, 20, 5, 100)]),
+    ([0, 50, 100], [0, 10, 19], [(0, 10, 0, 50), (10, 19, 50, 100)]),
+    ([0, 50, 100], [4, 10, 20], [(4, 10, 0, 50), (10, 20, 50, 100)]),
+])
+def test_queries_that_are_skipped_keep_their_outputs(row_off, q_off, served, dtype):
+    """Those of refused sequences and of none: not written, split or not."""
+    x, out, lse, code, splits = _attend(row_off, q_off, 20, 100, dtype, 20, 100)
+    assert code == 2 and (splits > 1) == (dtype == "f32")
+    kept = torch.ones(20, dtype=torch.bool, device="cuda")
+    for q0, q1, r0, r1 in served:
+        kept[q0:q1] = False
+        q, k, cache, v = x
+        check([q1 - q0], [r1 - r0], q[q0:q1], k[r0:r1], cache[r0:r1], v[r0:r1], out[q0:q1], lse[q0:q1])
+    assert kept.any() and (out[kept] == FILL).all() and (lse[kept] == FILL).all()
