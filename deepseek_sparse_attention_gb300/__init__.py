@@ -458,10 +458,14 @@ def _rows_at(t, like, dtype, device: int, what: str):
     return t.data_ptr(), ld if rows > 1 else width
 
 
+# Types that an output of e4m3 codes may have; others of one byte would be read as other numbers.
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def dsa_rms_norm(x, weight, eps, out, add=None, total=None, scales=None, group=0,
                  stream=None) -> None:
     """Norm of the rows of ``x`` [rows, width], or of ``x + add`` (see dsa.h);
-    ``total`` gets the sum.  ``out`` has x's type, or one-byte elements (e4m3
+    ``total`` gets the sum.  ``out`` has x's type, or is float8_e4m3fn or uint8 (e4m3
     codes) with ``scales`` [rows, ceil(width / group)] float32 (group 0: [rows, 1])."""
     kind, d = _dtype(x, "x"), _device()
     like, dt = x.shape, x.dtype
@@ -471,13 +475,13 @@ def dsa_rms_norm(x, weight, eps, out, add=None, total=None, scales=None, group=0
     px, x_ld = _rows_at(x, like, dt, d, "x")
     pa, a_ld = (None, 0) if add is None else _rows_at(add, like, dt, d, "add")
     pt, t_ld = (None, 0) if total is None else _rows_at(total, like, dt, d, "total")
-    codes = out is not None and out.element_size() == 1
+    codes = out is not None and out.dtype in _CODES
     po, o_ld = _rows_at(out, like, out.dtype if codes else dt, d, "out")
     ps = None
     if codes:
         ps = _at(scales, torch.float32, d, rows * (-(-width // group) if group else 1), "scales")
     elif scales is not None:
-        raise ValueError("scales go with an out of one-byte elements")
+        raise ValueError("scales go with an out of float8_e4m3fn or uint8")
     _call("dsa_rms_norm", rows, width, kind, px, x_ld, pa, a_ld,
           None if weight is None else _at(weight, torch.float32, d, width, "weight"), eps, pt, t_ld, po,
           o_ld, NORM_E4M3 if codes else NORM_SAME, ps, group, _stream_at(stream, d))
