@@ -7,6 +7,7 @@
 
 #include "dsa.h"
 #include "dsa_kernels.cuh"
+#include "extents.h"
 
 namespace dsa {
 namespace {
@@ -610,14 +611,25 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
         !aligned(weight, 4) || !aligned(scales, 4))
         return DSA_ERR_INVALID_ARG;
     if (width > 16384 || n_rows >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
-    // an output in an input's place has its rows where they are, and its type
-    auto apart = [&](const void* o, int64_t ld, const void* in, int64_t in_ld, bool same_type) {
-        return o == nullptr || o != in || (same_type && (n_rows < 2 || ld == in_ld));
-    };
-    if (!apart(out, out_ld, x, x_ld, !e4m3) || !apart(out, out_ld, add, add_ld, !e4m3) ||
-        !apart(total, total_ld, x, x_ld, true) || !apart(total, total_ld, add, add_ld, true) ||
-        !apart(out, out_ld, total, total_ld, false))
-        return DSA_ERR_INVALID_ARG;
+    // an output in an input's place has its rows where they are, and its type; else they are apart
+    if (n_rows > 0) {
+        struct Tensor { const void* p; Rows rows; wide size; };
+        auto rows = [&](const void* p, wide ld, wide size) { return Tensor{p, make_rows(p, n_rows, ld * size, width * size), size}; };
+        const wide n_scales = (wide)n_rows * (group == 0 ? 1 : (width + group - 1) / group);
+        const Tensor in[] = {rows(x, x_ld, e), rows(add, add_ld, e), {weight, make_rows(weight, 1, 0, (wide)width * 4), 0}};
+        const Tensor to[] = {rows(out, out_ld, e4m3 ? 1 : e), rows(total, total_ld, e),
+                             {e4m3 ? scales : nullptr, make_rows(scales, 1, 0, n_scales * 4), 0}};
+        for (int i = 0; i < 3; ++i) {
+            if (to[i].p == nullptr) continue;
+            for (int j = 0; j < i; ++j)
+                if (to[j].p != nullptr && rows_meet(to[i].rows, to[j].rows)) return DSA_ERR_INVALID_ARG;
+            for (int j = 0; j < 3; ++j) {
+                if (in[j].p == nullptr || !rows_meet(to[i].rows, in[j].rows)) continue;
+                if (j == 2 || to[i].p != in[j].p || to[i].size != in[j].size || to[i].rows.stride != in[j].rows.stride)
+                    return DSA_ERR_INVALID_ARG;
+            }
+        }
+    }
     const NormArgs a{n_rows, x_ld, add_ld, total_ld, out_ld, x,     add, weight,
                      total,  out,  scales, width,    group,  eps,   (float)(1.0 / width)};
     return cuda_status(launch_rms_norm(a, dtype, e4m3, static_cast<cudaStream_t>(stream)), "rms_norm");
@@ -669,6 +681,13 @@ dsa_status dsa_rope(const dsa_rope_plan* plan, int32_t dtype, int64_t n_tok, int
     const uintptr_t e = dtype == DSA_BF16 ? 2 : 4;
     if (!aligned(x, e) || !aligned(out, e) || !aligned(pos, 8)) return DSA_ERR_INVALID_ARG;
     if (n_tok >= ((int64_t)1 << 31) || heads > 65536) return DSA_ERR_UNSUPPORTED;
+    if (n_tok > 0 && heads > 0) {
+        const wide size = (wide)e, d = plan->dims * size;
+        const Heads to = make_heads(out, out_tok * size, n_tok, out_head * size, heads, d);
+        if (x != out && heads_meet(make_heads(x, x_tok * size, n_tok, x_head * size, heads, d), to))
+            return DSA_ERR_INVALID_ARG;
+        if (rows_meet(to.rows(), make_rows(pos, 1, 0, (wide)n_tok * 8))) return DSA_ERR_INVALID_ARG;
+    }
     return cuda_status(launch_rope(*plan, dtype, n_tok, heads, x, x_tok, x_head, pos, out, out_tok,
                                    out_head, static_cast<cudaStream_t>(stream)),
                        "rope");

@@ -364,8 +364,9 @@ dsa_status dsa_sparse_mla_attn(const dsa_shape *shape, const dsa_batch *batch, c
  *          to nearest even, and stands for code * scale.  Both quotients are the
  *          rounded ones of float32; of scales below 2^-92 a code's is within 2^-22
  *          of itself.  Not read otherwise, and group = 0.
- * total, and out in dtype, may be x or add themselves (same stride; refused with
- * another); no other overlap.
+ * total, and out in dtype, may be x or add themselves (same stride).  Outputs that
+ * share any other element with a tensor of the call are refused; rows may lie
+ * among each other's (columns of one wider matrix, say).
  * Columns between a row's width and the next row are neither read nor written.
  * float32 arithmetic; sums of squares beyond float32's range are formed again of
  * scaled values, so that any finite h gives its norm.  A row with an infinity
@@ -408,7 +409,9 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
  *       t * x_tok + h * x_head elements behind it, its columns one after another
  *   pos [n_tok] int64, any values (negative ones turn back)
  *   out laid out by out_tok and out_head; x itself with x's strides, or apart
- *       from it.  Its heads must not overlap.  Only rotated columns are written.
+ *       from it and from pos: refused where they share an element, and where its
+ *       heads lie among x's of a token with other strides.  Its heads must not
+ *       overlap.  Only rotated columns are written.
  * float32 arithmetic; the angle is exact modulo one turn up to the rate's 53
  * bits.  n_tok < 2^31, heads <= 65536.  Pointers aligned to their elements; 16-byte
  * aligned ones with strides of 16 bytes' multiples move in 16-byte pieces.  No
