@@ -640,7 +640,7 @@ dsa_status dsa_rope_init(dsa_rope_plan* plan, int32_t dims, int32_t layout, int3
                          double beta_slow, double magnitude) {
     if (plan == nullptr || dims < 2 || (dims & 1) || (layout != DSA_ROPE_PAIRS && layout != DSA_ROPE_HALVES) ||
         (inverse != 0 && inverse != 1) || !isfinite(base) || !(base > 1.0) || !isfinite(factor) ||
-        !(factor >= 1.0) || !isfinite(magnitude))
+        !(factor >= 1.0) || !isfinite((float)magnitude))
         return DSA_ERR_INVALID_ARG;
     if (factor != 1.0 && !(beta_fast == 0.0 && beta_slow == 0.0) &&
         (!isfinite(original_len) || !(original_len > 0.0) || !isfinite(beta_fast) || !(beta_slow > 0.0) ||

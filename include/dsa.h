@@ -402,7 +402,8 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
  *   that make beta_fast (32) turns or more over the trained context stay as they
  *   are, those with beta_slow (1) or fewer are divided by the factor (high - low
  *   counts as 0.001 at least).  beta_fast = beta_slow = 0 divides every rate.
- *   magnitude multiplies the result (1, or the scaling's own correction).
+ *   magnitude multiplies the result (1, or the scaling's own correction); a
+ *   float32.
  *   dims even, 2 .. 256.
  * dsa_rope:
  *   x   first rotated column of the first head; token t's head h starts
