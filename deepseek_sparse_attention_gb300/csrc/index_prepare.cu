@@ -98,7 +98,7 @@ index_prepare_kernel(int64_t n, const float* __restrict__ x, const int64_t* __re
                     // fractional turns of pos * theta_i / 2 pi (the product wraps
                     // modulo 2^64 = whole turns), as a signed fraction in [-1/2, 1/2),
                     // to radians in [-pi, pi): there the hardware sine and cosine
-                    // are within 2^-21.4 absolute, far below the output's rounding
+                    // are within 2^-21.41 and 2^-21.19 absolute
                     const int t32 = (int)(unsigned int)((p * rate[i]) >> 32);
                     float sn, cs;
                     __sincosf((float)t32 * 1.4629180792671596e-09f, &sn, &cs);   // 2 pi / 2^32
