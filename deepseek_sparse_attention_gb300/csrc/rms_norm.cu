@@ -442,7 +442,8 @@ cudaError_t launch_rms_norm(const NormArgs& a, int32_t dtype, bool e4m3, cudaStr
                      (e4m3 ? fits(a.out, a.out_ld, 1, 8) : fits(a.out, a.out_ld, e, 16));
     const bool in = fits(a.x, a.x_ld, e, 16) && fits(a.add, a.add_ld, e, 16);
     // shifted for codes alone, whose scales want neighbours in a lane: 3,400 bf16 rows of 8,192
-    // columns, 8,195 apart, 48 us and one by one 87; to bf16 rows 52 and 47
+    // columns, 8,195 apart, 49 us and one by one 92 (with a residual 121 and 122); to bf16 rows
+    // 52 and 48
     const Access how = out && in ? Access::kVec : out && e4m3 ? Access::kShift : Access::kSingle;
     return dtype == DSA_BF16 ? launch<__nv_bfloat16>(a, e4m3, how, st) : launch<float>(a, e4m3, how, st);
 }

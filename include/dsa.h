@@ -413,8 +413,9 @@ dsa_status dsa_rms_norm(int64_t n_rows, int32_t width, int32_t dtype, const void
  *       from it and from pos: refused where they share an element, and where its
  *       heads lie among x's of a token with other strides.  Its heads must not
  *       overlap.  Only rotated columns are written.
- * float32 arithmetic; the angle is exact modulo one turn up to the rate's 53
- * bits.  n_tok < 2^31, heads <= 65536.  Pointers aligned to their elements; 16-byte
+ * float32 arithmetic; the angle is the plan's fraction of a turn times pos, exact
+ * modulo one turn before its rounding (a fraction is within 2^-49 of itself and
+ * 2^-65 of a turn).  n_tok < 2^31, heads <= 65536.  Pointers aligned to their elements; 16-byte
  * aligned ones with strides of 16 bytes' multiples move in 16-byte pieces.  No
  * workspace. */
 typedef enum {
@@ -470,7 +471,8 @@ dsa_status dsa_rope(const dsa_rope_plan *plan, int32_t dtype, int64_t n_tok, int
  * A logit of NaN or +inf, or attended logits of -inf alone, give NaN.
  * float32 logits, maxima, sums and accumulation; bf16 operands give each
  * weight exp(z_j - m) to the value product rounded to bf16 (2^-8 of itself at most), the
- * weights' sum is of the unrounded ones.  n_q <= 2^24, n_seq <= 2^20, total_rows <
+ * weights' sum is of the unrounded ones (dsa_sparse_mla_attn with DSA_FLAG_DENSE carries
+ * them as two bf16 parts, and gives float32).  n_q <= 2^24, n_seq <= 2^20, total_rows <
  * 2^31.  A sequence whose offsets break the host bounds, idle or not, is skipped and
  * sets the error word (code 2); where q_off falls, sequences behind the fall may be
  * skipped with it.  Outputs of skipped queries, and of those that no sequence has, are
