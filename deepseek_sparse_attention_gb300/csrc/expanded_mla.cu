@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(256, 2) expanded_simt(const ExpandedArgs a) {
         else if (RPW > 2 && t.n_q <= 16) simt_tile<2, VD>(a, t, h, split, smem);
         else simt_tile<RPW, VD>(a, t, h, split, smem);
     }
-    expanded_check(a.b, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x, a.err, 60);
+    // a thread to a sequence, in as many CTAs as that takes
+    if (blockIdx.x <= (uint32_t)a.b.n_seq / 256)
+        expanded_check(a.b, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256, a.err, 60);
 }
 
 // One warp per (query, head): the splits' sums weighted by their maxima.  A CTA has eight queries of a

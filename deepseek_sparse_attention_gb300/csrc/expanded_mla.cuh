@@ -43,10 +43,12 @@ __host__ __device__ inline int64_t expanded_start(const BatchDev& b, int32_t s, 
 }
 
 // Whether sequence s lies within the bounds that the host gave, and whether the batch's ends do.
-__host__ __device__ inline bool expanded_sound(const BatchDev& b, int32_t s) {
-    const int64_t q0 = b.q_off[s], q1 = b.q_off[s + 1], r0 = b.row_off[s], r1 = b.row_off[s + 1];
+__host__ __device__ inline bool expanded_within(const BatchDev& b, int64_t q0, int64_t q1, int64_t r0, int64_t r1) {
     return q0 >= 0 && q1 >= q0 && q1 <= b.n_q && q1 - q0 <= b.max_q_len && r0 >= 0 && r1 >= r0 && r1 <= b.total_rows &&
            r1 - r0 <= b.max_kv_len && q1 - q0 <= r1 - r0;
+}
+__host__ __device__ inline bool expanded_sound(const BatchDev& b, int32_t s) {
+    return expanded_within(b, b.q_off[s], b.q_off[s + 1], b.row_off[s], b.row_off[s + 1]);
 }
 __host__ __device__ inline bool expanded_ends_sound(const BatchDev& b) {
     return b.q_off[0] == 0 && b.q_off[b.n_seq] == b.n_q;
@@ -67,8 +69,9 @@ __host__ __device__ inline bool expanded_tile(const BatchDev& b, int64_t slot, i
         const int32_t mid = lo + (hi - lo + 1) / 2;
         if (expanded_start(b, mid, bq) <= slot) lo = mid; else hi = mid - 1;
     }
-    if (!expanded_sound(b, lo)) return false;
-    const int64_t q0 = b.q_off[lo], q_len = b.q_off[lo + 1] - q0, r0 = b.row_off[lo], kv_len = b.row_off[lo + 1] - r0;
+    const int64_t q0 = b.q_off[lo], q1 = b.q_off[lo + 1], r0 = b.row_off[lo], r1 = b.row_off[lo + 1];
+    if (!expanded_within(b, q0, q1, r0, r1)) return false;
+    const int64_t q_len = q1 - q0, kv_len = r1 - r0;
     const int64_t at = slot - (q0 / bq + (lo < q0 ? lo : q0));
     if (at < 0 || at * bq >= q_len) return false;
     t.q0 = q0 + at * bq;
